@@ -87,7 +87,9 @@ typedef enum {
   LORA_E_HIP = -8         /* a HIP runtime call failed */
 } lora_status;
 
-typedef enum { LORA_F32 = 0, LORA_BF16 = 1 } lora_dtype;
+/* LORA_E4M3 (8 bits, four of them exponent, largest value 448) is a type of the
+ * decoder-block operators' operands only; adapter pools are fp32 or bf16. */
+typedef enum { LORA_F32 = 0, LORA_BF16 = 1, LORA_E4M3 = 2 } lora_dtype;
 
 /* Geometry of one adapter pool (one projection, possibly fused slices). */
 typedef struct {
@@ -498,6 +500,111 @@ int32_t lora_apply_ranked(const lora_pool_desc* desc, const void* A_pool, const 
                           const uint8_t* prefill_host, int32_t bgmv_max_rank,
                           const int32_t* slot_ranks, void* ws, int64_t ws_bytes,
                           void* meta_host, int64_t meta_host_bytes, void* stream);
+
+/* ------------------------------------------------ decoder-block operators */
+/* The base model's half of the layer that the adapters' delta joins: norm,
+ * projection, gated feed-forward block and that block's gradients.  All
+ * matrices are device memory, row-major and contiguous; every pointer is
+ * 16-byte aligned; calls are asynchronous on `stream`, allocate nothing, and
+ * can be captured in a graph.  T = 0 is a no-op (except that a gradient of the
+ * weights over no tokens is zero).  Sums and statistics are kept in fp32 or
+ * wider and every output is rounded once (nearest, ties to even).  The result
+ * of a call does not depend on timing: no atomics, fixed orders.
+ *
+ * A call's workspace size depends on the descriptor and T alone; 0 means that
+ * ws may be NULL.  Its contents need no preparation and mean nothing after
+ * the call. */
+
+typedef enum {
+  LORA_ACT_NONE = 0,       /* z */
+  LORA_ACT_SILU = 1,       /* z / (1 + e^-z) */
+  LORA_ACT_GELU = 2,       /* z Phi(z), Phi the normal distribution's cumulative function */
+  LORA_ACT_GELU_TANH = 3,  /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+  LORA_ACT_RELU = 4        /* max(z, 0); NaN stays NaN */
+} lora_act;
+
+typedef struct {
+  int32_t dtype;   /* LORA_F32 or LORA_BF16: x, residual, weight, sum, out */
+  int32_t hidden;  /* H: a multiple of 8, at most 32768 */
+  float eps;
+  int32_t reserved; /* 0 */
+} lora_norm_desc;
+
+typedef struct {
+  int32_t dtype;         /* x and w: LORA_F32, LORA_BF16 or LORA_E4M3 */
+  int32_t out_dtype;     /* bias, delta, residual, out: LORA_F32 or LORA_BF16
+                            (LORA_F32 when dtype is) */
+  int32_t in_features;   /* K: a multiple of 8 (16 for LORA_E4M3), at most 2^20 */
+  int32_t out_features;  /* O: any, at most 2^20 */
+  int32_t act;           /* lora_act */
+  int32_t reserved;      /* 0 */
+} lora_linear_desc;
+
+typedef struct {
+  int32_t dtype;           /* x and w: LORA_F32, LORA_BF16 or LORA_E4M3 */
+  int32_t out_dtype;       /* delta, pre, out: as in lora_linear_desc */
+  int32_t in_features;     /* K: a multiple of 8 (16 for LORA_E4M3), at most 2^20 */
+  int32_t inter_features;  /* I: likewise */
+  int32_t act;             /* lora_act of the gate */
+  int32_t reserved;        /* 0 */
+} lora_gated_desc;
+
+/* Root-mean-square norm with the residual's addition, and an output in 8 bits:
+ *   t = round_dtype(x + residual)          (t = x without a residual)
+ *   n = t * (mean_H(t^2) + eps)^(-1/2) * weight
+ *   sum = t;  out = round_dtype(n)
+ *   scale[t] = max(max_H |n| / 448, 2^-126);  out8 = e4m3(n / scale[t])
+ *   x, residual, sum, out [T][H], weight [H], out8 [T][H] e4m3, scale [T] fp32
+ * residual and sum are given together or both NULL; out8 and scale likewise;
+ * out may be NULL where out8 is given.  sum and out may be x or residual
+ * themselves (in place); other overlaps are not allowed.  A row that holds a
+ * NaN or an infinity has a NaN scale. */
+int32_t lora_add_rms_norm(const lora_norm_desc* desc, const void* x, const void* residual,
+                          const void* weight, void* sum, void* out, void* out8, float* scale,
+                          int32_t T, void* stream);
+
+/* A base projection with its epilogue:
+ *   out[t][o] = act(x_scale[t] w_scale[o] sum_k x[t][k] w[o][k] + bias[o] + delta[t][o])
+ *               + residual[t][o]
+ *   x [T][K], w [O][K] (a projection's weight as it is stored), x_scale [T]
+ *   and w_scale [O] fp32 (for e4m3 operands, else NULL), bias [O], delta and
+ *   residual [T][O] (each may be NULL), out [T][O]
+ * `delta` is an adapters' delta: lora_apply onto zeros, or onto anything that
+ * is to be added before the activation.  out may be delta or residual itself. */
+int64_t lora_linear_workspace_bytes(const lora_linear_desc* desc, int32_t T);
+int32_t lora_linear(const lora_linear_desc* desc, const void* x, const void* w,
+                    const float* x_scale, const float* w_scale, const void* bias,
+                    const void* delta, const void* residual, void* out, int32_t T, void* ws,
+                    int64_t ws_bytes, void* stream);
+
+/* The gated feed-forward block's first half, both projections, activation and
+ * product in one:
+ *   pre[t][j] = x_scale[t] w_scale[j] sum_k x[t][k] w[j][k] + delta[t][j],  j < 2 I
+ *   out[t][i] = act(pre[t][i]) * pre[t][I + i]
+ *   x [T][K], w [2 I][K] (gate rows, then up rows), x_scale [T] and w_scale
+ *   [2 I] fp32 (for e4m3 operands, else NULL), delta [T][2 I] or NULL, pre
+ *   [T][2 I] or NULL (training keeps it; rounded; out is made from the
+ *   unrounded values), out [T][I]
+ * pre may be delta itself. */
+int64_t lora_gated_ffn_workspace_bytes(const lora_gated_desc* desc, int32_t T);
+int32_t lora_gated_ffn(const lora_gated_desc* desc, const void* x, const void* w,
+                       const float* x_scale, const float* w_scale, const void* delta, void* pre,
+                       void* out, int32_t T, void* ws, int64_t ws_bytes, void* stream);
+
+/* Its gradients, from dout [T][I] and the pre [T][2 I] that lora_gated_ffn
+ * kept (fp32 or bf16 operands; every array has the descriptor's dtype):
+ *   dpre[t][i]     = dout[t][i] * pre[t][I + i] * act'(pre[t][i])
+ *   dpre[t][I + i] = dout[t][i] * act(pre[t][i])      (also the delta's gradient)
+ *   dx[t][k] = sum_j dpre[t][j] w[j][k],   dw[j][k] = sum_t dpre[t][j] x[t][k]
+ * dx [T][K] may be NULL (w is then not read and may be NULL), dw [2 I][K] may
+ * be NULL (likewise x); dpre is always written and may be pre itself.  The
+ * products take dpre as it is stored, rounded to the dtype.  dw is
+ * overwritten, not accumulated; for T = 0 it is zero. */
+int64_t lora_gated_ffn_backward_workspace_bytes(const lora_gated_desc* desc, int32_t T,
+                                                int32_t need_dx, int32_t need_dw);
+int32_t lora_gated_ffn_backward(const lora_gated_desc* desc, const void* dout, const void* pre,
+                                const void* x, const void* w, void* dpre, void* dx, void* dw,
+                                int32_t T, void* ws, int64_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

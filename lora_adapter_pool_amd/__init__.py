@@ -13,5 +13,8 @@ from ._lib import (  # noqa: F401
     lora_build_meta_device,
     lora_pool_bytes_A, lora_pool_bytes_B, lora_pool_clear, lora_pool_load, lora_pool_validate,
     lora_scaling, lora_sgmv_expand, lora_sgmv_shrink, last_error,
+    LORA_E4M3, make_norm_desc, make_linear_desc, make_gated_desc, lora_add_rms_norm,
+    lora_linear, lora_linear_workspace_bytes, lora_gated_ffn, lora_gated_ffn_workspace_bytes,
+    lora_gated_ffn_backward, lora_gated_ffn_backward_workspace_bytes,
 )
 from .pool import LoraPool  # noqa: F401

@@ -33,6 +33,8 @@ STATUS_NAMES = {0: "LORA_OK", -1: "LORA_E_ARG", -2: "LORA_E_DTYPE", -3: "LORA_E_
 
 LORA_F32 = 0
 LORA_BF16 = 1
+LORA_E4M3 = 2
+ACTS = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3, "relu": 4}
 LORA_MAX_SLICES = 8
 LORA_BGMV_MAX_RANK_DEFAULT = 64
 
@@ -48,6 +50,23 @@ class lora_pool_desc(ctypes.Structure):
                 ("max_lora_rank", ctypes.c_int32), ("in_features", ctypes.c_int32),
                 ("num_slices", ctypes.c_int32),
                 ("out_features", ctypes.c_int32 * LORA_MAX_SLICES)]
+
+
+class lora_norm_desc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("hidden", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
+class lora_linear_desc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class lora_gated_desc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("in_features", ctypes.c_int32), ("inter_features", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class lora_meta(ctypes.Structure):
@@ -84,6 +103,9 @@ _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _DP = ctypes.POINTER(lora_pool_desc)
+_NP = ctypes.POINTER(lora_norm_desc)
+_LP = ctypes.POINTER(lora_linear_desc)
+_GP = ctypes.POINTER(lora_gated_desc)
 
 _SIGNATURES = {
     "lora_last_error": (ctypes.c_char_p, []),
@@ -120,6 +142,13 @@ _SIGNATURES = {
     "lora_merge_weights": (_I32, [_DP, _P, _P, _I32, _I32, _P, _P, _P]),
     "lora_apply_ranked": (_I32, [_DP, _P, _P, _P, _P, _I32, _P, _P, _I32, _P, _P, _I64, _P, _I64,
                                  _P]),
+    "lora_add_rms_norm": (_I32, [_NP, _P, _P, _P, _P, _P, _P, _P, _I32, _P]),
+    "lora_linear_workspace_bytes": (_I64, [_LP, _I32]),
+    "lora_linear": (_I32, [_LP, _P, _P, _P, _P, _P, _P, _P, _P, _I32, _P, _I64, _P]),
+    "lora_gated_ffn_workspace_bytes": (_I64, [_GP, _I32]),
+    "lora_gated_ffn": (_I32, [_GP, _P, _P, _P, _P, _P, _P, _P, _I32, _P, _I64, _P]),
+    "lora_gated_ffn_backward_workspace_bytes": (_I64, [_GP, _I32, _I32, _I32]),
+    "lora_gated_ffn_backward": (_I32, [_GP, _P, _P, _P, _P, _P, _P, _P, _I32, _P, _I64, _P]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -158,7 +187,7 @@ _pycall = None
 
 def pycall():
     """The CPython binding of the per-call entry points (module _lora_call:
-    apply, apply_ranked, apply_device), built beside the library; raise if it
+    apply, apply_ranked, apply_device and the decoder-block operators), built beside the library; raise if it
     was not built.  Each function takes the entry point's address (see
     entry_address) and then that entry point's arguments as Python ints."""
     global _pycall
@@ -466,3 +495,73 @@ def lora_apply_device_ranked(desc, A_pool, B_pool, x, y, T, ids, prefill, bgmv_m
                                           _ptr(x), _ptr(y), int(T), _ptr(ids), _ptr(prefill),
                                           int(bgmv_max_rank), _ptr(slot_ranks), _ptr(ws),
                                           int(ws_bytes), _stream(stream)))
+
+
+# ---------------------------------------------------- decoder-block operators
+
+_DTYPE_CODES = {"f32": LORA_F32, "fp32": LORA_F32, "float32": LORA_F32,
+                "bf16": LORA_BF16, "bfloat16": LORA_BF16,
+                "e4m3": LORA_E4M3, "float8_e4m3fn": LORA_E4M3}
+
+
+def make_norm_desc(dtype: str, hidden: int, eps: float) -> lora_norm_desc:
+    """Descriptor of lora_add_rms_norm (keep it: it is read at every call)."""
+    return lora_norm_desc(_DTYPE_CODES[dtype], int(hidden), float(eps), 0)
+
+
+def make_linear_desc(dtype: str, out_dtype: str, in_features: int, out_features: int,
+                     act: str = "none") -> lora_linear_desc:
+    return lora_linear_desc(_DTYPE_CODES[dtype], _DTYPE_CODES[out_dtype], int(in_features),
+                            int(out_features), ACTS[act], 0)
+
+
+def make_gated_desc(dtype: str, out_dtype: str, in_features: int, inter_features: int,
+                    act: str = "silu") -> lora_gated_desc:
+    return lora_gated_desc(_DTYPE_CODES[dtype], _DTYPE_CODES[out_dtype], int(in_features),
+                           int(inter_features), ACTS[act], 0)
+
+
+def lora_add_rms_norm(desc, x, residual, weight, sum, out, out8, scale, T, stream=None) -> None:
+    """sum = x + residual; out = rms_norm(sum) * weight; out8 / scale the same in e4m3."""
+    _check(pycall().add_rms_norm(entry_address("lora_add_rms_norm"), ctypes.addressof(desc),
+                                 _ptr(x), _ptr(residual), _ptr(weight), _ptr(sum), _ptr(out),
+                                 _ptr(out8), _ptr(scale), int(T), _stream(stream)))
+
+
+def lora_linear_workspace_bytes(desc, T: int) -> int:
+    return _check(lib().lora_linear_workspace_bytes(ctypes.byref(desc), int(T)))
+
+
+def lora_linear(desc, x, w, x_scale, w_scale, bias, delta, residual, out, T, ws, ws_bytes,
+                stream=None) -> None:
+    """out = act(x_scale w_scale x W^T + bias + delta) + residual."""
+    _check(pycall().linear(entry_address("lora_linear"), ctypes.addressof(desc), _ptr(x), _ptr(w),
+                           _ptr(x_scale), _ptr(w_scale), _ptr(bias), _ptr(delta), _ptr(residual),
+                           _ptr(out), int(T), _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def lora_gated_ffn_workspace_bytes(desc, T: int) -> int:
+    return _check(lib().lora_gated_ffn_workspace_bytes(ctypes.byref(desc), int(T)))
+
+
+def lora_gated_ffn(desc, x, w, x_scale, w_scale, delta, pre, out, T, ws, ws_bytes,
+                   stream=None) -> None:
+    """pre = x_scale w_scale x W^T + delta; out = act(gate half of pre) * (up half)."""
+    _check(pycall().gated_ffn(entry_address("lora_gated_ffn"), ctypes.addressof(desc), _ptr(x),
+                              _ptr(w), _ptr(x_scale), _ptr(w_scale), _ptr(delta), _ptr(pre),
+                              _ptr(out), int(T), _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def lora_gated_ffn_backward_workspace_bytes(desc, T: int, need_dx: bool = True,
+                                            need_dw: bool = True) -> int:
+    return _check(lib().lora_gated_ffn_backward_workspace_bytes(
+        ctypes.byref(desc), int(T), int(bool(need_dx)), int(bool(need_dw))))
+
+
+def lora_gated_ffn_backward(desc, dout, pre, x, w, dpre, dx, dw, T, ws, ws_bytes,
+                            stream=None) -> None:
+    """Gradients of lora_gated_ffn from the pre it kept (dx and dw may be None)."""
+    _check(pycall().gated_ffn_backward(entry_address("lora_gated_ffn_backward"),
+                                       ctypes.addressof(desc), _ptr(dout), _ptr(pre), _ptr(x),
+                                       _ptr(w), _ptr(dpre), _ptr(dx), _ptr(dw), int(T), _ptr(ws),
+                                       int(ws_bytes), _stream(stream)))

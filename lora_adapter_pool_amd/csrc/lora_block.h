@@ -1,0 +1,267 @@
+// Shared declarations of the decoder-block operators (norm, linear, gated
+// feed-forward and its gradients): argument structs of the launchers and the
+// device helpers that their epilogues share.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "lora_internal.h"
+
+namespace lora {
+
+// One product z[m][n] = sum_k A[m][k] B[n][k] and what its epilogue does.
+// A and B are row-major with the reduction contiguous; `kb` is the length of a
+// row in bytes (a multiple of 16) and also its stride.
+//   linear: out[m][n] = act(sa[m] sb[n] z + bias[n] + delta[m][n]) + residual[m][n]
+//   gated:  B has 2 n rows (gate rows, then up rows); pre = sa sb z + delta,
+//           out[m][n] = act(pre[m][n]) * pre[m][n + N]
+struct GemmArgs {
+  const char* A;
+  const char* B;
+  const float* sa;        // one scale a row of A, or nullptr
+  const float* sb;        // one scale a row of B, or nullptr
+  const void* bias;       // [N], or nullptr
+  const void* delta;      // [M][N] ([M][2 N] gated), or nullptr
+  const void* residual;   // [M][N], or nullptr
+  void* pre;              // gated: [M][2 N], or nullptr
+  void* out;              // [M][N]
+  float* part;            // split K: [splits][M][ldp] raw products, or nullptr
+  int64_t kb;
+  int32_t M, N;
+  int32_t ldp;            // floats a row of `part`
+  int32_t splits;
+  int32_t out_dtype;      // of bias, delta, residual, pre and out
+  int32_t act;
+  int32_t tiles_m, tiles_n;
+};
+
+// Reduction bytes that a tile step takes: 128 (64 bf16, 128 e4m3, 32 fp32),
+// one whole cache line of every row.
+constexpr int kStepBytes = 128;
+
+// Launch plan of a product: tile shape and K split, from sizes and types alone.
+struct GemmPlan {
+  int32_t shape;   // index of a tile shape
+  int32_t splits;
+  int64_t ws_bytes;  // fp32 partials
+};
+GemmPlan gemm_plan(int32_t dtype, bool gated, int64_t M, int64_t N, int64_t kb);
+int32_t gemm_run(int32_t dtype, bool gated, const GemmPlan& plan, GemmArgs a, void* ws,
+                 hipStream_t st);
+// per type (each in its own source file)
+int32_t gemm_launch_bf16(bool gated, int shape, const GemmArgs& a, hipStream_t st);
+int32_t gemm_launch_e4m3(bool gated, int shape, const GemmArgs& a, hipStream_t st);
+int32_t gemm_launch_f32(bool gated, int shape, const GemmArgs& a, hipStream_t st);
+
+struct TileShape {
+  int bm, bn;  // rows of A and rows of B a workgroup covers
+};
+// shapes of gemm_ring_kernel, smallest first
+constexpr TileShape kShapes[] = {{64, 64}, {128, 128}};
+
+int32_t check_launch(const char* what);
+
+#ifdef __HIPCC__
+
+typedef uint32_t bk_u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t bk_u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef float bk_f32x4 __attribute__((ext_vector_type(4)));
+typedef float bk_f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef float bk_f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bk_bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bk_bf16x8 __attribute__((ext_vector_type(8)));
+typedef int bk_i32x8 __attribute__((ext_vector_type(8)));
+
+// two fp32 -> packed bf16, nearest, ties to even
+__device__ __forceinline__ uint32_t bk_pack(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(bk_f32x2{lo, hi}, bk_bf16x2));
+}
+__device__ __forceinline__ float bk_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bk_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// e^z.  The hardware's exponential is base 2; the product z log2(e) is kept
+// with the part that its rounding loses, or the result's relative error would
+// grow with |z| (2^-24 |z| log2 e).
+__device__ __forceinline__ float bk_exp(float z) {
+  constexpr float kL = 1.44269504088896341f, kLlo = 1.92596299e-8f;
+  const float p = z * kL;
+  const float r = __builtin_fmaf(z, kLlo, __builtin_fmaf(z, kL, -p));
+  const float e = __builtin_amdgcn_exp2f(p);
+  // past the range p is infinite and r no number: e alone is right there
+  return __builtin_fabsf(p) < 160.f ? __builtin_fmaf(e, r * 0.693147180559945309f, e) : e;
+}
+// 1 / (1 + e^-z)
+__device__ __forceinline__ float bk_logistic(float z) {
+  return __builtin_amdgcn_rcpf(1.f + bk_exp(-z));
+}
+constexpr float kGeluC = 0.797884560802865356f;  // sqrt(2 / pi)
+constexpr float kGeluA = 0.044715f;
+// the normal distribution's cumulative function; through erfc, which keeps
+// its relative accuracy for negative z
+__device__ __forceinline__ float bk_phi(float z) {
+  return 0.5f * erfcf(-0.707106781186547524f * z);
+}
+// gelu in its tanh form: 0.5 (1 + tanh u) = logistic(2 u)
+__device__ __forceinline__ float bk_tanh_gate(float z) {
+  return bk_logistic(2.f * kGeluC * __builtin_fmaf(kGeluA * z * z, z, z));
+}
+
+// Applies an activation to eight values.  z * 0 of an infinite z far below
+// zero is no number, so the products with a vanishing factor are taken as 0.
+template <int NV>
+__device__ __forceinline__ void act_apply(int act, float (&z)[NV]) {
+  if (act == LORA_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) z[i] = z[i] == -__builtin_inff() ? 0.f : z[i] * bk_logistic(z[i]);
+  } else if (act == LORA_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) z[i] = z[i] == -__builtin_inff() ? 0.f : z[i] * bk_phi(z[i]);
+  } else if (act == LORA_ACT_GELU_TANH) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) z[i] = z[i] == -__builtin_inff() ? 0.f : z[i] * bk_tanh_gate(z[i]);
+  } else if (act == LORA_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) z[i] = z[i] < 0.f ? 0.f : z[i];  // keeps NaN
+  }
+}
+
+// An activation's value and derivative.
+__device__ __forceinline__ void act_curve(int act, float z, float& value, float& slope) {
+  value = z;
+  slope = 1.f;
+  if (act == LORA_ACT_SILU) {
+    const float p = bk_logistic(z);
+    value = z * p;
+    slope = p * __builtin_fmaf(z, 1.f - p, 1.f);
+  } else if (act == LORA_ACT_GELU) {
+    const float p = bk_phi(z);
+    value = z * p;
+    slope = __builtin_fmaf(z * 0.398942280401432678f, bk_exp(-0.5f * z * z), p);
+  } else if (act == LORA_ACT_GELU_TANH) {
+    const float p = bk_tanh_gate(z);
+    value = z * p;
+    slope = __builtin_fmaf(value * (1.f - p),
+                           2.f * kGeluC * __builtin_fmaf(3.f * kGeluA * z, z, 1.f), p);
+  } else if (act == LORA_ACT_RELU) {
+    value = z < 0.f ? 0.f : z;
+    slope = z > 0.f ? 1.f : 0.f;
+  }
+}
+
+// Eight consecutive elements of a row of bf16 or fp32 at element `i`, as far
+// as `left` (>= 1) goes; rows of odd length start at any element, and global
+// memory takes 16-byte accesses at any element's alignment.
+__device__ __forceinline__ void load8(const void* base, int64_t i, int left, int dtype,
+                                      float (&v)[8]) {
+  if (dtype == LORA_BF16) {
+    const uint16_t* p = (const uint16_t*)base + i;
+    if (left >= 8) {
+      const bk_u32x4 w = *reinterpret_cast<const bk_u32x4_a2*>(p);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[2 * j] = bk_lo(w[j]), v[2 * j + 1] = bk_hi(w[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = j < left ? __uint_as_float((uint32_t)p[j] << 16) : 0.f;
+    }
+  } else {
+    const float* p = (const float*)base + i;
+    if (left >= 8) {
+      const bk_f32x4 a = *reinterpret_cast<const bk_f32x4_a4*>(p);
+      const bk_f32x4 b = *reinterpret_cast<const bk_f32x4_a4*>(p + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = j < left ? p[j] : 0.f;
+    }
+  }
+}
+__device__ __forceinline__ void store8(void* base, int64_t i, int left, int dtype,
+                                       const float (&v)[8]) {
+  if (dtype == LORA_BF16) {
+    uint16_t* p = (uint16_t*)base + i;
+    bk_u32x4 w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = bk_pack(v[2 * j], v[2 * j + 1]);
+    if (left >= 8) {
+      *reinterpret_cast<bk_u32x4_a2*>(p) = w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < left) p[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+    }
+  } else {
+    float* p = (float*)base + i;
+    if (left >= 8) {
+      *reinterpret_cast<bk_f32x4_a4*>(p) = bk_f32x4{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<bk_f32x4_a4*>(p + 4) = bk_f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < left) p[j] = v[j];
+    }
+  }
+}
+
+// The epilogue on eight raw products of row m, columns n .. n + 8 (n < N).
+template <bool kGated>
+__device__ __forceinline__ void epilogue8(const GemmArgs& p, int m, int n, float (&z)[8],
+                                          float (&u)[8]) {
+  const int left = p.N - n;
+  float t[8];
+  if (p.sa) {
+    const float s = p.sa[m];
+    load8(p.sb, n, left, LORA_F32, t);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[j] = z[j] * s * t[j];
+    if constexpr (kGated) {
+      load8(p.sb, (int64_t)p.N + n, left, LORA_F32, t);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] = u[j] * s * t[j];
+    }
+  }
+  if constexpr (kGated) {
+    const int64_t at = (int64_t)m * 2 * p.N + n;
+    if (p.delta) {
+      load8(p.delta, at, left, p.out_dtype, t);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[j] += t[j];
+      load8(p.delta, at + p.N, left, p.out_dtype, t);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] += t[j];
+    }
+    if (p.pre) {
+      store8(p.pre, at, left, p.out_dtype, z);
+      store8(p.pre, at + p.N, left, p.out_dtype, u);
+    }
+    act_apply(p.act, z);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[j] *= u[j];
+    store8(p.out, (int64_t)m * p.N + n, left, p.out_dtype, z);
+  } else {
+    const int64_t at = (int64_t)m * p.N + n;
+    if (p.bias) {
+      load8(p.bias, n, left, p.out_dtype, t);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[j] += t[j];
+    }
+    if (p.delta) {
+      load8(p.delta, at, left, p.out_dtype, t);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[j] += t[j];
+    }
+    act_apply(p.act, z);
+    if (p.residual) {
+      load8(p.residual, at, left, p.out_dtype, t);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[j] += t[j];
+    }
+    store8(p.out, at, left, p.out_dtype, z);
+  }
+}
+
+#endif  // __HIPCC__
+
+}  // namespace lora

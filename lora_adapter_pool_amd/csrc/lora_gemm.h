@@ -1,0 +1,303 @@
+// The matrix product of the decoder-block operators, for one operand type.
+//
+//   z[m][n] = sum_k A[m][k] B[n][k],  both row-major, reduction contiguous
+//
+// Everything but the matrix instruction itself is written in bytes: a tile
+// step takes 128 bytes of every row (64 bf16, 128 e4m3 or 32 fp32 values), a
+// lane reads 16-byte chunks, and lane group g = lane / 16 takes chunks g and
+// 4 + g of its row.  Which reduction index a chunk holds does not matter as
+// long as both operands agree, so one layout serves all three types:
+//   bf16  two v_mfma_f32_16x16x32 a pair of chunks
+//   e4m3  one v_mfma_f32_16x16x128_f8f6f4 (unit block scales), or, where the
+//         sums have to be exact to fp32, conversion to bf16 (exact) and four
+//         bf16 instructions: the 8-bit instructions of gfx950 add neighbouring
+//         products on a grid of 2^-11 of the larger one before the fp32 sum
+//         (measured: two terms alone are off by up to 2^-10.8 of the larger,
+//         terms in different lanes by 2^-23.7), less than bf16 outputs keep
+//         and more than fp32 outputs do
+//   fp32  eight v_mfma_f32_16x16x4, one a word
+// B is the instruction's first operand, so a lane ends with four consecutive
+// columns n of one row m.
+//
+// LDS rows are 128 bytes and chunk c of row r sits at position c ^ (r / 2 % 8):
+// 16 lanes that read one chunk of 16 consecutive rows then cover all 64 banks.
+// Direct global -> LDS loads write 1 KB runs (8 rows) in lane order, so the
+// permutation is made by the lane's choice of its global chunk.
+//
+// Rows past the end are clamped to the last row (their results are never
+// stored).  A last step that is partly past the row's end loads chunk 0 there
+// instead and both operands' chunks are zeroed after the LDS read.
+#pragma once
+
+#include "lora_block.h"
+
+namespace lora {
+namespace gemm {
+
+constexpr int kE4m3Exact = 3;  // a fourth operand type: e4m3 with fp32 sums
+
+// eight e4m3 values (two words) as bf16
+__device__ __forceinline__ bk_bf16x8 widen(uint32_t lo, uint32_t hi) {
+  const bk_bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)lo, 1.f, false);
+  const bk_bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)lo, 1.f, true);
+  const bk_bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)hi, 1.f, false);
+  const bk_bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)hi, 1.f, true);
+  return bk_bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+template <int DT>
+__device__ __forceinline__ bk_f32x4 mma(const bk_u32x4 (&a)[2], const bk_u32x4 (&b)[2],
+                                        bk_f32x4 c) {
+  if constexpr (DT == LORA_BF16) {
+    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bk_bf16x8, a[0]),
+                                                __builtin_bit_cast(bk_bf16x8, b[0]), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+        __builtin_bit_cast(bk_bf16x8, a[1]), __builtin_bit_cast(bk_bf16x8, b[1]), c, 0, 0, 0);
+  } else if constexpr (DT == LORA_E4M3) {
+    const bk_i32x8 x = {(int)a[0][0], (int)a[0][1], (int)a[0][2], (int)a[0][3],
+                        (int)a[1][0], (int)a[1][1], (int)a[1][2], (int)a[1][3]};
+    const bk_i32x8 y = {(int)b[0][0], (int)b[0][1], (int)b[0][2], (int)b[0][3],
+                        (int)b[1][0], (int)b[1][1], (int)b[1][2], (int)b[1][3]};
+    // block scales are powers of two with a bias of 127: 0x7f is 1
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 0, 0, 0, 0x7f7f7f7f, 0,
+                                                            0x7f7f7f7f);
+  } else if constexpr (DT == kE4m3Exact) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int h = 0; h < 4; h += 2)
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(a[s][h], a[s][h + 1]),
+                                                    widen(b[s][h], b[s][h + 1]), c, 0, 0, 0);
+    return c;
+  } else {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[s][j]),
+                                                 __uint_as_float(b[s][j]), c, 0, 0, 0);
+    return c;
+  }
+}
+
+// s_waitcnt operand (gfx9 encoding): at most n vector memory operations
+// outstanding, LDS operations not waited for
+__host__ __device__ constexpr int wait_vm(int n) {
+  return (n & 15) | ((n >> 4) << 14) | 0x0F70;
+}
+
+__device__ __forceinline__ void barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Workgroup id -> tile.  Workgroups are dealt round-robin to the 8 XCDs, each
+// with an L2 of its own: XCD x takes the x-th contiguous eighth of the tiles.
+// Within it tiles go in groups of 8 row tiles, columns outside, so that the
+// workgroups that run together share rows of A and of B.
+__device__ __forceinline__ void tile_of(const GemmArgs& p, int b, int& tm, int& tn, int& sp) {
+  const int total = p.tiles_m * p.tiles_n * p.splits;
+  const int q = total >> 3, r = total & 7, x = b & 7;
+  int id = x * q + (x < r ? x : r) + (b >> 3);
+  const int per = p.tiles_m * p.tiles_n;
+  sp = id / per;
+  id -= sp * per;
+  const int gsz = 8 * p.tiles_n, g = id / gsz, first = 8 * g;
+  const int rows = p.tiles_m - first < 8 ? p.tiles_m - first : 8;
+  id -= g * gsz;
+  tm = first + id % rows;
+  tn = id / rows;
+}
+
+// Global row of B that LDS row `r` of a tile holds.  gated: a wave's WN rows
+// are WN / 2 gate rows, then the up rows of the same columns.
+template <bool kGated, int WN>
+__device__ __forceinline__ int b_row(int r, int n0, int N) {
+  if constexpr (kGated) {
+    const int wc = r / WN, rr = r % WN, up = rr >= WN / 2;
+    int n = n0 + wc * (WN / 2) + (up ? rr - WN / 2 : rr);
+    n = n < N ? n : N - 1;
+    return up ? N + n : n;
+  } else {
+    const int n = n0 + r;
+    return n < N ? n : N - 1;
+  }
+}
+
+// A tile of BM x BN, waves of WM x WN, a ring of NST stages filled by direct
+// global -> LDS loads.  One barrier a step: after it stage kt has landed for
+// every wave and stage kt - 1 has been read by every wave, so its place takes
+// the loads of step kt + NST - 1.  The epilogue goes through LDS (a wave's own
+// region) so that it is a rolled loop over whole row pieces.
+template <int DT, bool kGated, int BM, int BN, int WM, int WN, int NST>
+__global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void gemm_ring_kernel(GemmArgs p) {
+  constexpr int NWN = BN / WN, NW = BM / WM * NWN;
+  constexpr int STAGE = (BM + BN) * kStepBytes;
+  constexpr int P = (BM + BN) / 8 / NW;  // loads a wave makes for a stage
+  static_assert(P * NW * 8 == BM + BN, "rows divide over the waves");
+  constexpr int LDE = WN + 4;            // floats a row of the epilogue's region
+  constexpr int EPI = NW * WM * LDE * 4;
+  constexpr int BYTES = STAGE * NST > EPI ? STAGE * NST : EPI;
+  __shared__ __align__(1024) char lds[BYTES];
+
+  int tm, tn, sp;
+  tile_of(p, blockIdx.x, tm, tn, sp);
+  const int m0 = tm * BM, n0 = tn * (kGated ? BN / 2 : BN);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l16 = lane & 15, g = lane >> 4;
+
+  const int nk_all = (int)((p.kb + kStepBytes - 1) / kStepBytes);
+  const int per = (nk_all + p.splits - 1) / p.splits;
+  const int k_lo = sp * per, nk = (k_lo + per < nk_all ? k_lo + per : nk_all) - k_lo;
+
+  const char* src[P];
+  int chunk[P];
+#pragma unroll
+  for (int j = 0; j < P; ++j) {
+    const int q = wave * P + j, r = 8 * q + (lane >> 3);
+    chunk[j] = (lane & 7) ^ ((r >> 1) & 7);
+    if (r < BM) {
+      const int m = m0 + r < p.M ? m0 + r : p.M - 1;
+      src[j] = p.A + (int64_t)m * p.kb;
+    } else {
+      src[j] = p.B + (int64_t)b_row<kGated, WN>(r - BM, n0, p.N) * p.kb;
+    }
+  }
+  auto issue = [&](int kt, int slot) {
+    const int64_t k = (int64_t)(k_lo + kt) * kStepBytes;
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      int64_t off = k + chunk[j] * 16;
+      off = off < p.kb ? off : 0;
+      __builtin_amdgcn_global_load_lds(
+          (const __attribute__((address_space(1))) void*)(src[j] + off),
+          (__attribute__((address_space(3))) void*)(lds + slot * STAGE + (wave * P + j) * 1024),
+          16, 0, 0);
+    }
+  };
+
+  const int wr = wave / NWN, wc = wave % NWN;
+  bk_f32x4 acc[WM / 16][WN / 16];
+#pragma unroll
+  for (int i = 0; i < WM / 16; ++i)
+#pragma unroll
+    for (int j = 0; j < WN / 16; ++j) acc[i][j] = bk_f32x4{0.f, 0.f, 0.f, 0.f};
+
+#pragma unroll
+  for (int s = 0; s < NST - 1; ++s)
+    if (s < nk) issue(s, s);
+
+  int slot = 0;
+  for (int kt = 0; kt < nk; ++kt) {
+    if (kt + NST - 1 <= nk)
+      __builtin_amdgcn_s_waitcnt(wait_vm((NST - 2) * P));
+    else
+      __builtin_amdgcn_s_waitcnt(wait_vm(0));
+    barrier();
+    if (kt + NST - 1 < nk) issue(kt + NST - 1, slot == 0 ? NST - 1 : slot - 1);
+
+    const char* sA = lds + slot * STAGE + (wr * WM + l16) * kStepBytes;
+    const char* sB = lds + slot * STAGE + (BM + wc * WN + l16) * kStepBytes;
+    const int c0 = (g ^ (l16 >> 1)) * 16, c1 = c0 ^ 64;
+    bk_u32x4 fa[WM / 16][2], fb[WN / 16][2];
+#pragma unroll
+    for (int i = 0; i < WM / 16; ++i) {
+      fa[i][0] = *reinterpret_cast<const bk_u32x4*>(sA + i * 16 * kStepBytes + c0);
+      fa[i][1] = *reinterpret_cast<const bk_u32x4*>(sA + i * 16 * kStepBytes + c1);
+    }
+#pragma unroll
+    for (int j = 0; j < WN / 16; ++j) {
+      fb[j][0] = *reinterpret_cast<const bk_u32x4*>(sB + j * 16 * kStepBytes + c0);
+      fb[j][1] = *reinterpret_cast<const bk_u32x4*>(sB + j * 16 * kStepBytes + c1);
+    }
+    const int64_t left = p.kb - (int64_t)(k_lo + kt) * kStepBytes;
+    if (left < kStepBytes) {  // uniform
+      const uint32_t e0 = g * 16 < left ? 0xffffffffu : 0u;
+      const uint32_t e1 = 64 + g * 16 < left ? 0xffffffffu : 0u;
+#pragma unroll
+      for (int i = 0; i < WM / 16; ++i) fa[i][0] &= e0, fa[i][1] &= e1;
+#pragma unroll
+      for (int j = 0; j < WN / 16; ++j) fb[j][0] &= e0, fb[j][1] &= e1;
+    }
+#pragma unroll
+    for (int i = 0; i < WM / 16; ++i)
+#pragma unroll
+      for (int j = 0; j < WN / 16; ++j) acc[i][j] = mma<DT>(fb[j], fa[i], acc[i][j]);
+    slot = slot == NST - 1 ? 0 : slot + 1;
+  }
+
+  // epilogue: the wave's products, row-major, in its own part of LDS
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's LDS reads are done
+  barrier();
+  float* reg = reinterpret_cast<float*>(lds) + wave * WM * LDE;
+#pragma unroll
+  for (int i = 0; i < WM / 16; ++i)
+#pragma unroll
+    for (int j = 0; j < WN / 16; ++j)
+      *reinterpret_cast<bk_f32x4*>(reg + (i * 16 + l16) * LDE + j * 16 + 4 * g) = acc[i][j];
+  __builtin_amdgcn_s_waitcnt(0xC07F);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_wave_barrier();
+
+  constexpr int WCOLS = kGated ? WN / 2 : WN;  // output columns of a wave
+  constexpr int LPR = WCOLS / 8;               // lanes a row
+  constexpr int RPI = 64 / LPR;                // rows an iteration
+  const int col = (lane % LPR) * 8, n = n0 + wc * WCOLS + col;
+  for (int r = lane / LPR; r < WM; r += RPI) {
+    const int m = m0 + wr * WM + r;
+    if (m >= p.M || n >= p.N) continue;
+    float z[8], u[8];
+    const float* row = reg + r * LDE + col;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bk_f32x4 v = *reinterpret_cast<const bk_f32x4*>(row + 4 * h);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) z[4 * h + j] = v[j];
+      if constexpr (kGated) {
+        const bk_f32x4 w = *reinterpret_cast<const bk_f32x4*>(row + WN / 2 + 4 * h);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[4 * h + j] = w[j];
+      }
+    }
+    if (p.part) {
+      float* d = p.part + ((int64_t)sp * p.M + m) * p.ldp + n;
+      *reinterpret_cast<bk_f32x4*>(d) = bk_f32x4{z[0], z[1], z[2], z[3]};
+      *reinterpret_cast<bk_f32x4*>(d + 4) = bk_f32x4{z[4], z[5], z[6], z[7]};
+      if constexpr (kGated) {
+        d += p.N;
+        *reinterpret_cast<bk_f32x4*>(d) = bk_f32x4{u[0], u[1], u[2], u[3]};
+        *reinterpret_cast<bk_f32x4*>(d + 4) = bk_f32x4{u[4], u[5], u[6], u[7]};
+      }
+    } else {
+      epilogue8<kGated>(p, m, n, z, u);
+    }
+  }
+}
+
+template <int DT, bool kGated, int BM, int BN, int WM, int WN, int NST>
+void launch_ring(const GemmArgs& a, hipStream_t st) {
+  hipLaunchKernelGGL((gemm_ring_kernel<DT, kGated, BM, BN, WM, WN, NST>),
+                     dim3(a.tiles_m * a.tiles_n * a.splits), dim3(BM / WM * (BN / WN) * 64), 0, st,
+                     a);
+}
+
+template <int DT>
+int32_t launch(bool gated, int shape, const GemmArgs& a, hipStream_t st) {
+  if (shape == 0) {
+    if (gated)
+      launch_ring<DT, true, 64, 64, 16, 64, 4>(a, st);
+    else
+      launch_ring<DT, false, 64, 64, 32, 32, 4>(a, st);
+  } else {
+    if (gated)
+      launch_ring<DT, true, 128, 128, 64, 64, 3>(a, st);
+    else
+      launch_ring<DT, false, 128, 128, 64, 64, 3>(a, st);
+  }
+  return check_launch("product");
+}
+
+}  // namespace gemm
+}  // namespace lora

@@ -1,5 +1,5 @@
 /* CPython binding of the per-call entry points (lora_apply, lora_apply_ranked,
- * lora_apply_device): argument marshalling only.  A serving loop calls one of
+ * lora_apply_device and the decoder-block operators): argument marshalling only.  A serving loop calls one of
  * these once per layer and step; through ctypes the conversion of their 14 to
  * 16 arguments costs more host time than the library's own plan for a small
  * decode batch, and the host then paces the GPU.  Here each argument is one
@@ -27,7 +27,27 @@ typedef int32_t (*apply_device_fn)(const lora_pool_desc*, const void*, const voi
                                    void*, int32_t, const int32_t*, const uint8_t*, int32_t, void*,
                                    int64_t, void*);
 
+typedef int32_t (*norm_fn)(const lora_norm_desc*, const void*, const void*, const void*, void*,
+                           void*, void*, float*, int32_t, void*);
+typedef int32_t (*linear_fn)(const lora_linear_desc*, const void*, const void*, const float*,
+                             const float*, const void*, const void*, const void*, void*, int32_t,
+                             void*, int64_t, void*);
+typedef int32_t (*gated_fn)(const lora_gated_desc*, const void*, const void*, const float*,
+                            const float*, const void*, void*, void*, int32_t, void*, int64_t,
+                            void*);
+typedef int32_t (*gated_backward_fn)(const lora_gated_desc*, const void*, const void*, const void*,
+                                     const void*, void*, void*, void*, int32_t, void*, int64_t,
+                                     void*);
+
 /* the typedefs match the header's declarations */
+_Static_assert(__builtin_types_compatible_p(__typeof__(&lora_add_rms_norm), norm_fn),
+               "lora_add_rms_norm");
+_Static_assert(__builtin_types_compatible_p(__typeof__(&lora_linear), linear_fn), "lora_linear");
+_Static_assert(__builtin_types_compatible_p(__typeof__(&lora_gated_ffn), gated_fn),
+               "lora_gated_ffn");
+_Static_assert(__builtin_types_compatible_p(__typeof__(&lora_gated_ffn_backward),
+                                            gated_backward_fn),
+               "lora_gated_ffn_backward");
 _Static_assert(__builtin_types_compatible_p(__typeof__(&lora_apply), apply_fn), "lora_apply");
 _Static_assert(__builtin_types_compatible_p(__typeof__(&lora_apply_ranked), apply_ranked_fn),
                "lora_apply_ranked");
@@ -127,7 +147,83 @@ static PyObject* py_apply_device(PyObject* self, PyObject* const* args, Py_ssize
   return PyLong_FromLong(st);
 }
 
+/* add_rms_norm(fn, desc, x, residual, weight, sum, out, out8, scale, T, stream) */
+static PyObject* py_norm(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+  (void)self;
+  static const int kinds[11] = {P, P, P, P, P, P, P, P, P, I32, P};
+  uint64_t a[11];
+  if (convert(args, nargs, "add_rms_norm", kinds, 11, a)) return NULL;
+  const norm_fn f = (norm_fn)(uintptr_t)a[0];
+  int32_t st;
+  Py_BEGIN_ALLOW_THREADS
+  st = f((const lora_norm_desc*)PTR(1), PTR(2), PTR(3), PTR(4), PTR(5), PTR(6), PTR(7),
+         (float*)PTR(8), I32V(9), PTR(10));
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(st);
+}
+
+/* linear(fn, desc, x, w, x_scale, w_scale, bias, delta, residual, out, T, ws,
+ *        ws_bytes, stream) */
+static PyObject* py_linear(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+  (void)self;
+  static const int kinds[14] = {P, P, P, P, P, P, P, P, P, P, I32, P, I64, P};
+  uint64_t a[14];
+  if (convert(args, nargs, "linear", kinds, 14, a)) return NULL;
+  const linear_fn f = (linear_fn)(uintptr_t)a[0];
+  int32_t st;
+  Py_BEGIN_ALLOW_THREADS
+  st = f((const lora_linear_desc*)PTR(1), PTR(2), PTR(3), (const float*)PTR(4),
+         (const float*)PTR(5), PTR(6), PTR(7), PTR(8), PTR(9), I32V(10), PTR(11), I64V(12),
+         PTR(13));
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(st);
+}
+
+/* gated_ffn(fn, desc, x, w, x_scale, w_scale, delta, pre, out, T, ws, ws_bytes,
+ *           stream) */
+static PyObject* py_gated(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+  (void)self;
+  static const int kinds[13] = {P, P, P, P, P, P, P, P, P, I32, P, I64, P};
+  uint64_t a[13];
+  if (convert(args, nargs, "gated_ffn", kinds, 13, a)) return NULL;
+  const gated_fn f = (gated_fn)(uintptr_t)a[0];
+  int32_t st;
+  Py_BEGIN_ALLOW_THREADS
+  st = f((const lora_gated_desc*)PTR(1), PTR(2), PTR(3), (const float*)PTR(4),
+         (const float*)PTR(5), PTR(6), PTR(7), PTR(8), I32V(9), PTR(10), I64V(11), PTR(12));
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(st);
+}
+
+/* gated_ffn_backward(fn, desc, dout, pre, x, w, dpre, dx, dw, T, ws, ws_bytes,
+ *                    stream) */
+static PyObject* py_gated_backward(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+  (void)self;
+  static const int kinds[13] = {P, P, P, P, P, P, P, P, P, I32, P, I64, P};
+  uint64_t a[13];
+  if (convert(args, nargs, "gated_ffn_backward", kinds, 13, a)) return NULL;
+  const gated_backward_fn f = (gated_backward_fn)(uintptr_t)a[0];
+  int32_t st;
+  Py_BEGIN_ALLOW_THREADS
+  st = f((const lora_gated_desc*)PTR(1), PTR(2), PTR(3), PTR(4), PTR(5), PTR(6), PTR(7), PTR(8),
+         I32V(9), PTR(10), I64V(11), PTR(12));
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(st);
+}
+
 static PyMethodDef methods[] = {
+    {"add_rms_norm", (PyCFunction)(void (*)(void))py_norm, METH_FASTCALL,
+     "add_rms_norm(fn, desc, x, residual, weight, sum, out, out8, scale, T, stream) -> status of "
+     "lora_add_rms_norm"},
+    {"linear", (PyCFunction)(void (*)(void))py_linear, METH_FASTCALL,
+     "linear(fn, desc, x, w, x_scale, w_scale, bias, delta, residual, out, T, ws, ws_bytes, "
+     "stream) -> status of lora_linear"},
+    {"gated_ffn", (PyCFunction)(void (*)(void))py_gated, METH_FASTCALL,
+     "gated_ffn(fn, desc, x, w, x_scale, w_scale, delta, pre, out, T, ws, ws_bytes, stream) -> "
+     "status of lora_gated_ffn"},
+    {"gated_ffn_backward", (PyCFunction)(void (*)(void))py_gated_backward, METH_FASTCALL,
+     "gated_ffn_backward(fn, desc, dout, pre, x, w, dpre, dx, dw, T, ws, ws_bytes, stream) -> "
+     "status of lora_gated_ffn_backward"},
     {"apply", (PyCFunction)(void (*)(void))py_apply, METH_FASTCALL,
      "apply(fn, desc, A_pool, B_pool, x, y, T, ids_host, prefill_host, bgmv_max_rank, ws, "
      "ws_bytes, meta_host, meta_host_bytes, stream) -> status of lora_apply"},
