@@ -58,8 +58,8 @@ int32_t gemm_launch_f32(bool gated, int shape, const GemmArgs& a, hipStream_t st
 struct TileShape {
   int bm, bn;  // rows of A and rows of B a workgroup covers
 };
-// shapes of gemm_ring_kernel, smallest first
-constexpr TileShape kShapes[] = {{64, 64}, {128, 128}};
+// shapes, smallest first: two of gemm_ring_kernel, then gemm_phase_kernel's
+constexpr TileShape kShapes[] = {{64, 64}, {128, 128}, {256, 256}};
 
 int32_t check_launch(const char* what);
 

@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cstdlib>
 
 #include "lora_block.h"
 
@@ -62,13 +63,21 @@ GemmPlan gemm_plan(int32_t dtype, bool gated, int64_t M, int64_t N, int64_t kb) 
            ((width + kShapes[s].bn - 1) / kShapes[s].bn);
   };
   // the large tile where it gives every compute unit one
-  g.shape = tiles(1) >= kComputeUnits ? 1 : 0;
+  g.shape = tiles(2) >= kComputeUnits ? 2 : tiles(1) >= kComputeUnits ? 1 : 0;
   const int64_t steps = (kb + kStepBytes - 1) / kStepBytes;
   const int64_t t = tiles(g.shape);
   // a K split where the tiles leave compute units idle: up to two workgroups a
   // unit, at least eight steps a part
   int64_t s = std::max<int64_t>(1, std::min<int64_t>(2 * kComputeUnits / t, steps / 8));
   s = std::min<int64_t>(s, 16);
+  if (const char* e = std::getenv("LORA_GEMM_PLAN")) {  // tuning override: shape,splits
+    char* end = nullptr;
+    const long shape = std::strtol(e, &end, 10);
+    const long parts = *end == ',' ? std::strtol(end + 1, nullptr, 10) : 0;
+    if (shape >= 0 && shape < (long)(sizeof(kShapes) / sizeof(kShapes[0])))
+      g.shape = (int32_t)shape;
+    if (parts >= 1 && parts <= 64) s = std::min<int64_t>(parts, steps);
+  }
   if (s > 1) {
     const int64_t per = (steps + s - 1) / s;
     s = (steps + per - 1) / per;  // no part is empty

@@ -125,6 +125,29 @@ __device__ __forceinline__ int b_row(int r, int n0, int N) {
   }
 }
 
+template <int V>
+struct Int {
+  static constexpr int value = V;
+};
+
+// Eight products of row m: a partial of K split `sp`, or the epilogue.
+template <bool kGated>
+__device__ __forceinline__ void finish8(const GemmArgs& p, int sp, int m, int n, float (&z)[8],
+                                        float (&u)[8]) {
+  if (p.part) {
+    float* d = p.part + ((int64_t)sp * p.M + m) * p.ldp + n;
+    *reinterpret_cast<bk_f32x4*>(d) = bk_f32x4{z[0], z[1], z[2], z[3]};
+    *reinterpret_cast<bk_f32x4*>(d + 4) = bk_f32x4{z[4], z[5], z[6], z[7]};
+    if constexpr (kGated) {
+      d += p.N;
+      *reinterpret_cast<bk_f32x4*>(d) = bk_f32x4{u[0], u[1], u[2], u[3]};
+      *reinterpret_cast<bk_f32x4*>(d + 4) = bk_f32x4{u[4], u[5], u[6], u[7]};
+    }
+  } else {
+    epilogue8<kGated>(p, m, n, z, u);
+  }
+}
+
 // A tile of BM x BN, waves of WM x WN, a ring of NST stages filled by direct
 // global -> LDS loads.  One barrier a step: after it stage kt has landed for
 // every wave and stage kt - 1 has been read by every wave, so its place takes
@@ -261,18 +284,232 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void gemm_ring_kernel(Gem
         for (int j = 0; j < 4; ++j) u[4 * h + j] = w[j];
       }
     }
-    if (p.part) {
-      float* d = p.part + ((int64_t)sp * p.M + m) * p.ldp + n;
-      *reinterpret_cast<bk_f32x4*>(d) = bk_f32x4{z[0], z[1], z[2], z[3]};
-      *reinterpret_cast<bk_f32x4*>(d + 4) = bk_f32x4{z[4], z[5], z[6], z[7]};
-      if constexpr (kGated) {
-        d += p.N;
-        *reinterpret_cast<bk_f32x4*>(d) = bk_f32x4{u[0], u[1], u[2], u[3]};
-        *reinterpret_cast<bk_f32x4*>(d + 4) = bk_f32x4{u[4], u[5], u[6], u[7]};
-      }
-    } else {
-      epilogue8<kGated>(p, m, n, z, u);
+    finish8<kGated>(p, sp, m, n, z, u);
+  }
+}
+
+// The large product: a 256 x 256 tile, 8 waves of 128 x 64 (two a SIMD), and
+// two LDS buffers of one step each, cut into four pieces of 16 KB (A0, A1: the
+// two halves of the rows of A; B0, B1: of B) that are read and refilled apart.
+//
+// A step is four phases, one quadrant of a wave's tile each:
+//   phase 0: read A0, B0, multiply A0 B0;  load B1 of the next step
+//   phase 1: read B1,     multiply A0 B1;  load A1 of the next step
+//   phase 2: read A1,     multiply A1 B1;  load A0 of the step after
+//   phase 3:              multiply A1 B0;  load B0 of the step after
+// and a phase is two slots with a barrier after each: one for memory (LDS
+// reads into registers, two direct loads) and one for 16 matrix instructions.
+// Waves 4 to 7 run one slot behind waves 0 to 3, so on every SIMD one wave
+// multiplies while the other reads: the matrix unit sees no memory slots.
+//
+// What orders the accesses.  A wave's reads of a phase are complete when the
+// phase's products are, at most two slots after the reads were issued; a piece
+// is refilled two phases (four slots) or more after it was read.  Loads of a
+// wave complete in order, eight (four pieces) may be outstanding when the wave
+// leaves a memory slot, and the piece that the next phase reads is the fifth
+// newest: it has landed for every wave once all have passed the barriers of
+// that slot and the next.
+template <int DT, bool kGated>
+__global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
+  constexpr int PIECE = 128 * kStepBytes, BUF = 4 * PIECE;
+  constexpr int LDE = 64 + 4;             // floats a row of the epilogue's region
+  constexpr int EPI = 8 * 64 * LDE * 4;   // half of every wave's rows at a time
+  __shared__ __align__(1024) char lds[EPI > 2 * BUF ? EPI : 2 * BUF];
+
+  int tm, tn, sp;
+  tile_of(p, blockIdx.x, tm, tn, sp);
+  const int m0 = tm * 256, n0 = tn * (kGated ? 128 : 256);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l16 = lane & 15, g = lane >> 4;
+  const int wr = wave >> 2, wc = wave & 3;
+
+  const int nk_all = (int)((p.kb + kStepBytes - 1) / kStepBytes);
+  const int per = (nk_all + p.splits - 1) / p.splits;
+  const int k_lo = sp * per, nk = (k_lo + per < nk_all ? k_lo + per : nk_all) - k_lo;
+  const int tail = (int)(p.kb - (int64_t)(k_lo + nk - 1) * kStepBytes);  // of the last step
+
+  // loads: a wave fills 8-row runs w and w + 8 of every piece, so its lanes
+  // take the same chunk of a row in every load
+  const int chunk16 = 16 * ((lane & 7) ^ ((wave & 1) * 4 + (lane >> 4)));
+  const char* baseA = p.A + (int64_t)m0 * p.kb + (int64_t)k_lo * kStepBytes;
+  const char* baseB0 = p.B + (int64_t)n0 * p.kb + (int64_t)k_lo * kStepBytes;
+  const char* baseB1 = kGated ? baseB0 + (int64_t)p.N * p.kb : baseB0;
+  uint32_t offA[2][2], offB[2][2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int r = 8 * (wave + 8 * j) + (lane >> 3);
+      int m = h * 128 + r;
+      m = m0 + m < p.M ? m : p.M - 1 - m0;
+      // linear: a wave's 64 columns are consecutive, 32 from each half of B
+      int n = kGated ? r : (r >> 5) * 64 + h * 32 + (r & 31);
+      n = n0 + n < p.N ? n : p.N - 1 - n0;
+      offA[h][j] = (uint32_t)(m * (int)p.kb);
+      offB[h][j] = (uint32_t)(n * (int)p.kb);
     }
+  auto fill = [&](const char* base, const uint32_t (&off)[2], int piece, int kt) {
+    // past the end of a row, the step's first chunk (zeroed after the LDS read)
+    const int c = kt == nk - 1 && chunk16 >= tail ? 0 : chunk16;
+    char* to = lds + (kt & 1) * BUF + piece * PIECE + wave * 1024;
+    const char* from = base + (int64_t)kt * kStepBytes;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      __builtin_amdgcn_global_load_lds(
+          (const __attribute__((address_space(1))) void*)(from + (off[j] + (uint32_t)c)),
+          (__attribute__((address_space(3))) void*)(to + j * 8192), 16, 0, 0);
+  };
+
+  bk_f32x4 acc[2][2][4][2];
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[a][b][i][j] = bk_f32x4{0.f, 0.f, 0.f, 0.f};
+  bk_u32x4 fa[4][2], fb[2][2][2];
+
+  const int c0 = (g ^ (l16 >> 1)) * 16, c1 = c0 ^ 64;
+  const char* rdA = lds + (wr * 64 + l16) * kStepBytes;
+  const char* rdB = lds + 2 * PIECE + (wc * 32 + l16) * kStepBytes;
+  const uint32_t keep0 = g * 16 < tail ? 0xffffffffu : 0u;
+  const uint32_t keep1 = 64 + g * 16 < tail ? 0xffffffffu : 0u;
+
+  auto read_a = [&](int h, int kt) {
+    const char* s = rdA + (kt & 1) * BUF + h * PIECE;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      fa[i][0] = *reinterpret_cast<const bk_u32x4*>(s + i * 16 * kStepBytes + c0);
+      fa[i][1] = *reinterpret_cast<const bk_u32x4*>(s + i * 16 * kStepBytes + c1);
+    }
+  };
+  auto read_b = [&](int h, int kt) {
+    const char* s = rdB + (kt & 1) * BUF + h * PIECE;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      fb[h][j][0] = *reinterpret_cast<const bk_u32x4*>(s + j * 16 * kStepBytes + c0);
+      fb[h][j][1] = *reinterpret_cast<const bk_u32x4*>(s + j * 16 * kStepBytes + c1);
+    }
+  };
+  auto products = [&](int ha, int hb) {
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        acc[ha][hb][i][j] = mma<DT>(fb[hb][j], fa[i], acc[ha][hb][i][j]);
+    __builtin_amdgcn_s_setprio(0);
+  };
+  auto slot_end = [&]() {
+    __builtin_amdgcn_sched_barrier(0);
+    barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // kLeft: steps after this one (2: two or more, all loads are made)
+  auto step = [&](int kt, auto left_tag) {
+    constexpr int kLeft = decltype(left_tag)::value;
+    read_a(0, kt);
+    read_b(0, kt);
+    if constexpr (kLeft >= 1) fill(baseB1, offB[1], 3, kt + 1);
+    __builtin_amdgcn_s_waitcnt(wait_vm(kLeft >= 1 ? 8 : 2));
+    slot_end();
+    if constexpr (kLeft == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) fa[i][0] &= keep0, fa[i][1] &= keep1;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) fb[0][j][0] &= keep0, fb[0][j][1] &= keep1;
+    }
+    products(0, 0);
+    slot_end();
+
+    read_b(1, kt);
+    if constexpr (kLeft >= 1) fill(baseA, offA[1], 1, kt + 1);
+    __builtin_amdgcn_s_waitcnt(wait_vm(kLeft >= 1 ? 8 : 0));
+    slot_end();
+    if constexpr (kLeft == 0) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) fb[1][j][0] &= keep0, fb[1][j][1] &= keep1;
+    }
+    products(0, 1);
+    slot_end();
+
+    read_a(1, kt);
+    if constexpr (kLeft >= 2) fill(baseA, offA[0], 0, kt + 2);
+    slot_end();
+    if constexpr (kLeft == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) fa[i][0] &= keep0, fa[i][1] &= keep1;
+    }
+    products(1, 1);
+    slot_end();
+
+    if constexpr (kLeft >= 2) fill(baseB0, offB[0], 2, kt + 2);
+    if constexpr (kLeft >= 1) __builtin_amdgcn_s_waitcnt(wait_vm(kLeft >= 2 ? 8 : 4));
+    slot_end();
+    products(1, 0);
+    slot_end();
+  };
+
+  fill(baseA, offA[0], 0, 0);
+  fill(baseB0, offB[0], 2, 0);
+  fill(baseB1, offB[1], 3, 0);
+  fill(baseA, offA[1], 1, 0);
+  if (nk > 1) {
+    fill(baseA, offA[0], 0, 1);
+    fill(baseB0, offB[0], 2, 1);
+    __builtin_amdgcn_s_waitcnt(wait_vm(8));
+  } else {
+    __builtin_amdgcn_s_waitcnt(wait_vm(4));
+  }
+  slot_end();
+  if (wave >= 4) slot_end();  // one slot behind
+  int kt = 0;
+  for (; kt < nk - 2; ++kt) step(kt, Int<2>{});
+  if (nk > 1) step(kt++, Int<1>{});
+  step(kt, Int<0>{});
+  if (wave < 4) slot_end();
+
+  // epilogue: 64 rows of every wave at a time through its own part of LDS
+  float* reg = reinterpret_cast<float*>(lds) + wave * 64 * LDE;
+  constexpr int LPR = kGated ? 4 : 8, RPI = 64 / LPR;
+  const int col = (lane % LPR) * 8;
+  const int n = n0 + wc * (kGated ? 32 : 64) + col;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    barrier();  // (all waves are past their LDS reads; the pass before is read)
+#pragma unroll
+    for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          *reinterpret_cast<bk_f32x4*>(reg + (i * 16 + l16) * LDE + hb * 32 + j * 16 + 4 * g) =
+              acc[h][hb][i][j];
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+    for (int r = lane / LPR; r < 64; r += RPI) {
+      const int m = m0 + h * 128 + wr * 64 + r;
+      if (m >= p.M || n >= p.N) continue;
+      float z[8], u[8];
+      const float* row = reg + r * LDE + col;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const bk_f32x4 v = *reinterpret_cast<const bk_f32x4*>(row + 4 * q);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[4 * q + j] = v[j];
+        if constexpr (kGated) {
+          const bk_f32x4 w = *reinterpret_cast<const bk_f32x4*>(row + 32 + 4 * q);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) u[4 * q + j] = w[j];
+        }
+      }
+      finish8<kGated>(p, sp, m, n, z, u);
+    }
+    __builtin_amdgcn_s_waitcnt(0xC07F);
   }
 }
 
@@ -290,11 +527,17 @@ int32_t launch(bool gated, int shape, const GemmArgs& a, hipStream_t st) {
       launch_ring<DT, true, 64, 64, 16, 64, 4>(a, st);
     else
       launch_ring<DT, false, 64, 64, 32, 32, 4>(a, st);
-  } else {
+  } else if (shape == 1) {
     if (gated)
       launch_ring<DT, true, 128, 128, 64, 64, 3>(a, st);
     else
       launch_ring<DT, false, 128, 128, 64, 64, 3>(a, st);
+  } else {
+    const dim3 grid(a.tiles_m * a.tiles_n * a.splits);
+    if (gated)
+      hipLaunchKernelGGL((gemm_phase_kernel<DT, true>), grid, dim3(512), 0, st, a);
+    else
+      hipLaunchKernelGGL((gemm_phase_kernel<DT, false>), grid, dim3(512), 0, st, a);
   }
   return check_launch("product");
 }

@@ -187,6 +187,30 @@ def test_linear_exact_integers(dtype, od, T, K, O):
     assert torch.equal(got, z.to(TORCH[od]))
 
 
+# tile shapes, each with and without a K split (the plan would take some of
+# them at large sizes alone)
+SHAPES = ["0,1", "0,3", "1,1", "1,2", "2,1", "2,3"]
+
+
+@pytest.mark.parametrize("plan", SHAPES)
+@pytest.mark.parametrize("dtype,od", TYPES)
+def test_every_shape(dtype, od, plan, monkeypatch):
+    monkeypatch.setenv("LORA_GEMM_PLAN", plan)
+    unit = 16 if dtype == "e4m3" else 8
+    for k, (T, K, O) in enumerate(((1, unit, 17), (255, 64, 255), (257, 272, 513), (600, 1040, 301),
+                                   (300, 2064, 260), (513, 384, 777))):
+        _check_linear(T, K, O, dtype, od, "none", k % 2 == 0, k % 3 == 0, k % 2 == 1, k)
+        I = max(unit, O // unit * unit)
+        _check_gated(T, K, I, dtype, od, "silu", k % 2 == 0, k % 3 == 0, k)
+    g = gen(2)
+    for T, K, O in ((300, 528, 270), (130, 64, 1000)):
+        x, xs = operand(g, T, K, dtype, 1.0, integer=True)
+        w, ws = operand(g, O, K, dtype, 1.0, integer=True)
+        got = run_linear(x, w, xs, ws, None, None, None, dtype, "f32" if dtype == "f32" else od,
+                         "none")
+        assert torch.equal(got, (x.double() @ w.double().t()).to(got.dtype))
+
+
 def test_linear_inf_and_nan_stay_in_their_rows():
     # K ends inside a tile step and T inside a tile: what lies past a row's end
     # is the next row, whose infinities and NaN must not come in
