@@ -86,6 +86,9 @@ __host__ __device__ constexpr int wait_vm(int n) {
   return (n & 15) | ((n >> 4) << 14) | 0x0F70;
 }
 
+// the same with every LDS operation waited for
+__host__ __device__ constexpr int wait_all_lds(int n) { return wait_vm(n) & ~0x0F00; }
+
 __device__ __forceinline__ void barrier() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
@@ -292,23 +295,21 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void gemm_ring_kernel(Gem
 // two LDS buffers of one step each, cut into four pieces of 16 KB (A0, A1: the
 // two halves of the rows of A; B0, B1: of B) that are read and refilled apart.
 //
-// A step is four phases, one quadrant of a wave's tile each:
-//   phase 0: read A0, B0, multiply A0 B0;  load B1 of the next step
-//   phase 1: read B1,     multiply A0 B1;  load A1 of the next step
-//   phase 2: read A1,     multiply A1 B1;  load A0 of the step after
-//   phase 3:              multiply A1 B0;  load B0 of the step after
+// A step is two phases, one half of a wave's rows each:
+//   phase 0: read A0, B0, B1, multiply A0 B0, A0 B1;  load A1 of the next step
+//   phase 1: read A1, multiply A1 B1, A1 B0;  load A0, B0, B1 of the step after
 // and a phase is two slots with a barrier after each: one for memory (LDS
-// reads into registers, two direct loads) and one for 16 matrix instructions.
-// Waves 4 to 7 run one slot behind waves 0 to 3, so on every SIMD one wave
-// multiplies while the other reads: the matrix unit sees no memory slots.
+// reads into registers, direct loads) and one for the products (32 matrix
+// instructions of 16 cycles).  Waves 4 to 7 run one slot behind waves 0 to 3,
+// so on every SIMD one wave multiplies while the other reads.  Four phases of
+// half this length spent 23% of their time in the barriers between them.
 //
-// What orders the accesses.  A wave's reads of a phase are complete when the
-// phase's products are, at most two slots after the reads were issued; a piece
-// is refilled two phases (four slots) or more after it was read.  Loads of a
-// wave complete in order, eight (four pieces) may be outstanding when the wave
-// leaves a memory slot, and the piece that the next phase reads is the fifth
-// newest: it has landed for every wave once all have passed the barriers of
-// that slot and the next.
+// What orders the accesses.  A wave's LDS reads are complete at the end of the
+// memory slot that issued them; a piece is refilled in the next phase's memory
+// slot at the earliest, two slots later.  Loads of a wave complete in order
+// and eight may be outstanding when it leaves a memory slot: those issued
+// before have landed, which are the ones that the next phase reads, and do so
+// for every wave once all have passed the barriers of that slot and the next.
 template <int DT, bool kGated>
 __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
   constexpr int PIECE = 128 * kStepBytes, BUF = 4 * PIECE;
@@ -394,13 +395,15 @@ __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
       fb[h][j][1] = *reinterpret_cast<const bk_u32x4*>(s + j * 16 * kStepBytes + c1);
     }
   };
-  auto products = [&](int ha, int hb) {
+  auto products = [&](int ha) {
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        acc[ha][hb][i][j] = mma<DT>(fb[hb][j], fa[i], acc[ha][hb][i][j]);
+      for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[ha][hb][i][j] = mma<DT>(fb[hb][j], fa[i], acc[ha][hb][i][j]);
     __builtin_amdgcn_s_setprio(0);
   };
   auto slot_end = [&]() {
@@ -413,43 +416,34 @@ __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
     constexpr int kLeft = decltype(left_tag)::value;
     read_a(0, kt);
     read_b(0, kt);
-    if constexpr (kLeft >= 1) fill(baseB1, offB[1], 3, kt + 1);
-    __builtin_amdgcn_s_waitcnt(wait_vm(kLeft >= 1 ? 8 : 2));
+    read_b(1, kt);
+    if constexpr (kLeft >= 1) fill(baseA, offA[1], 1, kt + 1);
+    __builtin_amdgcn_s_waitcnt(wait_all_lds(kLeft >= 1 ? 8 : 0));
     slot_end();
     if constexpr (kLeft == 0) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) fa[i][0] &= keep0, fa[i][1] &= keep1;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) fb[0][j][0] &= keep0, fb[0][j][1] &= keep1;
-    }
-    products(0, 0);
-    slot_end();
-
-    read_b(1, kt);
-    if constexpr (kLeft >= 1) fill(baseA, offA[1], 1, kt + 1);
-    __builtin_amdgcn_s_waitcnt(wait_vm(kLeft >= 1 ? 8 : 0));
-    slot_end();
-    if constexpr (kLeft == 0) {
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) fb[1][j][0] &= keep0, fb[1][j][1] &= keep1;
+        for (int j = 0; j < 2; ++j) fb[h][j][0] &= keep0, fb[h][j][1] &= keep1;
     }
-    products(0, 1);
+    products(0);
     slot_end();
 
     read_a(1, kt);
-    if constexpr (kLeft >= 2) fill(baseA, offA[0], 0, kt + 2);
+    if constexpr (kLeft >= 2) {
+      fill(baseA, offA[0], 0, kt + 2);
+      fill(baseB0, offB[0], 2, kt + 2);
+      fill(baseB1, offB[1], 3, kt + 2);
+    }
+    __builtin_amdgcn_s_waitcnt(wait_all_lds(kLeft >= 2 ? 8 : kLeft == 1 ? 2 : 0));
     slot_end();
     if constexpr (kLeft == 0) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) fa[i][0] &= keep0, fa[i][1] &= keep1;
     }
-    products(1, 1);
-    slot_end();
-
-    if constexpr (kLeft >= 2) fill(baseB0, offB[0], 2, kt + 2);
-    if constexpr (kLeft >= 1) __builtin_amdgcn_s_waitcnt(wait_vm(kLeft >= 2 ? 8 : 4));
-    slot_end();
-    products(1, 0);
+    products(1);
     slot_end();
   };
 
@@ -460,9 +454,10 @@ __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
   if (nk > 1) {
     fill(baseA, offA[0], 0, 1);
     fill(baseB0, offB[0], 2, 1);
+    fill(baseB1, offB[1], 3, 1);
     __builtin_amdgcn_s_waitcnt(wait_vm(8));
   } else {
-    __builtin_amdgcn_s_waitcnt(wait_vm(4));
+    __builtin_amdgcn_s_waitcnt(wait_vm(2));
   }
   slot_end();
   if (wave >= 4) slot_end();  // one slot behind
