@@ -12,11 +12,14 @@
 namespace lora {
 
 // One product z[m][n] = sum_k A[m][k] B[n][k] and what its epilogue does.
-// A and B are row-major with the reduction contiguous; `kb` is the length of a
-// row in bytes (a multiple of 16) and also its stride.
 //   linear: out[m][n] = act(sa[m] sb[n] z + bias[n] + delta[m][n]) + residual[m][n]
 //   gated:  B has 2 n rows (gate rows, then up rows); pre = sa sb z + delta,
 //           out[m][n] = act(pre[m][n]) * pre[m][n + N]
+// A and B are stored with the reduction contiguous; in the gradients' products
+// (epilogue as linear) they are stored reduction-major: B as [k][n] in the
+// gradient of x, A as [k][m] and B as [k][n] in the gradient of w.
+enum Form { kLinearForm = 0, kGatedForm = 1, kGradX = 2, kGradW = 3 };
+
 struct GemmArgs {
   const char* A;
   const char* B;
@@ -28,7 +31,8 @@ struct GemmArgs {
   void* pre;              // gated: [M][2 N], or nullptr
   void* out;              // [M][N]
   float* part;            // split K: [splits][M][ldp] raw products, or nullptr
-  int64_t kb;
+  int64_t kb;             // bytes of the reduction
+  int64_t lda, ldb;       // bytes from a stored row to the next (multiples of 16)
   int32_t M, N;
   int32_t ldp;            // floats a row of `part`
   int32_t splits;
@@ -47,13 +51,13 @@ struct GemmPlan {
   int32_t splits;
   int64_t ws_bytes;  // fp32 partials
 };
-GemmPlan gemm_plan(int32_t dtype, bool gated, int64_t M, int64_t N, int64_t kb);
-int32_t gemm_run(int32_t dtype, bool gated, const GemmPlan& plan, GemmArgs a, void* ws,
+GemmPlan gemm_plan(int32_t dtype, Form form, int64_t M, int64_t N, int64_t kb);
+int32_t gemm_run(int32_t dtype, Form form, const GemmPlan& plan, GemmArgs a, void* ws,
                  hipStream_t st);
 // per type (each in its own source file)
-int32_t gemm_launch_bf16(bool gated, int shape, const GemmArgs& a, hipStream_t st);
-int32_t gemm_launch_e4m3(bool gated, int shape, const GemmArgs& a, hipStream_t st);
-int32_t gemm_launch_f32(bool gated, int shape, const GemmArgs& a, hipStream_t st);
+int32_t gemm_launch_bf16(Form form, int shape, const GemmArgs& a, hipStream_t st);
+int32_t gemm_launch_e4m3(Form form, int shape, const GemmArgs& a, hipStream_t st);
+int32_t gemm_launch_f32(Form form, int shape, const GemmArgs& a, hipStream_t st);
 
 struct TileShape {
   int bm, bn;  // rows of A and rows of B a workgroup covers

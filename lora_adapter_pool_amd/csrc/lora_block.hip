@@ -55,9 +55,9 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs p) {
 
 }  // namespace
 
-GemmPlan gemm_plan(int32_t dtype, bool gated, int64_t M, int64_t N, int64_t kb) {
+GemmPlan gemm_plan(int32_t dtype, Form form, int64_t M, int64_t N, int64_t kb) {
   GemmPlan g{0, 1, 0};
-  const int64_t width = gated ? 2 * N : N;  // rows of B
+  const int64_t width = form == kGatedForm ? 2 * N : N;  // rows of B
   auto tiles = [&](int s) {
     return ((M + kShapes[s].bm - 1) / kShapes[s].bm) *
            ((width + kShapes[s].bn - 1) / kShapes[s].bn);
@@ -87,8 +87,9 @@ GemmPlan gemm_plan(int32_t dtype, bool gated, int64_t M, int64_t N, int64_t kb) 
   return g;
 }
 
-int32_t gemm_run(int32_t dtype, bool gated, const GemmPlan& plan, GemmArgs a, void* ws,
+int32_t gemm_run(int32_t dtype, Form form, const GemmPlan& plan, GemmArgs a, void* ws,
                  hipStream_t st) {
+  const bool gated = form == kGatedForm;
   const TileShape sh = kShapes[plan.shape];
   const int width = gated ? 2 * a.N : a.N;
   a.tiles_m = (a.M + sh.bm - 1) / sh.bm;
@@ -96,9 +97,9 @@ int32_t gemm_run(int32_t dtype, bool gated, const GemmPlan& plan, GemmArgs a, vo
   a.splits = plan.splits;
   a.part = plan.splits > 1 ? (float*)ws : nullptr;
   a.ldp = (width + 7) / 8 * 8;
-  int32_t e = dtype == LORA_BF16   ? gemm_launch_bf16(gated, plan.shape, a, st)
-              : dtype == LORA_E4M3 ? gemm_launch_e4m3(gated, plan.shape, a, st)
-                                   : gemm_launch_f32(gated, plan.shape, a, st);
+  int32_t e = dtype == LORA_BF16   ? gemm_launch_bf16(form, plan.shape, a, st)
+              : dtype == LORA_E4M3 ? gemm_launch_e4m3(form, plan.shape, a, st)
+                                   : gemm_launch_f32(form, plan.shape, a, st);
   if (e || plan.splits == 1) return e;
   const int64_t threads = (int64_t)a.M * ((a.N + 7) / 8);
   const dim3 grid((unsigned)((threads + 255) / 256));
@@ -140,66 +141,28 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(const void* dout, const 
   store8(dpre, m * 2 * I + I + n, 8, DT, u);
 }
 
-// dst[c][r] = src[r][c] for r < R, zero for R <= r < ldd; a 64 x 64 tile a
-// workgroup through LDS.
-template <typename E>
-__global__ __launch_bounds__(256) void transpose_kernel(const E* src, E* dst, int R, int C,
-                                                        int ldd) {
-  __shared__ E tile[64][65];
-  const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
-  for (int i = threadIdx.x; i < 64 * 64; i += 256) {
-    const int r = i >> 6, c = i & 63;
-    tile[r][c] = r0 + r < R && c0 + c < C ? src[(int64_t)(r0 + r) * C + c0 + c] : E(0);
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 64 * 64; i += 256) {
-    const int c = i >> 6, r = i & 63;
-    if (c0 + c < C && r0 + r < ldd) dst[(int64_t)(c0 + c) * ldd + r0 + r] = tile[r][c];
-  }
-}
-
-void transpose(int32_t dtype, const void* src, void* dst, int R, int C, int ldd, hipStream_t st) {
-  const dim3 grid((C + 63) / 64, (ldd + 63) / 64);
-  if (dtype == LORA_BF16)
-    hipLaunchKernelGGL(transpose_kernel<uint16_t>, grid, dim3(256), 0, st, (const uint16_t*)src,
-                       (uint16_t*)dst, R, C, ldd);
-  else
-    hipLaunchKernelGGL(transpose_kernel<uint32_t>, grid, dim3(256), 0, st, (const uint32_t*)src,
-                       (uint32_t*)dst, R, C, ldd);
-}
-
 __global__ __launch_bounds__(256) void clear_kernel(bk_u32x4* p, int64_t n) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
     p[i] = bk_u32x4{0, 0, 0, 0};
 }
 
-struct BackwardLayout {
-  int64_t wt, dt, xt, part, total;
+// The two products run one after the other and share the workspace.
+struct BackwardPlan {
   GemmPlan dx, dw;
-  int32_t ldt;  // elements a row of the arrays transposed over the tokens
+  int64_t total;
 };
 
-BackwardLayout backward_layout(const lora_gated_desc& d, int64_t T, bool dx, bool dw) {
-  BackwardLayout b{};
+BackwardPlan backward_plan(const lora_gated_desc& d, int64_t T, bool dx, bool dw) {
+  BackwardPlan b{};
   const int64_t e = esize(d.dtype), K = d.in_features, I2 = 2 * (int64_t)d.inter_features;
-  b.ldt = (int32_t)align_up(T, 16 / e);
-  int64_t at = 0, part = 0;
-  b.wt = at;
   if (dx) {
-    at = align_up(at + e * K * I2, 256);
-    b.dx = gemm_plan(d.dtype, false, T, K, e * I2);
-    part = std::max(part, b.dx.ws_bytes);
+    b.dx = gemm_plan(d.dtype, kGradX, T, K, e * I2);
+    b.total = std::max(b.total, b.dx.ws_bytes);
   }
-  b.dt = at;
   if (dw) {
-    at = align_up(at + e * I2 * b.ldt, 256);
-    b.xt = at;
-    at = align_up(at + e * K * b.ldt, 256);
-    b.dw = gemm_plan(d.dtype, false, I2, K, e * b.ldt);
-    part = std::max(part, b.dw.ws_bytes);
+    b.dw = gemm_plan(d.dtype, kGradW, I2, K, e * T);
+    b.total = std::max(b.total, b.dw.ws_bytes);
   }
-  b.part = at;
-  b.total = at + part;
   return b;
 }
 
@@ -294,7 +257,7 @@ int64_t lora_linear_workspace_bytes(const lora_linear_desc* desc, int32_t T) {
   if (int32_t e = check_linear(desc)) return e;
   if (int32_t e = check_rows(T)) return e;
   if (T == 0) return 0;
-  return gemm_plan(desc->dtype, false, T, desc->out_features,
+  return gemm_plan(desc->dtype, kLinearForm, T, desc->out_features,
                    desc->in_features * esize(desc->dtype))
       .ws_bytes;
 }
@@ -315,7 +278,7 @@ int32_t lora_linear(const lora_linear_desc* desc, const void* x, const void* w,
   if (int32_t e = may(residual, "residual")) return e;
   if (int32_t e = need(out, "out")) return e;
   const int64_t kb = desc->in_features * esize(desc->dtype);
-  const GemmPlan plan = gemm_plan(desc->dtype, false, T, desc->out_features, kb);
+  const GemmPlan plan = gemm_plan(desc->dtype, kLinearForm, T, desc->out_features, kb);
   if (int32_t e = check_ws(ws, ws_bytes, plan.ws_bytes)) return e;
   GemmArgs a{};
   a.A = (const char*)x;
@@ -326,12 +289,12 @@ int32_t lora_linear(const lora_linear_desc* desc, const void* x, const void* w,
   a.delta = delta;
   a.residual = residual;
   a.out = out;
-  a.kb = kb;
+  a.kb = a.lda = a.ldb = kb;
   a.M = T;
   a.N = desc->out_features;
   a.out_dtype = desc->out_dtype;
   a.act = desc->act;
-  return gemm_run(desc->dtype, false, plan, a, ws, (hipStream_t)stream);
+  return gemm_run(desc->dtype, kLinearForm, plan, a, ws, (hipStream_t)stream);
 }
 
 int64_t lora_gated_ffn_workspace_bytes(const lora_gated_desc* desc, int32_t T) {
@@ -339,7 +302,7 @@ int64_t lora_gated_ffn_workspace_bytes(const lora_gated_desc* desc, int32_t T) {
   if (int32_t e = check_gated(desc)) return e;
   if (int32_t e = check_rows(T)) return e;
   if (T == 0) return 0;
-  return gemm_plan(desc->dtype, true, T, desc->inter_features,
+  return gemm_plan(desc->dtype, kGatedForm, T, desc->inter_features,
                    desc->in_features * esize(desc->dtype))
       .ws_bytes;
 }
@@ -358,7 +321,7 @@ int32_t lora_gated_ffn(const lora_gated_desc* desc, const void* x, const void* w
   if (int32_t e = may(pre, "pre")) return e;
   if (int32_t e = need(out, "out")) return e;
   const int64_t kb = desc->in_features * esize(desc->dtype);
-  const GemmPlan plan = gemm_plan(desc->dtype, true, T, desc->inter_features, kb);
+  const GemmPlan plan = gemm_plan(desc->dtype, kGatedForm, T, desc->inter_features, kb);
   if (int32_t e = check_ws(ws, ws_bytes, plan.ws_bytes)) return e;
   GemmArgs a{};
   a.A = (const char*)x;
@@ -368,12 +331,12 @@ int32_t lora_gated_ffn(const lora_gated_desc* desc, const void* x, const void* w
   a.delta = delta;
   a.pre = pre;
   a.out = out;
-  a.kb = kb;
+  a.kb = a.lda = a.ldb = kb;
   a.M = T;
   a.N = desc->inter_features;
   a.out_dtype = desc->out_dtype;
   a.act = desc->act;
-  return gemm_run(desc->dtype, true, plan, a, ws, (hipStream_t)stream);
+  return gemm_run(desc->dtype, kGatedForm, plan, a, ws, (hipStream_t)stream);
 }
 
 static int32_t check_backward(const lora_gated_desc* desc) {
@@ -391,7 +354,7 @@ int64_t lora_gated_ffn_backward_workspace_bytes(const lora_gated_desc* desc, int
   if (int32_t e = check_backward(desc)) return e;
   if (int32_t e = check_rows(T)) return e;
   if (T == 0) return 0;
-  return backward_layout(*desc, T, need_dx != 0, need_dw != 0).total;
+  return backward_plan(*desc, T, need_dx != 0, need_dw != 0).total;
 }
 
 int32_t lora_gated_ffn_backward(const lora_gated_desc* desc, const void* dout, const void* pre,
@@ -421,7 +384,7 @@ int32_t lora_gated_ffn_backward(const lora_gated_desc* desc, const void* dout, c
   if (dx) {
     if (int32_t e = need(w, "w")) return e;
   }
-  const BackwardLayout b = backward_layout(*desc, T, dx != nullptr, dw != nullptr);
+  const BackwardPlan b = backward_plan(*desc, T, dx != nullptr, dw != nullptr);
   if (int32_t e = check_ws(ws, ws_bytes, b.total)) return e;
 
   const dim3 grid((unsigned)(((int64_t)T * (I / 8) + 255) / 256));
@@ -433,32 +396,26 @@ int32_t lora_gated_ffn_backward(const lora_gated_desc* desc, const void* dout, c
                        (int64_t)T, I, desc->act);
   if (int32_t e = check_launch("gate gradient")) return e;
 
-  char* base = (char*)ws;
   GemmArgs a{};
+  a.A = (const char*)dpre;
+  a.lda = 2 * I * es;
+  a.N = K;
+  a.ldb = K * es;
   a.out_dtype = desc->dtype;
   a.act = LORA_ACT_NONE;
   if (dx) {
-    transpose(desc->dtype, w, base + b.wt, 2 * I, K, 2 * I, st);
-    if (int32_t e = check_launch("transpose")) return e;
-    a.A = (const char*)dpre;
-    a.B = base + b.wt;
+    a.B = (const char*)w;
     a.out = dx;
-    a.kb = 2 * I * es;
     a.M = T;
-    a.N = K;
-    if (int32_t e = gemm_run(desc->dtype, false, b.dx, a, base + b.part, st)) return e;
+    a.kb = 2 * I * es;
+    if (int32_t e = gemm_run(desc->dtype, kGradX, b.dx, a, ws, st)) return e;
   }
   if (dw) {
-    transpose(desc->dtype, dpre, base + b.dt, T, 2 * I, b.ldt, st);
-    transpose(desc->dtype, x, base + b.xt, T, K, b.ldt, st);
-    if (int32_t e = check_launch("transpose")) return e;
-    a.A = base + b.dt;
-    a.B = base + b.xt;
+    a.B = (const char*)x;
     a.out = dw;
-    a.kb = b.ldt * es;
     a.M = 2 * I;
-    a.N = K;
-    if (int32_t e = gemm_run(desc->dtype, false, b.dw, a, base + b.part, st)) return e;
+    a.kb = T * es;
+    if (int32_t e = gemm_run(desc->dtype, kGradW, b.dw, a, ws, st)) return e;
   }
   return LORA_OK;
 }

@@ -27,6 +27,20 @@
 // Rows past the end are clamped to the last row (their results are never
 // stored).  A last step that is partly past the row's end loads chunk 0 there
 // instead and both operands' chunks are zeroed after the LDS read.
+//
+// The gradients sum over what their operands store as rows, so an operand may
+// also be reduction-major (bf16 and fp32): A[k][m], m contiguous.  A step of
+// it is the same number of bytes, 128 / size rows of k; it lies in LDS as it
+// does in memory, and the read turns it into the fragments above:
+//   bf16  ds_read_b64_tr_b16: 16 lanes read four rows of 16 values and lane i
+//         gets column i.  Two a chunk; 32 bytes a row, so the 32-byte units of
+//         a row are permuted by k until the eight rows that 32 lanes read
+//         cover all 64 banks.
+//   fp32  one value is one matrix instruction's word, so a lane reads NT
+//         consecutive columns of one row k and has that word for NT tiles: its
+//         tile i holds column NT l16 + i, and the epilogue puts it back.
+// Transposed copies instead cost 420 us of the 1820 us of the gradients of
+// 4096 rows (4096 x 14336 bf16).
 #pragma once
 
 #include "lora_block.h"
@@ -133,6 +147,89 @@ struct Int {
   static constexpr int value = V;
 };
 
+constexpr int type_size(int dt) { return dt == LORA_F32 ? 4 : dt == LORA_BF16 ? 2 : 1; }
+
+// Which words of chunks g and 4 + g lie before the end of a reduction with
+// `left` bytes in this step.  Rows are whole chunks; a reduction over
+// reduction-major operands alone may end anywhere.
+template <bool kWhole>
+__device__ __forceinline__ void keep_words(int g, int left, bk_u32x4 (&keep)[2]) {
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const int rest = left - (64 * s + 16 * g + (kWhole ? 0 : 4 * w));
+      keep[s][w] = rest >= 4 ? 0xffffffffu : rest > 0 ? 0xffffu : 0u;
+    }
+}
+
+// A reduction-major tile of ROWS columns m: rows of RB bytes, one a k.
+template <int DT, int ROWS>
+struct ColTile {
+  static constexpr int ES = type_size(DT), RB = ROWS * ES;
+  // position of column byte `c` of row k (its own inverse)
+  static __device__ __forceinline__ int swizzle(int c, int k) {
+    if constexpr (DT == LORA_F32) return c ^ (((k >> 2) & 1) << 7);
+    // two rows of 128 bytes or one of 256 cover the banks once
+    if constexpr (RB == 128) return c ^ ((((k >> 1) & 1) | ((k >> 3) & 1) << 1) << 5);
+    return c ^ (((k & 3) | ((k >> 3) & 1) << 2) << 5);
+  }
+  // the fragments of NT tiles from column `col` on (a multiple of 16 NT)
+  template <int NT>
+  static __device__ __forceinline__ void read(const char* tile, int col, int l16, int g,
+                                              bk_u32x4 (&f)[NT][2]) {
+    if constexpr (DT == LORA_F32) {
+      typedef uint32_t vec __attribute__((ext_vector_type(NT)));
+      const int at = swizzle(ES * (col + NT * l16), 4 * g);
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const vec v = *reinterpret_cast<const vec*>(tile + (16 * s + 4 * g + w) * RB + at);
+#pragma unroll
+          for (int i = 0; i < NT; ++i) f[i][s][w] = v[i];
+        }
+    } else {
+      typedef short half4 __attribute__((ext_vector_type(4)));
+      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+      const int k = 8 * g + (l16 >> 2);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const char* at = tile + k * RB + swizzle(ES * (col + 16 * i + 4 * (l16 & 3)), k);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const u32x2 v = __builtin_bit_cast(
+                u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                           (__attribute__((address_space(3))) half4*)(at + (32 * s + 4 * h) * RB)));
+            f[i][s][2 * h] = v[0];
+            f[i][s][2 * h + 1] = v[1];
+          }
+      }
+    }
+  }
+};
+
+// Column (of NT tiles) that index r of tile i is, as the reads above deal them.
+template <int DT, bool kCol, int NT>
+__device__ __forceinline__ int tile_index(int i, int r) {
+  return kCol && DT == LORA_F32 ? NT * r + i : 16 * i + r;
+}
+
+// A wave's products of one row of tiles into its part of LDS.
+template <int DT, bool kBCol, int NT>
+__device__ __forceinline__ void put_row(float* row, int g, const bk_f32x4 (&acc)[NT]) {
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+    if constexpr (kBCol && DT == LORA_F32) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) row[tile_index<DT, kBCol, NT>(j, 4 * g + r)] = acc[j][r];
+    } else {
+      *reinterpret_cast<bk_f32x4*>(row + j * 16 + 4 * g) = acc[j];
+    }
+}
+
 // Eight products of row m: a partial of K split `sp`, or the epilogue.
 template <bool kGated>
 __device__ __forceinline__ void finish8(const GemmArgs& p, int sp, int m, int n, float (&z)[8],
@@ -156,8 +253,13 @@ __device__ __forceinline__ void finish8(const GemmArgs& p, int sp, int m, int n,
 // every wave and stage kt - 1 has been read by every wave, so its place takes
 // the loads of step kt + NST - 1.  The epilogue goes through LDS (a wave's own
 // region) so that it is a rolled loop over whole row pieces.
-template <int DT, bool kGated, int BM, int BN, int WM, int WN, int NST>
+template <int DT, Form kForm, int BM, int BN, int WM, int WN, int NST>
 __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void gemm_ring_kernel(GemmArgs p) {
+  constexpr bool kGated = kForm == kGatedForm, kACol = kForm == kGradW;
+  constexpr bool kBCol = kForm == kGradX || kForm == kGradW;
+  constexpr int ES = type_size(DT);
+  using TileA = ColTile<DT, BM>;
+  using TileB = ColTile<DT, BN>;
   constexpr int NWN = BN / WN, NW = BM / WM * NWN;
   constexpr int STAGE = (BM + BN) * kStepBytes;
   constexpr int P = (BM + BN) / 8 / NW;  // loads a wave makes for a stage
@@ -178,27 +280,56 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void gemm_ring_kernel(Gem
   const int per = (nk_all + p.splits - 1) / p.splits;
   const int k_lo = sp * per, nk = (k_lo + per < nk_all ? k_lo + per : nk_all) - k_lo;
 
+  // a load's lanes: their address at this part's first step and the offset
+  // within the step, which is 0 where a last step has no such chunk or row
   const char* src[P];
-  int chunk[P];
+  uint32_t off[P];
+  int lim[P];
+  const int64_t step_a = kACol ? kStepBytes / ES * p.lda : kStepBytes;
+  const int64_t step_b = kBCol ? kStepBytes / ES * p.ldb : kStepBytes;
 #pragma unroll
   for (int j = 0; j < P; ++j) {
-    const int q = wave * P + j, r = 8 * q + (lane >> 3);
-    chunk[j] = (lane & 7) ^ ((r >> 1) & 7);
-    if (r < BM) {
-      const int m = m0 + r < p.M ? m0 + r : p.M - 1;
-      src[j] = p.A + (int64_t)m * p.kb;
+    const int o = (wave * P + j) * 1024 + lane * 16;
+    if (o < BM * kStepBytes) {
+      if constexpr (kACol) {
+        const int k = o / TileA::RB;
+        int c = TileA::swizzle(o % TileA::RB, k);
+        c = m0 + c / ES < p.M ? c : 0;
+        src[j] = p.A + (int64_t)m0 * ES + c + k_lo * step_a;
+        off[j] = (uint32_t)k * (uint32_t)p.lda;
+        lim[j] = k * ES;
+      } else {
+        const int r = o / kStepBytes;
+        const int m = m0 + r < p.M ? m0 + r : p.M - 1;
+        lim[j] = 16 * ((lane & 7) ^ ((r >> 1) & 7));
+        src[j] = p.A + (int64_t)m * p.lda + k_lo * step_a;
+        off[j] = (uint32_t)lim[j];
+      }
     } else {
-      src[j] = p.B + (int64_t)b_row<kGated, WN>(r - BM, n0, p.N) * p.kb;
+      const int ob = o - BM * kStepBytes;
+      if constexpr (kBCol) {
+        const int k = ob / TileB::RB;
+        int c = TileB::swizzle(ob % TileB::RB, k);
+        c = n0 + c / ES < p.N ? c : 0;
+        src[j] = p.B + (int64_t)n0 * ES + c + k_lo * step_b;
+        off[j] = (uint32_t)k * (uint32_t)p.ldb;
+        lim[j] = k * ES;
+      } else {
+        const int r = ob / kStepBytes;
+        lim[j] = 16 * ((lane & 7) ^ ((r >> 1) & 7));
+        src[j] = p.B + (int64_t)b_row<kGated, WN>(r, n0, p.N) * p.ldb + k_lo * step_b;
+        off[j] = (uint32_t)lim[j];
+      }
     }
   }
   auto issue = [&](int kt, int slot) {
-    const int64_t k = (int64_t)(k_lo + kt) * kStepBytes;
+    const int64_t left = p.kb - (int64_t)(k_lo + kt) * kStepBytes;
 #pragma unroll
     for (int j = 0; j < P; ++j) {
-      int64_t off = k + chunk[j] * 16;
-      off = off < p.kb ? off : 0;
+      const bool of_a = (wave * P + j) * 1024 < BM * kStepBytes;
       __builtin_amdgcn_global_load_lds(
-          (const __attribute__((address_space(1))) void*)(src[j] + off),
+          (const __attribute__((address_space(1))) void*)(src[j] + kt * (of_a ? step_a : step_b) +
+                                                          (lim[j] < left ? off[j] : 0u)),
           (__attribute__((address_space(3))) void*)(lds + slot * STAGE + (wave * P + j) * 1024),
           16, 0, 0);
     }
@@ -224,28 +355,40 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void gemm_ring_kernel(Gem
     barrier();
     if (kt + NST - 1 < nk) issue(kt + NST - 1, slot == 0 ? NST - 1 : slot - 1);
 
-    const char* sA = lds + slot * STAGE + (wr * WM + l16) * kStepBytes;
-    const char* sB = lds + slot * STAGE + (BM + wc * WN + l16) * kStepBytes;
+    const char* stage = lds + slot * STAGE;
     const int c0 = (g ^ (l16 >> 1)) * 16, c1 = c0 ^ 64;
     bk_u32x4 fa[WM / 16][2], fb[WN / 16][2];
+    if constexpr (kACol) {
+      TileA::read(stage, wr * WM, l16, g, fa);
+    } else {
+      const char* sA = stage + (wr * WM + l16) * kStepBytes;
 #pragma unroll
-    for (int i = 0; i < WM / 16; ++i) {
-      fa[i][0] = *reinterpret_cast<const bk_u32x4*>(sA + i * 16 * kStepBytes + c0);
-      fa[i][1] = *reinterpret_cast<const bk_u32x4*>(sA + i * 16 * kStepBytes + c1);
+      for (int i = 0; i < WM / 16; ++i) {
+        fa[i][0] = *reinterpret_cast<const bk_u32x4*>(sA + i * 16 * kStepBytes + c0);
+        fa[i][1] = *reinterpret_cast<const bk_u32x4*>(sA + i * 16 * kStepBytes + c1);
+      }
     }
+    if constexpr (kBCol) {
+      TileB::read(stage + BM * kStepBytes, wc * WN, l16, g, fb);
+    } else {
+      const char* sB = stage + (BM + wc * WN + l16) * kStepBytes;
 #pragma unroll
-    for (int j = 0; j < WN / 16; ++j) {
-      fb[j][0] = *reinterpret_cast<const bk_u32x4*>(sB + j * 16 * kStepBytes + c0);
-      fb[j][1] = *reinterpret_cast<const bk_u32x4*>(sB + j * 16 * kStepBytes + c1);
+      for (int j = 0; j < WN / 16; ++j) {
+        fb[j][0] = *reinterpret_cast<const bk_u32x4*>(sB + j * 16 * kStepBytes + c0);
+        fb[j][1] = *reinterpret_cast<const bk_u32x4*>(sB + j * 16 * kStepBytes + c1);
+      }
     }
     const int64_t left = p.kb - (int64_t)(k_lo + kt) * kStepBytes;
     if (left < kStepBytes) {  // uniform
-      const uint32_t e0 = g * 16 < left ? 0xffffffffu : 0u;
-      const uint32_t e1 = 64 + g * 16 < left ? 0xffffffffu : 0u;
+      bk_u32x4 keep[2];
+      keep_words<!kACol>(g, (int)left, keep);
 #pragma unroll
-      for (int i = 0; i < WM / 16; ++i) fa[i][0] &= e0, fa[i][1] &= e1;
+      for (int s = 0; s < 2; ++s) {
 #pragma unroll
-      for (int j = 0; j < WN / 16; ++j) fb[j][0] &= e0, fb[j][1] &= e1;
+        for (int i = 0; i < WM / 16; ++i) fa[i][s] &= keep[s];
+#pragma unroll
+        for (int j = 0; j < WN / 16; ++j) fb[j][s] &= keep[s];
+      }
     }
 #pragma unroll
     for (int i = 0; i < WM / 16; ++i)
@@ -260,9 +403,7 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void gemm_ring_kernel(Gem
   float* reg = reinterpret_cast<float*>(lds) + wave * WM * LDE;
 #pragma unroll
   for (int i = 0; i < WM / 16; ++i)
-#pragma unroll
-    for (int j = 0; j < WN / 16; ++j)
-      *reinterpret_cast<bk_f32x4*>(reg + (i * 16 + l16) * LDE + j * 16 + 4 * g) = acc[i][j];
+    put_row<DT, kBCol>(reg + tile_index<DT, kACol, WM / 16>(i, l16) * LDE, g, acc[i]);
   __builtin_amdgcn_s_waitcnt(0xC07F);
   asm volatile("" ::: "memory");
   __builtin_amdgcn_wave_barrier();
@@ -310,8 +451,12 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void gemm_ring_kernel(Gem
 // and eight may be outstanding when it leaves a memory slot: those issued
 // before have landed, which are the ones that the next phase reads, and do so
 // for every wave once all have passed the barriers of that slot and the next.
-template <int DT, bool kGated>
+template <int DT, Form kForm>
 __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
+  constexpr bool kGated = kForm == kGatedForm, kACol = kForm == kGradW;
+  constexpr bool kBCol = kForm == kGradX || kForm == kGradW;
+  constexpr int ES = type_size(DT);
+  using Piece = ColTile<DT, 128>;
   constexpr int PIECE = 128 * kStepBytes, BUF = 4 * PIECE;
   constexpr int LDE = 64 + 4;             // floats a row of the epilogue's region
   constexpr int EPI = 8 * 64 * LDE * 4;   // half of every wave's rows at a time
@@ -330,36 +475,57 @@ __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
   const int k_lo = sp * per, nk = (k_lo + per < nk_all ? k_lo + per : nk_all) - k_lo;
   const int tail = (int)(p.kb - (int64_t)(k_lo + nk - 1) * kStepBytes);  // of the last step
 
-  // loads: a wave fills 8-row runs w and w + 8 of every piece, so its lanes
-  // take the same chunk of a row in every load
+  // loads: a wave fills 1 KB runs w and w + 8 of every piece, so the chunk of a
+  // row that a lane takes is the same in every load of a row-major operand
   const int chunk16 = 16 * ((lane & 7) ^ ((wave & 1) * 4 + (lane >> 4)));
-  const char* baseA = p.A + (int64_t)m0 * p.kb + (int64_t)k_lo * kStepBytes;
-  const char* baseB0 = p.B + (int64_t)n0 * p.kb + (int64_t)k_lo * kStepBytes;
-  const char* baseB1 = kGated ? baseB0 + (int64_t)p.N * p.kb : baseB0;
+  const int64_t step_a = kACol ? kStepBytes / ES * p.lda : kStepBytes;
+  const int64_t step_b = kBCol ? kStepBytes / ES * p.ldb : kStepBytes;
+  const char* baseA = p.A + (kACol ? (int64_t)m0 * ES : m0 * p.lda) + k_lo * step_a;
+  const char* baseB0 = p.B + (kBCol ? (int64_t)n0 * ES : n0 * p.ldb) + k_lo * step_b;
+  const char* baseB1 = kGated ? baseB0 + p.N * p.ldb : baseB0;
   uint32_t offA[2][2], offB[2][2];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int r = 8 * (wave + 8 * j) + (lane >> 3);
-      int m = h * 128 + r;
-      m = m0 + m < p.M ? m : p.M - 1 - m0;
+      const int o = 1024 * (wave + 8 * j) + 16 * lane, r = o / kStepBytes, k = o / Piece::RB;
+      const int c = Piece::swizzle(o % Piece::RB, k) / ES;  // first of the chunk's columns
       // linear: a wave's 64 columns are consecutive, 32 from each half of B
-      int n = kGated ? r : (r >> 5) * 64 + h * 32 + (r & 31);
-      n = n0 + n < p.N ? n : p.N - 1 - n0;
-      offA[h][j] = (uint32_t)(m * (int)p.kb);
-      offB[h][j] = (uint32_t)(n * (int)p.kb);
+      int m = h * 128 + (kACol ? c : r), n = kBCol ? c : r;
+      if constexpr (!kGated) n = (n >> 5) * 64 + h * 32 + (n & 31);
+      if constexpr (kACol)
+        offA[h][j] = (uint32_t)((m0 + m < p.M ? m : 0) * ES) + (uint32_t)k * (uint32_t)p.lda;
+      else
+        offA[h][j] = (uint32_t)(m0 + m < p.M ? m : p.M - 1 - m0) * (uint32_t)p.lda + chunk16;
+      if constexpr (kBCol)
+        offB[h][j] = (uint32_t)((n0 + n < p.N ? n : 0) * ES) + (uint32_t)k * (uint32_t)p.ldb;
+      else
+        offB[h][j] = (uint32_t)(n0 + n < p.N ? n : p.N - 1 - n0) * (uint32_t)p.ldb + chunk16;
     }
-  auto fill = [&](const char* base, const uint32_t (&off)[2], int piece, int kt) {
-    // past the end of a row, the step's first chunk (zeroed after the LDS read)
-    const int c = kt == nk - 1 && chunk16 >= tail ? 0 : chunk16;
+  auto fill = [&](auto col, const char* base, int64_t step, int64_t ld, const uint32_t (&off)[2],
+                  int piece, int kt) {
+    constexpr bool kCol = decltype(col)::value;
     char* to = lds + (kt & 1) * BUF + piece * PIECE + wave * 1024;
-    const char* from = base + (int64_t)kt * kStepBytes;
+    const char* from = base + kt * step;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 2; ++j) {
+      // past the end of a row or of the rows, the step's first (zeroed after
+      // the LDS read)
+      const int k = (1024 * (wave + 8 * j) + 16 * lane) / Piece::RB;
+      uint32_t back = 0;
+      if (kt == nk - 1 && (kCol ? k * ES : chunk16) >= tail)
+        back = kCol ? (uint32_t)k * (uint32_t)ld : (uint32_t)chunk16;
       __builtin_amdgcn_global_load_lds(
-          (const __attribute__((address_space(1))) void*)(from + (off[j] + (uint32_t)c)),
+          (const __attribute__((address_space(1))) void*)(from + (off[j] - back)),
           (__attribute__((address_space(3))) void*)(to + j * 8192), 16, 0, 0);
+    }
+  };
+  auto fill_a = [&](int h, int kt) {
+    fill(Int<kACol>{}, baseA, step_a, p.lda, offA[h], h, kt);
+  };
+  auto fill_b = [&](int kt) {
+    fill(Int<kBCol>{}, baseB0, step_b, p.ldb, offB[0], 2, kt);
+    fill(Int<kBCol>{}, baseB1, step_b, p.ldb, offB[1], 3, kt);
   };
 
   bk_f32x4 acc[2][2][4][2];
@@ -376,10 +542,12 @@ __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
   const int c0 = (g ^ (l16 >> 1)) * 16, c1 = c0 ^ 64;
   const char* rdA = lds + (wr * 64 + l16) * kStepBytes;
   const char* rdB = lds + 2 * PIECE + (wc * 32 + l16) * kStepBytes;
-  const uint32_t keep0 = g * 16 < tail ? 0xffffffffu : 0u;
-  const uint32_t keep1 = 64 + g * 16 < tail ? 0xffffffffu : 0u;
 
   auto read_a = [&](int h, int kt) {
+    if constexpr (kACol) {
+      Piece::read(lds + (kt & 1) * BUF + h * PIECE, wr * 64, l16, g, fa);
+      return;
+    }
     const char* s = rdA + (kt & 1) * BUF + h * PIECE;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -388,6 +556,10 @@ __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
     }
   };
   auto read_b = [&](int h, int kt) {
+    if constexpr (kBCol) {
+      Piece::read(lds + (kt & 1) * BUF + (2 + h) * PIECE, wc * 32, l16, g, fb[h]);
+      return;
+    }
     const char* s = rdB + (kt & 1) * BUF + h * PIECE;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -396,6 +568,37 @@ __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
     }
   };
   auto products = [&](int ha) {
+    if constexpr (DT == kE4m3Exact) {
+      // Half a chunk pair at a time, A widened anew for each half of B: all of
+      // the widened fragments at once do not fit in the registers.
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          bk_bf16x8 wb[2][2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              wb[j][q] = widen(fb[hb][j][s][2 * q], fb[hb][j][s][2 * q + 1]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            bk_u32x4 v = fa[i][s];
+            asm volatile("" : "+v"(v));  // (no reuse of the other half's)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const bk_bf16x8 wa = widen(v[2 * q], v[2 * q + 1]);
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                acc[ha][hb][i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    wb[j][q], wa, acc[ha][hb][i][j], 0, 0, 0);
+            }
+          }
+        }
+      __builtin_amdgcn_s_setprio(0);
+      return;
+    }
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -417,44 +620,48 @@ __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
     read_a(0, kt);
     read_b(0, kt);
     read_b(1, kt);
-    if constexpr (kLeft >= 1) fill(baseA, offA[1], 1, kt + 1);
+    if constexpr (kLeft >= 1) fill_a(1, kt + 1);
     __builtin_amdgcn_s_waitcnt(wait_all_lds(kLeft >= 1 ? 8 : 0));
     slot_end();
     if constexpr (kLeft == 0) {
+      bk_u32x4 keep[2];
+      keep_words<!kACol>(g, tail, keep);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) fa[i][0] &= keep0, fa[i][1] &= keep1;
+      for (int s = 0; s < 2; ++s) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+        for (int i = 0; i < 4; ++i) fa[i][s] &= keep[s];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) fb[h][j][0] &= keep0, fb[h][j][1] &= keep1;
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) fb[h][j][s] &= keep[s];
+      }
     }
     products(0);
     slot_end();
 
     read_a(1, kt);
     if constexpr (kLeft >= 2) {
-      fill(baseA, offA[0], 0, kt + 2);
-      fill(baseB0, offB[0], 2, kt + 2);
-      fill(baseB1, offB[1], 3, kt + 2);
+      fill_a(0, kt + 2);
+      fill_b(kt + 2);
     }
     __builtin_amdgcn_s_waitcnt(wait_all_lds(kLeft >= 2 ? 8 : kLeft == 1 ? 2 : 0));
     slot_end();
     if constexpr (kLeft == 0) {
+      bk_u32x4 keep[2];
+      keep_words<!kACol>(g, tail, keep);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) fa[i][0] &= keep0, fa[i][1] &= keep1;
+      for (int i = 0; i < 4; ++i) fa[i][0] &= keep[0], fa[i][1] &= keep[1];
     }
     products(1);
     slot_end();
   };
 
-  fill(baseA, offA[0], 0, 0);
-  fill(baseB0, offB[0], 2, 0);
-  fill(baseB1, offB[1], 3, 0);
-  fill(baseA, offA[1], 1, 0);
+  fill_a(0, 0);
+  fill_b(0);
+  fill_a(1, 0);
   if (nk > 1) {
-    fill(baseA, offA[0], 0, 1);
-    fill(baseB0, offB[0], 2, 1);
-    fill(baseB1, offB[1], 3, 1);
+    fill_a(0, 1);
+    fill_b(1);
     __builtin_amdgcn_s_waitcnt(wait_vm(8));
   } else {
     __builtin_amdgcn_s_waitcnt(wait_vm(2));
@@ -479,10 +686,8 @@ __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
     for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          *reinterpret_cast<bk_f32x4*>(reg + (i * 16 + l16) * LDE + hb * 32 + j * 16 + 4 * g) =
-              acc[h][hb][i][j];
+        put_row<DT, kBCol>(reg + tile_index<DT, kACol, 4>(i, l16) * LDE + hb * 32, g,
+                           acc[h][hb][i]);
     __builtin_amdgcn_s_waitcnt(0xC07F);
     asm volatile("" ::: "memory");
     __builtin_amdgcn_wave_barrier();
@@ -508,33 +713,38 @@ __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
   }
 }
 
-template <int DT, bool kGated, int BM, int BN, int WM, int WN, int NST>
+template <int DT, Form kForm, int BM, int BN, int WM, int WN, int NST>
 void launch_ring(const GemmArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((gemm_ring_kernel<DT, kGated, BM, BN, WM, WN, NST>),
+  hipLaunchKernelGGL((gemm_ring_kernel<DT, kForm, BM, BN, WM, WN, NST>),
                      dim3(a.tiles_m * a.tiles_n * a.splits), dim3(BM / WM * (BN / WN) * 64), 0, st,
                      a);
 }
 
-template <int DT>
-int32_t launch(bool gated, int shape, const GemmArgs& a, hipStream_t st) {
-  if (shape == 0) {
-    if (gated)
-      launch_ring<DT, true, 64, 64, 16, 64, 4>(a, st);
-    else
-      launch_ring<DT, false, 64, 64, 32, 32, 4>(a, st);
-  } else if (shape == 1) {
-    if (gated)
-      launch_ring<DT, true, 128, 128, 64, 64, 3>(a, st);
-    else
-      launch_ring<DT, false, 128, 128, 64, 64, 3>(a, st);
-  } else {
-    const dim3 grid(a.tiles_m * a.tiles_n * a.splits);
-    if (gated)
-      hipLaunchKernelGGL((gemm_phase_kernel<DT, true>), grid, dim3(512), 0, st, a);
-    else
-      hipLaunchKernelGGL((gemm_phase_kernel<DT, false>), grid, dim3(512), 0, st, a);
-  }
+template <int DT, Form kForm>
+int32_t launch_form(int shape, const GemmArgs& a, hipStream_t st) {
+  // gated: a wave has 64 rows of B, 32 columns' gate and up rows
+  if (shape == 0)
+    launch_ring<DT, kForm, 64, 64, kForm == kGatedForm ? 16 : 32, kForm == kGatedForm ? 64 : 32,
+                4>(a, st);
+  else if (shape == 1)
+    launch_ring<DT, kForm, 128, 128, 64, 64, 3>(a, st);
+  else
+    hipLaunchKernelGGL((gemm_phase_kernel<DT, kForm>), dim3(a.tiles_m * a.tiles_n * a.splits),
+                       dim3(512), 0, st, a);
   return check_launch("product");
+}
+
+// the forms of the forward pass, and those of the gradients
+template <int DT>
+int32_t launch(Form form, int shape, const GemmArgs& a, hipStream_t st) {
+  return form == kGatedForm ? launch_form<DT, kGatedForm>(shape, a, st)
+                            : launch_form<DT, kLinearForm>(shape, a, st);
+}
+template <int DT>
+int32_t launch_any(Form form, int shape, const GemmArgs& a, hipStream_t st) {
+  if (form == kGradX) return launch_form<DT, kGradX>(shape, a, st);
+  if (form == kGradW) return launch_form<DT, kGradW>(shape, a, st);
+  return launch<DT>(form, shape, a, st);
 }
 
 }  // namespace gemm

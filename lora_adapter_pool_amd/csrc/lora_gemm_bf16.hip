@@ -3,8 +3,8 @@
 
 namespace lora {
 
-int32_t gemm_launch_bf16(bool gated, int shape, const GemmArgs& a, hipStream_t st) {
-  return gemm::launch<LORA_BF16>(gated, shape, a, st);
+int32_t gemm_launch_bf16(Form form, int shape, const GemmArgs& a, hipStream_t st) {
+  return gemm::launch_any<LORA_BF16>(form, shape, a, st);
 }
 
 }  // namespace lora

@@ -3,8 +3,8 @@
 
 namespace lora {
 
-int32_t gemm_launch_f32(bool gated, int shape, const GemmArgs& a, hipStream_t st) {
-  return gemm::launch<LORA_F32>(gated, shape, a, st);
+int32_t gemm_launch_f32(Form form, int shape, const GemmArgs& a, hipStream_t st) {
+  return gemm::launch_any<LORA_F32>(form, shape, a, st);
 }
 
 }  // namespace lora

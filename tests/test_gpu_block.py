@@ -339,6 +339,51 @@ def test_backward_sizes(dtype, T):
         _check_backward(T, K, I, dtype, "silu", 10 * T + k, inplace=k == 1)
 
 
+@pytest.mark.parametrize("plan", SHAPES)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_backward_every_shape(dtype, plan, monkeypatch):
+    monkeypatch.setenv("LORA_GEMM_PLAN", plan)
+    for k, (T, K, I) in enumerate(((1, 8, 8), (31, 264, 136), (257, 520, 264), (600, 304, 72),
+                                   (67, 72, 520))):
+        _check_backward(T, K, I, dtype, "silu", 30 + k)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_backward_exact_integers(dtype):
+    # relu over positive gates: dpre, and with it every product, is whole
+    for T, K, I in ((3, 136, 72), (129, 264, 392), (1031, 520, 648)):
+        g = gen(T)
+        whole = lambda *s: torch.randint(-2, 3, s, generator=g, device="cuda").to(  # noqa: E731
+            TORCH[dtype])
+        x, w, dout = whole(T, K), whole(2 * I, K), whole(T, I)
+        pre = torch.cat([whole(T, I).abs() + 1, whole(T, I)], 1)
+        dpre, gx, gw = run_backward(dout, pre, x, w, "relu", dtype)
+        d = dout.double()
+        want = torch.cat([d * pre[:, I:].double(), d * pre[:, :I].double()], 1)
+        assert torch.equal(dpre.double(), want)
+        assert torch.equal(gx, (want @ w.double()).to(TORCH[dtype]))
+        assert torch.equal(gw, (want.t().contiguous() @ x.double()).to(TORCH[dtype]))
+
+
+def test_backward_rows_past_the_end_stay_out():
+    # the reduction over the tokens ends inside a step; what lies behind it in
+    # memory is not a number
+    for dtype in ("bf16", "f32"):
+        for T in (5, 70):
+            K, I = 72, 40
+            g = gen(T)
+            buf = lambda n: torch.full((T + 70, n), float("nan"), dtype=TORCH[dtype],  # noqa: E731
+                                       device="cuda")
+            x, pre, dout = buf(K), buf(2 * I), buf(I)
+            for t in (x, pre, dout):
+                t[:T] = normal(g, t[:T].shape, dtype)
+            w = normal(g, (2 * I, K), dtype)
+            dpre = buf(2 * I)
+            _, gx, gw = run_backward(dout[:T], pre[:T], x[:T], w, "silu", dtype, dpre=dpre[:T])
+            assert torch.isfinite(gx).all() and torch.isfinite(gw).all()
+            assert torch.isnan(dpre[T:]).all()
+
+
 @pytest.mark.parametrize("act", ["none", "silu", "gelu", "gelu_tanh", "relu"])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_backward_activations(dtype, act):
