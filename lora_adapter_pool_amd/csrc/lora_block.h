@@ -30,12 +30,12 @@ struct GemmArgs {
   const void* residual;   // [M][N], or nullptr
   void* pre;              // gated: [M][2 N], or nullptr
   void* out;              // [M][N]
-  float* part;            // split K: [splits][M][ldp] raw products, or nullptr
+  float* part;            // split K: [tiles - whole][splits][bm][bn] raw products
   int64_t kb;             // bytes of the reduction
   int64_t lda, ldb;       // bytes from a stored row to the next (multiples of 16)
   int32_t M, N;
-  int32_t ldp;            // floats a row of `part`
-  int32_t splits;
+  int32_t whole;          // tiles that are not split: the first ones
+  int32_t splits;         // parts of each other tile
   int32_t out_dtype;      // of bias, delta, residual, pre and out
   int32_t act;
   int32_t tiles_m, tiles_n;
@@ -48,7 +48,8 @@ constexpr int kStepBytes = 128;
 // Launch plan of a product: tile shape and K split, from sizes and types alone.
 struct GemmPlan {
   int32_t shape;   // index of a tile shape
-  int32_t splits;
+  int32_t whole;   // tiles that are not split
+  int32_t splits;  // parts of each of the others
   int64_t ws_bytes;  // fp32 partials
 };
 GemmPlan gemm_plan(int32_t dtype, Form form, int64_t M, int64_t N, int64_t kb);
@@ -209,13 +210,63 @@ __device__ __forceinline__ void store8(void* base, int64_t i, int left, int dtyp
   }
 }
 
-// The epilogue on eight raw products of row m, columns n .. n + 8 (n < N).
+// What an epilogue reads beside the products, for eight columns of a row: it
+// is fetched for several rows before the first of them is finished, so that
+// one latency is waited for and not one a row.  bf16 outputs only (a fetch of
+// fp32 would take twice the registers).
 template <bool kGated>
-__device__ __forceinline__ void epilogue8(const GemmArgs& p, int m, int n, float (&z)[8],
-                                          float (&u)[8]) {
+struct Extra {
+  bk_u32x4 d[kGated ? 2 : 1], r;
+};
+
+__device__ __forceinline__ bk_u32x4 load8_raw(const void* base, int64_t i, int left) {
+  const uint16_t* p = (const uint16_t*)base + i;
+  if (left >= 8) return *reinterpret_cast<const bk_u32x4_a2*>(p);
+  bk_u32x4 w = {0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < left) w[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+  return w;
+}
+
+template <bool kGated>
+__device__ __forceinline__ void fetch_extra(const GemmArgs& p, int m, int n, Extra<kGated>& x) {
+  if (m >= p.M || n >= p.N) return;
   const int left = p.N - n;
+  if constexpr (kGated) {
+    const int64_t at = (int64_t)m * 2 * p.N + n;
+    if (p.delta) {
+      x.d[0] = load8_raw(p.delta, at, left);
+      x.d[1] = load8_raw(p.delta, at + p.N, left);
+    }
+  } else {
+    const int64_t at = (int64_t)m * p.N + n;
+    if (p.delta) x.d[0] = load8_raw(p.delta, at, left);
+    if (p.residual) x.r = load8_raw(p.residual, at, left);
+  }
+}
+
+__device__ __forceinline__ void add8(float (&z)[8], const bk_u32x4& w) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) z[2 * j] += bk_lo(w[j]), z[2 * j + 1] += bk_hi(w[j]);
+}
+__device__ __forceinline__ void add8(float (&z)[8], const void* base, int64_t i, int left,
+                                     int dtype) {
   float t[8];
+  load8(base, i, left, dtype, t);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) z[j] += t[j];
+}
+
+// The epilogue on eight raw products of row m, columns n .. n + 8 (n < N);
+// kFetched: bf16 outputs, delta and residual already in `x`.
+template <bool kGated, bool kFetched>
+__device__ __forceinline__ void epilogue8(const GemmArgs& p, int m, int n, float (&z)[8],
+                                          float (&u)[8], const Extra<kGated>& x) {
+  const int left = p.N - n;
+  const int od = kFetched ? (int)LORA_BF16 : p.out_dtype;
   if (p.sa) {
+    float t[8];
     const float s = p.sa[m];
     load8(p.sb, n, left, LORA_F32, t);
 #pragma unroll
@@ -229,41 +280,56 @@ __device__ __forceinline__ void epilogue8(const GemmArgs& p, int m, int n, float
   if constexpr (kGated) {
     const int64_t at = (int64_t)m * 2 * p.N + n;
     if (p.delta) {
-      load8(p.delta, at, left, p.out_dtype, t);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) z[j] += t[j];
-      load8(p.delta, at + p.N, left, p.out_dtype, t);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] += t[j];
+      if constexpr (kFetched) {
+        add8(z, x.d[0]);
+        add8(u, x.d[1]);
+      } else {
+        add8(z, p.delta, at, left, od);
+        add8(u, p.delta, at + p.N, left, od);
+      }
     }
     if (p.pre) {
-      store8(p.pre, at, left, p.out_dtype, z);
-      store8(p.pre, at + p.N, left, p.out_dtype, u);
+      store8(p.pre, at, left, od, z);
+      store8(p.pre, at + p.N, left, od, u);
     }
     act_apply(p.act, z);
 #pragma unroll
     for (int j = 0; j < 8; ++j) z[j] *= u[j];
-    store8(p.out, (int64_t)m * p.N + n, left, p.out_dtype, z);
+    store8(p.out, (int64_t)m * p.N + n, left, od, z);
   } else {
     const int64_t at = (int64_t)m * p.N + n;
-    if (p.bias) {
-      load8(p.bias, n, left, p.out_dtype, t);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) z[j] += t[j];
-    }
+    if (p.bias) add8(z, p.bias, n, left, od);
     if (p.delta) {
-      load8(p.delta, at, left, p.out_dtype, t);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) z[j] += t[j];
+      if constexpr (kFetched)
+        add8(z, x.d[0]);
+      else
+        add8(z, p.delta, at, left, od);
     }
     act_apply(p.act, z);
     if (p.residual) {
-      load8(p.residual, at, left, p.out_dtype, t);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) z[j] += t[j];
+      if constexpr (kFetched)
+        add8(z, x.r);
+      else
+        add8(z, p.residual, at, left, od);
     }
-    store8(p.out, at, left, p.out_dtype, z);
+    store8(p.out, at, left, od, z);
   }
+}
+
+// Workgroup -> XCD: workgroups are dealt round-robin to the 8 XCDs, each with
+// an L2 of its own; XCD x takes the x-th contiguous eighth of `total` items.
+__device__ __forceinline__ int xcd_item(int b, int total) {
+  const int q = total >> 3, r = total & 7, x = b & 7;
+  return x * q + (x < r ? x : r) + (b >> 3);
+}
+// Tiles go in groups of 8 row tiles, columns outside, so that the workgroups
+// that run together share rows of A and of B.
+__device__ __forceinline__ void tile_place(const GemmArgs& p, int id, int& tm, int& tn) {
+  const int gsz = 8 * p.tiles_n, g = id / gsz, first = 8 * g;
+  const int rows = p.tiles_m - first < 8 ? p.tiles_m - first : 8;
+  id -= g * gsz;
+  tm = first + id % rows;
+  tn = id / rows;
 }
 
 #endif  // __HIPCC__

@@ -27,36 +27,41 @@ int64_t esize(int32_t dtype) { return dtype == LORA_F32 ? 4 : dtype == LORA_BF16
 
 // ---------------------------------------------------------------- products
 
-// Sums the K splits' partials in their order and applies the epilogue, eight
-// columns a thread.
+// Sums the partials of the split tiles in the order of K and applies the
+// epilogue, eight columns a thread.
 template <bool kGated>
-__global__ __launch_bounds__(256) void join_kernel(GemmArgs p) {
-  const int per = (p.N + 7) / 8;
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (id >= (int64_t)p.M * per) return;
-  const int m = (int)(id / per), n = (int)(id % per) * 8;
+__global__ __launch_bounds__(256) void join_kernel(GemmArgs p, int bm, int bn) {
+  const int cols = kGated ? bn / 2 : bn, per = cols / 8;
+  const int id = blockIdx.x * 256 + threadIdx.x;  // bm * per is a multiple of 256
+  const int tile = id / (bm * per), in = id - tile * (bm * per);
+  const int r = in / per, c = (in - r * per) * 8;
+  int tm, tn;
+  tile_place(p, p.whole + tile, tm, tn);
+  const int m = tm * bm + r, n = tn * cols + c;
+  if (m >= p.M || n >= p.N) return;
   float z[8], u[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) z[j] = 0.f, u[j] = 0.f;
-  for (int s = 0; s < p.splits; ++s) {
-    const float* d = p.part + ((int64_t)s * p.M + m) * p.ldp + n;
+  const float* d = p.part + (int64_t)tile * p.splits * (bm * bn) + r * bn + c;
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s, d += bm * bn) {
     float t[8];
     load8(d, 0, 8, LORA_F32, t);
 #pragma unroll
     for (int j = 0; j < 8; ++j) z[j] += t[j];
     if constexpr (kGated) {
-      load8(d, p.N, 8, LORA_F32, t);
+      load8(d, bn / 2, 8, LORA_F32, t);
 #pragma unroll
       for (int j = 0; j < 8; ++j) u[j] += t[j];
     }
   }
-  epilogue8<kGated>(p, m, n, z, u);
+  epilogue8<kGated, false>(p, m, n, z, u, Extra<kGated>{});
 }
 
 }  // namespace
 
 GemmPlan gemm_plan(int32_t dtype, Form form, int64_t M, int64_t N, int64_t kb) {
-  GemmPlan g{0, 1, 0};
+  GemmPlan g{0, 0, 1, 0};
   const int64_t width = form == kGatedForm ? 2 * N : N;  // rows of B
   auto tiles = [&](int s) {
     return ((M + kShapes[s].bm - 1) / kShapes[s].bm) *
@@ -65,11 +70,7 @@ GemmPlan gemm_plan(int32_t dtype, Form form, int64_t M, int64_t N, int64_t kb) {
   // the large tile where it gives every compute unit one
   g.shape = tiles(2) >= kComputeUnits ? 2 : tiles(1) >= kComputeUnits ? 1 : 0;
   const int64_t steps = (kb + kStepBytes - 1) / kStepBytes;
-  const int64_t t = tiles(g.shape);
-  // a K split where the tiles leave compute units idle: up to two workgroups a
-  // unit, at least eight steps a part
-  int64_t s = std::max<int64_t>(1, std::min<int64_t>(2 * kComputeUnits / t, steps / 8));
-  s = std::min<int64_t>(s, 16);
+  int64_t s = 0;
   if (const char* e = std::getenv("LORA_GEMM_PLAN")) {  // tuning override: shape,splits
     char* end = nullptr;
     const long shape = std::strtol(e, &end, 10);
@@ -78,12 +79,20 @@ GemmPlan gemm_plan(int32_t dtype, Form form, int64_t M, int64_t N, int64_t kb) {
       g.shape = (int32_t)shape;
     if (parts >= 1 && parts <= 64) s = std::min<int64_t>(parts, steps);
   }
-  if (s > 1) {
+  // whole rounds of tiles, one a compute unit, are not split; the tiles of the
+  // last round are, where they leave compute units idle
+  const int64_t t = tiles(g.shape), rest = t % kComputeUnits;
+  if (s == 0 && rest) s = std::min<int64_t>({kComputeUnits / rest, steps / 8, 16});
+  if (s > 1 && rest) {
     const int64_t per = (steps + s - 1) / s;
     s = (steps + per - 1) / per;  // no part is empty
   }
-  g.splits = (int32_t)s;
-  if (s > 1) g.ws_bytes = s * M * ((width + 7) / 8 * 8) * 4;
+  g.whole = (int32_t)t;
+  if (s > 1 && rest) {
+    g.splits = (int32_t)s;
+    g.whole = (int32_t)(t - rest);
+    g.ws_bytes = rest * s * kShapes[g.shape].bm * kShapes[g.shape].bn * 4;
+  }
   return g;
 }
 
@@ -94,19 +103,19 @@ int32_t gemm_run(int32_t dtype, Form form, const GemmPlan& plan, GemmArgs a, voi
   const int width = gated ? 2 * a.N : a.N;
   a.tiles_m = (a.M + sh.bm - 1) / sh.bm;
   a.tiles_n = (width + sh.bn - 1) / sh.bn;
+  a.whole = plan.whole;
   a.splits = plan.splits;
-  a.part = plan.splits > 1 ? (float*)ws : nullptr;
-  a.ldp = (width + 7) / 8 * 8;
+  a.part = (float*)ws;
   int32_t e = dtype == LORA_BF16   ? gemm_launch_bf16(form, plan.shape, a, st)
               : dtype == LORA_E4M3 ? gemm_launch_e4m3(form, plan.shape, a, st)
                                    : gemm_launch_f32(form, plan.shape, a, st);
   if (e || plan.splits == 1) return e;
-  const int64_t threads = (int64_t)a.M * ((a.N + 7) / 8);
-  const dim3 grid((unsigned)((threads + 255) / 256));
+  const int rest = a.tiles_m * a.tiles_n - a.whole;
+  const dim3 grid((unsigned)(rest * (sh.bm * (gated ? sh.bn / 2 : sh.bn) / 8 / 256)));
   if (gated)
-    hipLaunchKernelGGL(join_kernel<true>, grid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL(join_kernel<true>, grid, dim3(256), 0, st, a, sh.bm, sh.bn);
   else
-    hipLaunchKernelGGL(join_kernel<false>, grid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL(join_kernel<false>, grid, dim3(256), 0, st, a, sh.bm, sh.bn);
   return check_launch("join of the K splits");
 }
 

@@ -109,22 +109,20 @@ __device__ __forceinline__ void barrier() {
   asm volatile("" ::: "memory");
 }
 
-// Workgroup id -> tile.  Workgroups are dealt round-robin to the 8 XCDs, each
-// with an L2 of its own: XCD x takes the x-th contiguous eighth of the tiles.
-// Within it tiles go in groups of 8 row tiles, columns outside, so that the
-// workgroups that run together share rows of A and of B.
-__device__ __forceinline__ void tile_of(const GemmArgs& p, int b, int& tm, int& tn, int& sp) {
-  const int total = p.tiles_m * p.tiles_n * p.splits;
-  const int q = total >> 3, r = total & 7, x = b & 7;
-  int id = x * q + (x < r ? x : r) + (b >> 3);
-  const int per = p.tiles_m * p.tiles_n;
-  sp = id / per;
-  id -= sp * per;
-  const int gsz = 8 * p.tiles_n, g = id / gsz, first = 8 * g;
-  const int rows = p.tiles_m - first < 8 ? p.tiles_m - first : 8;
-  id -= g * gsz;
-  tm = first + id % rows;
-  tn = id / rows;
+// Workgroup -> tile and K part.  The whole tiles come first (their number is a
+// multiple of 8 unless all are whole), then the parts of the others.
+__device__ __forceinline__ void tile_of(const GemmArgs& p, int b, int& tm, int& tn, int& tile,
+                                        int& sp) {
+  const int rest = p.tiles_m * p.tiles_n - p.whole;
+  sp = 0;
+  if (b < p.whole) {
+    tile = xcd_item(b, p.whole);
+  } else {
+    const int id = xcd_item(b - p.whole, rest * p.splits);
+    sp = id / rest;
+    tile = p.whole + id - sp * rest;
+  }
+  tile_place(p, tile, tm, tn);
 }
 
 // Global row of B that LDS row `r` of a tile holds.  gated: a wave's WN rows
@@ -230,21 +228,69 @@ __device__ __forceinline__ void put_row(float* row, int g, const bk_f32x4 (&acc)
     }
 }
 
-// Eight products of row m: a partial of K split `sp`, or the epilogue.
-template <bool kGated>
-__device__ __forceinline__ void finish8(const GemmArgs& p, int sp, int m, int n, float (&z)[8],
-                                        float (&u)[8]) {
-  if (p.part) {
-    float* d = p.part + ((int64_t)sp * p.M + m) * p.ldp + n;
-    *reinterpret_cast<bk_f32x4*>(d) = bk_f32x4{z[0], z[1], z[2], z[3]};
-    *reinterpret_cast<bk_f32x4*>(d + 4) = bk_f32x4{z[4], z[5], z[6], z[7]};
-    if constexpr (kGated) {
-      d += p.N;
-      *reinterpret_cast<bk_f32x4*>(d) = bk_f32x4{u[0], u[1], u[2], u[3]};
-      *reinterpret_cast<bk_f32x4*>(d + 4) = bk_f32x4{u[4], u[5], u[6], u[7]};
+// The rows of a wave's products, from its part of LDS (row-major, LDE floats a
+// row) to the partials or through the epilogue.  ROWS rows from m on, COLS
+// output columns from n on (gated: the up products lie COLS to the right);
+// row and col are the wave's place in the tile of BM x BN.
+template <bool kGated, int BM, int BN, int ROWS, int COLS, int LDE>
+__device__ __forceinline__ void finish_rows(const GemmArgs& p, const float* reg, int lane, int m,
+                                            int n, int tile, int sp, int row, int col) {
+  constexpr int LPR = COLS / 8;   // lanes a row
+  constexpr int RPI = 64 / LPR;   // rows an iteration
+  constexpr int NI = ROWS / RPI > 0 ? ROWS / RPI : 1;
+  constexpr int GRP = NI < 4 ? NI : 4;
+  const int r0 = lane / LPR, c = lane % LPR * 8;
+  n += c;
+  auto get = [&](int r, float (&z)[8], float (&u)[8]) {
+    const float* from = reg + r * LDE + c;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bk_f32x4 v = *reinterpret_cast<const bk_f32x4*>(from + 4 * h);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) z[4 * h + j] = v[j];
+      if constexpr (kGated) {
+        const bk_f32x4 w = *reinterpret_cast<const bk_f32x4*>(from + COLS + 4 * h);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[4 * h + j] = w[j];
+      }
+    }
+  };
+  if (tile >= p.whole) {
+    float* to = p.part + (int64_t)((tile - p.whole) * p.splits + sp) * (BM * BN);
+    for (int r = r0; r < ROWS; r += RPI) {
+      if (m + r >= p.M || n >= p.N) continue;
+      float z[8], u[8];
+      get(r, z, u);
+      float* d = to + (row + r) * BN + col + c;
+      *reinterpret_cast<bk_f32x4*>(d) = bk_f32x4{z[0], z[1], z[2], z[3]};
+      *reinterpret_cast<bk_f32x4*>(d + 4) = bk_f32x4{z[4], z[5], z[6], z[7]};
+      if constexpr (kGated) {
+        d += BN / 2;
+        *reinterpret_cast<bk_f32x4*>(d) = bk_f32x4{u[0], u[1], u[2], u[3]};
+        *reinterpret_cast<bk_f32x4*>(d + 4) = bk_f32x4{u[4], u[5], u[6], u[7]};
+      }
+    }
+  } else if (p.out_dtype == LORA_BF16) {
+    for (int i0 = 0; i0 < NI; i0 += GRP) {
+      Extra<kGated> x[GRP];
+#pragma unroll
+      for (int i = 0; i < GRP; ++i) fetch_extra<kGated>(p, m + r0 + (i0 + i) * RPI, n, x[i]);
+#pragma unroll
+      for (int i = 0; i < GRP; ++i) {
+        const int r = r0 + (i0 + i) * RPI;
+        if (r >= ROWS || m + r >= p.M || n >= p.N) continue;
+        float z[8], u[8];
+        get(r, z, u);
+        epilogue8<kGated, true>(p, m + r, n, z, u, x[i]);
+      }
     }
   } else {
-    epilogue8<kGated>(p, m, n, z, u);
+    for (int r = r0; r < ROWS; r += RPI) {
+      if (m + r >= p.M || n >= p.N) continue;
+      float z[8], u[8];
+      get(r, z, u);
+      epilogue8<kGated, false>(p, m + r, n, z, u, Extra<kGated>{});
+    }
   }
 }
 
@@ -269,15 +315,15 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void gemm_ring_kernel(Gem
   constexpr int BYTES = STAGE * NST > EPI ? STAGE * NST : EPI;
   __shared__ __align__(1024) char lds[BYTES];
 
-  int tm, tn, sp;
-  tile_of(p, blockIdx.x, tm, tn, sp);
+  int tm, tn, tile, sp;
+  tile_of(p, blockIdx.x, tm, tn, tile, sp);
   const int m0 = tm * BM, n0 = tn * (kGated ? BN / 2 : BN);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
 
   const int nk_all = (int)((p.kb + kStepBytes - 1) / kStepBytes);
-  const int per = (nk_all + p.splits - 1) / p.splits;
+  const int per = tile < p.whole ? nk_all : (nk_all + p.splits - 1) / p.splits;
   const int k_lo = sp * per, nk = (k_lo + per < nk_all ? k_lo + per : nk_all) - k_lo;
 
   // a load's lanes: their address at this part's first step and the offset
@@ -409,27 +455,8 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void gemm_ring_kernel(Gem
   __builtin_amdgcn_wave_barrier();
 
   constexpr int WCOLS = kGated ? WN / 2 : WN;  // output columns of a wave
-  constexpr int LPR = WCOLS / 8;               // lanes a row
-  constexpr int RPI = 64 / LPR;                // rows an iteration
-  const int col = (lane % LPR) * 8, n = n0 + wc * WCOLS + col;
-  for (int r = lane / LPR; r < WM; r += RPI) {
-    const int m = m0 + wr * WM + r;
-    if (m >= p.M || n >= p.N) continue;
-    float z[8], u[8];
-    const float* row = reg + r * LDE + col;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const bk_f32x4 v = *reinterpret_cast<const bk_f32x4*>(row + 4 * h);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) z[4 * h + j] = v[j];
-      if constexpr (kGated) {
-        const bk_f32x4 w = *reinterpret_cast<const bk_f32x4*>(row + WN / 2 + 4 * h);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) u[4 * h + j] = w[j];
-      }
-    }
-    finish8<kGated>(p, sp, m, n, z, u);
-  }
+  finish_rows<kGated, BM, BN, WM, WCOLS, LDE>(p, reg, lane, m0 + wr * WM, n0 + wc * WCOLS, tile,
+                                              sp, wr * WM, wc * WCOLS);
 }
 
 // The large product: a 256 x 256 tile, 8 waves of 128 x 64 (two a SIMD), and
@@ -462,8 +489,8 @@ __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
   constexpr int EPI = 8 * 64 * LDE * 4;   // half of every wave's rows at a time
   __shared__ __align__(1024) char lds[EPI > 2 * BUF ? EPI : 2 * BUF];
 
-  int tm, tn, sp;
-  tile_of(p, blockIdx.x, tm, tn, sp);
+  int tm, tn, tile, sp;
+  tile_of(p, blockIdx.x, tm, tn, tile, sp);
   const int m0 = tm * 256, n0 = tn * (kGated ? 128 : 256);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -471,7 +498,7 @@ __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
   const int wr = wave >> 2, wc = wave & 3;
 
   const int nk_all = (int)((p.kb + kStepBytes - 1) / kStepBytes);
-  const int per = (nk_all + p.splits - 1) / p.splits;
+  const int per = tile < p.whole ? nk_all : (nk_all + p.splits - 1) / p.splits;
   const int k_lo = sp * per, nk = (k_lo + per < nk_all ? k_lo + per : nk_all) - k_lo;
   const int tail = (int)(p.kb - (int64_t)(k_lo + nk - 1) * kStepBytes);  // of the last step
 
@@ -676,9 +703,7 @@ __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
 
   // epilogue: 64 rows of every wave at a time through its own part of LDS
   float* reg = reinterpret_cast<float*>(lds) + wave * 64 * LDE;
-  constexpr int LPR = kGated ? 4 : 8, RPI = 64 / LPR;
-  const int col = (lane % LPR) * 8;
-  const int n = n0 + wc * (kGated ? 32 : 64) + col;
+  constexpr int WCOLS = kGated ? 32 : 64;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     barrier();  // (all waves are past their LDS reads; the pass before is read)
@@ -691,24 +716,9 @@ __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
     __builtin_amdgcn_s_waitcnt(0xC07F);
     asm volatile("" ::: "memory");
     __builtin_amdgcn_wave_barrier();
-    for (int r = lane / LPR; r < 64; r += RPI) {
-      const int m = m0 + h * 128 + wr * 64 + r;
-      if (m >= p.M || n >= p.N) continue;
-      float z[8], u[8];
-      const float* row = reg + r * LDE + col;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const bk_f32x4 v = *reinterpret_cast<const bk_f32x4*>(row + 4 * q);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) z[4 * q + j] = v[j];
-        if constexpr (kGated) {
-          const bk_f32x4 w = *reinterpret_cast<const bk_f32x4*>(row + 32 + 4 * q);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) u[4 * q + j] = w[j];
-        }
-      }
-      finish8<kGated>(p, sp, m, n, z, u);
-    }
+    finish_rows<kGated, 256, 256, 64, WCOLS, LDE>(p, reg, lane, m0 + h * 128 + wr * 64,
+                                                  n0 + wc * WCOLS, tile, sp, h * 128 + wr * 64,
+                                                  wc * WCOLS);
     __builtin_amdgcn_s_waitcnt(0xC07F);
   }
 }
@@ -716,7 +726,7 @@ __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
 template <int DT, Form kForm, int BM, int BN, int WM, int WN, int NST>
 void launch_ring(const GemmArgs& a, hipStream_t st) {
   hipLaunchKernelGGL((gemm_ring_kernel<DT, kForm, BM, BN, WM, WN, NST>),
-                     dim3(a.tiles_m * a.tiles_n * a.splits), dim3(BM / WM * (BN / WN) * 64), 0, st,
+                     dim3(a.whole + (a.tiles_m * a.tiles_n - a.whole) * a.splits), dim3(BM / WM * (BN / WN) * 64), 0, st,
                      a);
 }
 
@@ -729,7 +739,7 @@ int32_t launch_form(int shape, const GemmArgs& a, hipStream_t st) {
   else if (shape == 1)
     launch_ring<DT, kForm, 128, 128, 64, 64, 3>(a, st);
   else
-    hipLaunchKernelGGL((gemm_phase_kernel<DT, kForm>), dim3(a.tiles_m * a.tiles_n * a.splits),
+    hipLaunchKernelGGL((gemm_phase_kernel<DT, kForm>), dim3(a.whole + (a.tiles_m * a.tiles_n - a.whole) * a.splits),
                        dim3(512), 0, st, a);
   return check_launch("product");
 }
