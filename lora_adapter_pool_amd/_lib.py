@@ -187,9 +187,10 @@ _pycall = None
 
 def pycall():
     """The CPython binding of the per-call entry points (module _lora_call:
-    apply, apply_ranked, apply_device and the decoder-block operators), built beside the library; raise if it
-    was not built.  Each function takes the entry point's address (see
-    entry_address) and then that entry point's arguments as Python ints."""
+    apply, apply_ranked, apply_device and the decoder-block operators), built
+    beside the library; raise if it was not built.  Each function takes the
+    entry point's address (see entry_address) and then that entry point's
+    arguments: ints, tensors or numpy arrays for pointers, None for NULL."""
     global _pycall
     if _pycall is None:
         try:
@@ -248,10 +249,24 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
+def _current_stream() -> int:
+    """The current stream's handle.  torch.cuda.current_stream() builds a Python
+    object for it (2.5 us, more than a small kernel's launch); the raw handle is
+    0.3 us."""
+    global _raw_stream
+    import torch
+    if _raw_stream is None:
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return _raw_stream(torch.cuda.current_device())
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -524,8 +539,8 @@ def make_gated_desc(dtype: str, out_dtype: str, in_features: int, inter_features
 def lora_add_rms_norm(desc, x, residual, weight, sum, out, out8, scale, T, stream=None) -> None:
     """sum = x + residual; out = rms_norm(sum) * weight; out8 / scale the same in e4m3."""
     _check(pycall().add_rms_norm(entry_address("lora_add_rms_norm"), ctypes.addressof(desc),
-                                 _ptr(x), _ptr(residual), _ptr(weight), _ptr(sum), _ptr(out),
-                                 _ptr(out8), _ptr(scale), int(T), _stream(stream)))
+                                 x, residual, weight, sum, out,
+                                 out8, scale, T, _stream(stream)))
 
 
 def lora_linear_workspace_bytes(desc, T: int) -> int:
@@ -535,9 +550,9 @@ def lora_linear_workspace_bytes(desc, T: int) -> int:
 def lora_linear(desc, x, w, x_scale, w_scale, bias, delta, residual, out, T, ws, ws_bytes,
                 stream=None) -> None:
     """out = act(x_scale w_scale x W^T + bias + delta) + residual."""
-    _check(pycall().linear(entry_address("lora_linear"), ctypes.addressof(desc), _ptr(x), _ptr(w),
-                           _ptr(x_scale), _ptr(w_scale), _ptr(bias), _ptr(delta), _ptr(residual),
-                           _ptr(out), int(T), _ptr(ws), int(ws_bytes), _stream(stream)))
+    _check(pycall().linear(entry_address("lora_linear"), ctypes.addressof(desc), x, w,
+                           x_scale, w_scale, bias, delta, residual,
+                           out, T, ws, ws_bytes, _stream(stream)))
 
 
 def lora_gated_ffn_workspace_bytes(desc, T: int) -> int:
@@ -547,9 +562,9 @@ def lora_gated_ffn_workspace_bytes(desc, T: int) -> int:
 def lora_gated_ffn(desc, x, w, x_scale, w_scale, delta, pre, out, T, ws, ws_bytes,
                    stream=None) -> None:
     """pre = x_scale w_scale x W^T + delta; out = act(gate half of pre) * (up half)."""
-    _check(pycall().gated_ffn(entry_address("lora_gated_ffn"), ctypes.addressof(desc), _ptr(x),
-                              _ptr(w), _ptr(x_scale), _ptr(w_scale), _ptr(delta), _ptr(pre),
-                              _ptr(out), int(T), _ptr(ws), int(ws_bytes), _stream(stream)))
+    _check(pycall().gated_ffn(entry_address("lora_gated_ffn"), ctypes.addressof(desc), x,
+                              w, x_scale, w_scale, delta, pre,
+                              out, T, ws, ws_bytes, _stream(stream)))
 
 
 def lora_gated_ffn_backward_workspace_bytes(desc, T: int, need_dx: bool = True,
@@ -562,6 +577,6 @@ def lora_gated_ffn_backward(desc, dout, pre, x, w, dpre, dx, dw, T, ws, ws_bytes
                             stream=None) -> None:
     """Gradients of lora_gated_ffn from the pre it kept (dx and dw may be None)."""
     _check(pycall().gated_ffn_backward(entry_address("lora_gated_ffn_backward"),
-                                       ctypes.addressof(desc), _ptr(dout), _ptr(pre), _ptr(x),
-                                       _ptr(w), _ptr(dpre), _ptr(dx), _ptr(dw), int(T), _ptr(ws),
+                                       ctypes.addressof(desc), dout, pre, x,
+                                       w, dpre, dx, dw, int(T), ws,
                                        int(ws_bytes), _stream(stream)))

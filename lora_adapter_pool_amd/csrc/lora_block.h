@@ -52,7 +52,8 @@ struct GemmPlan {
   int32_t splits;  // parts of each of the others
   int64_t ws_bytes;  // fp32 partials
 };
-GemmPlan gemm_plan(int32_t dtype, Form form, int64_t M, int64_t N, int64_t kb);
+GemmPlan gemm_plan(int32_t dtype, int32_t out_dtype, Form form, int64_t M, int64_t N,
+                   int64_t kb);
 int32_t gemm_run(int32_t dtype, Form form, const GemmPlan& plan, GemmArgs a, void* ws,
                  hipStream_t st);
 // per type (each in its own source file)
@@ -63,8 +64,9 @@ int32_t gemm_launch_f32(Form form, int shape, const GemmArgs& a, hipStream_t st)
 struct TileShape {
   int bm, bn;  // rows of A and rows of B a workgroup covers
 };
-// shapes, smallest first: two of gemm_ring_kernel, then gemm_phase_kernel's
-constexpr TileShape kShapes[] = {{64, 64}, {128, 128}, {256, 256}};
+// shapes, smallest first: three of gemm_ring_kernel, then gemm_phase_kernel's
+constexpr int kNumShapes = 4;
+constexpr TileShape kShapes[kNumShapes] = {{32, 32}, {64, 64}, {128, 128}, {256, 256}};
 
 int32_t check_launch(const char* what);
 

@@ -32,8 +32,9 @@ int64_t esize(int32_t dtype) { return dtype == LORA_F32 ? 4 : dtype == LORA_BF16
 template <bool kGated>
 __global__ __launch_bounds__(256) void join_kernel(GemmArgs p, int bm, int bn) {
   const int cols = kGated ? bn / 2 : bn, per = cols / 8;
-  const int id = blockIdx.x * 256 + threadIdx.x;  // bm * per is a multiple of 256
+  const int id = blockIdx.x * 256 + threadIdx.x;
   const int tile = id / (bm * per), in = id - tile * (bm * per);
+  if (tile >= p.tiles_m * p.tiles_n - p.whole) return;
   const int r = in / per, c = (in - r * per) * 8;
   int tm, tn;
   tile_place(p, p.whole + tile, tm, tn);
@@ -60,40 +61,93 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs p, int bm, int bn) {
 
 }  // namespace
 
-GemmPlan gemm_plan(int32_t dtype, Form form, int64_t M, int64_t N, int64_t kb) {
-  GemmPlan g{0, 0, 1, 0};
+namespace {
+
+// What a workgroup of a tile shape takes, in microseconds: a start and an end,
+// and a step of kStepBytes, where few compute units run and where all do.
+// Fitted to 1300 times of products of 1 to 8960 rows and 256 to 14336 columns
+// and terms under every shape and split (rms error 7 to 15%).  Of those the
+// plan that the model picks is on average 2 to 3% slower than the best; the
+// largest shape that fills the compute units, else a split that does, was 18%
+// slower in bf16 (700 x 14336 x 4096: 178 us against 86).
+struct ShapeCost {
+  float start, step_few, step_all;
+};
+constexpr ShapeCost kCosts[4][kNumShapes] = {
+    {{1.9f, 0.26f, 0.53f}, {1.8f, 0.65f, 1.15f}, {2.2f, 2.15f, 2.15f}, {3.4f, 7.0f, 7.0f}},   // fp32
+    {{1.4f, 0.22f, 0.30f}, {2.1f, 0.32f, 0.41f}, {3.6f, 0.64f, 0.70f}, {6.3f, 0.81f, 1.40f}},  // bf16
+    // e4m3 with bf16 outputs, with fp32 outputs
+    {{1.7f, 0.21f, 0.30f}, {2.4f, 0.31f, 0.41f}, {4.2f, 0.64f, 0.71f}, {7.0f, 0.79f, 1.46f}},
+    {{1.4f, 0.27f, 0.45f}, {2.3f, 0.42f, 0.63f}, {3.5f, 1.04f, 1.15f}, {5.2f, 3.20f, 3.50f}}};
+constexpr float kJoinStart = 2.4f;        // a second launch
+constexpr float kJoinPart = 0.15f;        // a part of a tile
+constexpr float kJoinPerByte = 0.26e-6f;  // partials written and read again
+
+constexpr int64_t kMaxPartials = 64 << 20;  // bytes
+
+// `n` workgroups of `steps` steps.  A compute unit holds three of the smallest
+// shape, two of the next and one of the others; the last round is cheaper the
+// fewer it has.
+float round_time(const ShapeCost& c, int shape, int64_t n, int64_t steps) {
+  const int64_t cap = (shape < 2 ? 3 - shape : 1) * kComputeUnits;
+  const int64_t full = n / cap, rest = n % cap;
+  float us = full * (c.start + steps * c.step_all);
+  if (rest) {
+    const float idle = shape < 2 ? 128.f : 0.f;  // alone on its unit, or nearly
+    const float load = std::max(0.f, rest - idle) / (cap - idle);
+    us += c.start + steps * (c.step_few + (c.step_all - c.step_few) * load);
+  }
+  return us;
+}
+
+}  // namespace
+
+GemmPlan gemm_plan(int32_t dtype, int32_t out_dtype, Form form, int64_t M, int64_t N,
+                   int64_t kb) {
   const int64_t width = form == kGatedForm ? 2 * N : N;  // rows of B
-  auto tiles = [&](int s) {
-    return ((M + kShapes[s].bm - 1) / kShapes[s].bm) *
-           ((width + kShapes[s].bn - 1) / kShapes[s].bn);
-  };
-  // the large tile where it gives every compute unit one
-  g.shape = tiles(2) >= kComputeUnits ? 2 : tiles(1) >= kComputeUnits ? 1 : 0;
   const int64_t steps = (kb + kStepBytes - 1) / kStepBytes;
-  int64_t s = 0;
-  if (const char* e = std::getenv("LORA_GEMM_PLAN")) {  // tuning override: shape,splits
+  const int type = dtype == LORA_E4M3 && out_dtype == LORA_F32 ? 3 : dtype;
+  int only_shape = -1, only_parts = 0;
+  if (const char* e = std::getenv("LORA_GEMM_PLAN")) {  // tuning override: shape,parts
     char* end = nullptr;
     const long shape = std::strtol(e, &end, 10);
     const long parts = *end == ',' ? std::strtol(end + 1, nullptr, 10) : 0;
-    if (shape >= 0 && shape < (long)(sizeof(kShapes) / sizeof(kShapes[0])))
-      g.shape = (int32_t)shape;
-    if (parts >= 1 && parts <= 64) s = std::min<int64_t>(parts, steps);
+    if (shape >= 0 && shape < kNumShapes) only_shape = (int)shape;
+    if (parts >= 1 && parts <= 64) only_parts = (int)parts;
   }
-  // whole rounds of tiles, one a compute unit, are not split; the tiles of the
-  // last round are, where they leave compute units idle
-  const int64_t t = tiles(g.shape), rest = t % kComputeUnits;
-  if (s == 0 && rest) s = std::min<int64_t>({kComputeUnits / rest, steps / 8, 16});
-  if (s > 1 && rest) {
-    const int64_t per = (steps + s - 1) / s;
-    s = (steps + per - 1) / per;  // no part is empty
+  GemmPlan best{};
+  float best_us = 0.f;
+  for (int shape = 0; shape < kNumShapes; ++shape) {
+    if (only_shape >= 0 && shape != only_shape) continue;
+    const TileShape& sh = kShapes[shape];
+    const ShapeCost& c = kCosts[type][shape];
+    const int64_t t = ((M + sh.bm - 1) / sh.bm) * ((width + sh.bn - 1) / sh.bn);
+    // Whole rounds of tiles, one a compute unit, are not split; the tiles of the
+    // last round may be, where they leave compute units idle.
+    const int64_t rest = t % kComputeUnits;
+    for (int64_t s = 1; s <= 16; ++s) {
+      const int64_t want = only_parts ? only_parts : s;
+      const int64_t per = (steps + want - 1) / want, parts = (steps + per - 1) / per;
+      GemmPlan g{shape, (int32_t)t, 1, 0};
+      float us = 0.f;
+      if (parts > 1 && rest) {
+        const int64_t bytes = rest * parts * sh.bm * sh.bn * 4;
+        if (bytes > kMaxPartials && !only_parts) break;
+        g = {shape, (int32_t)(t - rest), (int32_t)parts, bytes};
+        us = round_time(c, shape, t - rest, steps) + round_time(c, shape, rest * parts, per) +
+             kJoinStart + parts * kJoinPart + bytes * kJoinPerByte;
+        us *= 1.03f;  // (a tie goes to one launch)
+      } else {
+        us = round_time(c, shape, t, steps);
+      }
+      if (best_us == 0.f || us < best_us) {
+        best = g;
+        best_us = us;
+      }
+      if (only_parts || rest == 0 || rest * s > 4 * kComputeUnits) break;
+    }
   }
-  g.whole = (int32_t)t;
-  if (s > 1 && rest) {
-    g.splits = (int32_t)s;
-    g.whole = (int32_t)(t - rest);
-    g.ws_bytes = rest * s * kShapes[g.shape].bm * kShapes[g.shape].bn * 4;
-  }
-  return g;
+  return best;
 }
 
 int32_t gemm_run(int32_t dtype, Form form, const GemmPlan& plan, GemmArgs a, void* ws,
@@ -111,7 +165,7 @@ int32_t gemm_run(int32_t dtype, Form form, const GemmPlan& plan, GemmArgs a, voi
                                    : gemm_launch_f32(form, plan.shape, a, st);
   if (e || plan.splits == 1) return e;
   const int rest = a.tiles_m * a.tiles_n - a.whole;
-  const dim3 grid((unsigned)(rest * (sh.bm * (gated ? sh.bn / 2 : sh.bn) / 8 / 256)));
+  const dim3 grid((unsigned)((rest * (sh.bm * (gated ? sh.bn / 2 : sh.bn) / 8) + 255) / 256));
   if (gated)
     hipLaunchKernelGGL(join_kernel<true>, grid, dim3(256), 0, st, a, sh.bm, sh.bn);
   else
@@ -165,11 +219,11 @@ BackwardPlan backward_plan(const lora_gated_desc& d, int64_t T, bool dx, bool dw
   BackwardPlan b{};
   const int64_t e = esize(d.dtype), K = d.in_features, I2 = 2 * (int64_t)d.inter_features;
   if (dx) {
-    b.dx = gemm_plan(d.dtype, kGradX, T, K, e * I2);
+    b.dx = gemm_plan(d.dtype, d.dtype, kGradX, T, K, e * I2);
     b.total = std::max(b.total, b.dx.ws_bytes);
   }
   if (dw) {
-    b.dw = gemm_plan(d.dtype, kGradW, I2, K, e * T);
+    b.dw = gemm_plan(d.dtype, d.dtype, kGradW, I2, K, e * T);
     b.total = std::max(b.total, b.dw.ws_bytes);
   }
   return b;
@@ -266,7 +320,7 @@ int64_t lora_linear_workspace_bytes(const lora_linear_desc* desc, int32_t T) {
   if (int32_t e = check_linear(desc)) return e;
   if (int32_t e = check_rows(T)) return e;
   if (T == 0) return 0;
-  return gemm_plan(desc->dtype, kLinearForm, T, desc->out_features,
+  return gemm_plan(desc->dtype, desc->out_dtype, kLinearForm, T, desc->out_features,
                    desc->in_features * esize(desc->dtype))
       .ws_bytes;
 }
@@ -287,7 +341,7 @@ int32_t lora_linear(const lora_linear_desc* desc, const void* x, const void* w,
   if (int32_t e = may(residual, "residual")) return e;
   if (int32_t e = need(out, "out")) return e;
   const int64_t kb = desc->in_features * esize(desc->dtype);
-  const GemmPlan plan = gemm_plan(desc->dtype, kLinearForm, T, desc->out_features, kb);
+  const GemmPlan plan = gemm_plan(desc->dtype, desc->out_dtype, kLinearForm, T, desc->out_features, kb);
   if (int32_t e = check_ws(ws, ws_bytes, plan.ws_bytes)) return e;
   GemmArgs a{};
   a.A = (const char*)x;
@@ -311,7 +365,7 @@ int64_t lora_gated_ffn_workspace_bytes(const lora_gated_desc* desc, int32_t T) {
   if (int32_t e = check_gated(desc)) return e;
   if (int32_t e = check_rows(T)) return e;
   if (T == 0) return 0;
-  return gemm_plan(desc->dtype, kGatedForm, T, desc->inter_features,
+  return gemm_plan(desc->dtype, desc->out_dtype, kGatedForm, T, desc->inter_features,
                    desc->in_features * esize(desc->dtype))
       .ws_bytes;
 }
@@ -330,7 +384,7 @@ int32_t lora_gated_ffn(const lora_gated_desc* desc, const void* x, const void* w
   if (int32_t e = may(pre, "pre")) return e;
   if (int32_t e = need(out, "out")) return e;
   const int64_t kb = desc->in_features * esize(desc->dtype);
-  const GemmPlan plan = gemm_plan(desc->dtype, kGatedForm, T, desc->inter_features, kb);
+  const GemmPlan plan = gemm_plan(desc->dtype, desc->out_dtype, kGatedForm, T, desc->inter_features, kb);
   if (int32_t e = check_ws(ws, ws_bytes, plan.ws_bytes)) return e;
   GemmArgs a{};
   a.A = (const char*)x;

@@ -25,8 +25,8 @@
 // permutation is made by the lane's choice of its global chunk.
 //
 // Rows past the end are clamped to the last row (their results are never
-// stored).  A last step that is partly past the row's end loads chunk 0 there
-// instead and both operands' chunks are zeroed after the LDS read.
+// stored).  What a step has past the end of the reduction is loaded from 16
+// bytes of zeros instead: no masks, and nothing of the next row can come in.
 //
 // The gradients sum over what their operands store as rows, so an operand may
 // also be reduction-major (bf16 and fp32): A[k][m], m contiguous.  A step of
@@ -147,28 +147,25 @@ struct Int {
 
 constexpr int type_size(int dt) { return dt == LORA_F32 ? 4 : dt == LORA_BF16 ? 2 : 1; }
 
-// Which words of chunks g and 4 + g lie before the end of a reduction with
-// `left` bytes in this step.  Rows are whole chunks; a reduction over
-// reduction-major operands alone may end anywhere.
-template <bool kWhole>
-__device__ __forceinline__ void keep_words(int g, int left, bk_u32x4 (&keep)[2]) {
-#pragma unroll
-  for (int s = 0; s < 2; ++s)
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const int rest = left - (64 * s + 16 * g + (kWhole ? 0 : 4 * w));
-      keep[s][w] = rest >= 4 ? 0xffffffffu : rest > 0 ? 0xffffu : 0u;
-    }
+// Loaded in place of what lies past the end of the reduction.
+static __device__ const uint32_t kZeros[4] __attribute__((aligned(16))) = {0, 0, 0, 0};
+
+__device__ __forceinline__ void load_lds(const char* from, bool past, char* to) {
+  from = past ? reinterpret_cast<const char*>(kZeros) : from;
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                   (__attribute__((address_space(3))) void*)to, 16, 0, 0);
 }
 
 // A reduction-major tile of ROWS columns m: rows of RB bytes, one a k.
 template <int DT, int ROWS>
 struct ColTile {
   static constexpr int ES = type_size(DT), RB = ROWS * ES;
+  static_assert(DT == LORA_F32 ? RB >= 128 : RB == 64 || RB == 128 || RB == 256, "");
   // position of column byte `c` of row k (its own inverse)
   static __device__ __forceinline__ int swizzle(int c, int k) {
-    if constexpr (DT == LORA_F32) return c ^ (((k >> 2) & 1) << 7);
-    // two rows of 128 bytes or one of 256 cover the banks once
+    if constexpr (DT == LORA_F32) return c ^ (((k >> 2) & 1) << (RB == 128 ? 6 : 7));
+    // four rows of 64 bytes, two of 128 or one of 256 cover the banks once
+    if constexpr (RB == 64) return c ^ (((k >> 3) & 1) << 5);
     if constexpr (RB == 128) return c ^ ((((k >> 1) & 1) | ((k >> 3) & 1) << 1) << 5);
     return c ^ (((k & 3) | ((k >> 3) & 1) << 2) << 5);
   }
@@ -326,11 +323,10 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void gemm_ring_kernel(Gem
   const int per = tile < p.whole ? nk_all : (nk_all + p.splits - 1) / p.splits;
   const int k_lo = sp * per, nk = (k_lo + per < nk_all ? k_lo + per : nk_all) - k_lo;
 
-  // a load's lanes: their address at this part's first step and the offset
-  // within the step, which is 0 where a last step has no such chunk or row
+  // a load's lanes: their address at this part's first step, and how many bytes
+  // of the reduction lie before theirs in the step
   const char* src[P];
-  uint32_t off[P];
-  int lim[P];
+  int before[P];
   const int64_t step_a = kACol ? kStepBytes / ES * p.lda : kStepBytes;
   const int64_t step_b = kBCol ? kStepBytes / ES * p.ldb : kStepBytes;
 #pragma unroll
@@ -341,15 +337,13 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void gemm_ring_kernel(Gem
         const int k = o / TileA::RB;
         int c = TileA::swizzle(o % TileA::RB, k);
         c = m0 + c / ES < p.M ? c : 0;
-        src[j] = p.A + (int64_t)m0 * ES + c + k_lo * step_a;
-        off[j] = (uint32_t)k * (uint32_t)p.lda;
-        lim[j] = k * ES;
+        src[j] = p.A + (int64_t)m0 * ES + c + k_lo * step_a + k * p.lda;
+        before[j] = k * ES;
       } else {
         const int r = o / kStepBytes;
         const int m = m0 + r < p.M ? m0 + r : p.M - 1;
-        lim[j] = 16 * ((lane & 7) ^ ((r >> 1) & 7));
-        src[j] = p.A + (int64_t)m * p.lda + k_lo * step_a;
-        off[j] = (uint32_t)lim[j];
+        before[j] = 16 * ((lane & 7) ^ ((r >> 1) & 7));
+        src[j] = p.A + (int64_t)m * p.lda + k_lo * step_a + before[j];
       }
     } else {
       const int ob = o - BM * kStepBytes;
@@ -357,14 +351,12 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void gemm_ring_kernel(Gem
         const int k = ob / TileB::RB;
         int c = TileB::swizzle(ob % TileB::RB, k);
         c = n0 + c / ES < p.N ? c : 0;
-        src[j] = p.B + (int64_t)n0 * ES + c + k_lo * step_b;
-        off[j] = (uint32_t)k * (uint32_t)p.ldb;
-        lim[j] = k * ES;
+        src[j] = p.B + (int64_t)n0 * ES + c + k_lo * step_b + k * p.ldb;
+        before[j] = k * ES;
       } else {
         const int r = ob / kStepBytes;
-        lim[j] = 16 * ((lane & 7) ^ ((r >> 1) & 7));
-        src[j] = p.B + (int64_t)b_row<kGated, WN>(r, n0, p.N) * p.ldb + k_lo * step_b;
-        off[j] = (uint32_t)lim[j];
+        before[j] = 16 * ((lane & 7) ^ ((r >> 1) & 7));
+        src[j] = p.B + (int64_t)b_row<kGated, WN>(r, n0, p.N) * p.ldb + k_lo * step_b + before[j];
       }
     }
   }
@@ -373,11 +365,8 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void gemm_ring_kernel(Gem
 #pragma unroll
     for (int j = 0; j < P; ++j) {
       const bool of_a = (wave * P + j) * 1024 < BM * kStepBytes;
-      __builtin_amdgcn_global_load_lds(
-          (const __attribute__((address_space(1))) void*)(src[j] + kt * (of_a ? step_a : step_b) +
-                                                          (lim[j] < left ? off[j] : 0u)),
-          (__attribute__((address_space(3))) void*)(lds + slot * STAGE + (wave * P + j) * 1024),
-          16, 0, 0);
+      load_lds(src[j] + kt * (of_a ? step_a : step_b), before[j] >= left,
+               lds + slot * STAGE + (wave * P + j) * 1024);
     }
   };
 
@@ -422,18 +411,6 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void gemm_ring_kernel(Gem
       for (int j = 0; j < WN / 16; ++j) {
         fb[j][0] = *reinterpret_cast<const bk_u32x4*>(sB + j * 16 * kStepBytes + c0);
         fb[j][1] = *reinterpret_cast<const bk_u32x4*>(sB + j * 16 * kStepBytes + c1);
-      }
-    }
-    const int64_t left = p.kb - (int64_t)(k_lo + kt) * kStepBytes;
-    if (left < kStepBytes) {  // uniform
-      bk_u32x4 keep[2];
-      keep_words<!kACol>(g, (int)left, keep);
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-#pragma unroll
-        for (int i = 0; i < WM / 16; ++i) fa[i][s] &= keep[s];
-#pragma unroll
-        for (int j = 0; j < WN / 16; ++j) fb[j][s] &= keep[s];
       }
     }
 #pragma unroll
@@ -529,30 +506,23 @@ __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
       else
         offB[h][j] = (uint32_t)(n0 + n < p.N ? n : p.N - 1 - n0) * (uint32_t)p.ldb + chunk16;
     }
-  auto fill = [&](auto col, const char* base, int64_t step, int64_t ld, const uint32_t (&off)[2],
-                  int piece, int kt) {
+  auto fill = [&](auto col, const char* base, int64_t step, const uint32_t (&off)[2], int piece,
+                  int kt) {
     constexpr bool kCol = decltype(col)::value;
     char* to = lds + (kt & 1) * BUF + piece * PIECE + wave * 1024;
     const char* from = base + kt * step;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      // past the end of a row or of the rows, the step's first (zeroed after
-      // the LDS read)
-      const int k = (1024 * (wave + 8 * j) + 16 * lane) / Piece::RB;
-      uint32_t back = 0;
-      if (kt == nk - 1 && (kCol ? k * ES : chunk16) >= tail)
-        back = kCol ? (uint32_t)k * (uint32_t)ld : (uint32_t)chunk16;
-      __builtin_amdgcn_global_load_lds(
-          (const __attribute__((address_space(1))) void*)(from + (off[j] - back)),
-          (__attribute__((address_space(3))) void*)(to + j * 8192), 16, 0, 0);
+      const int before = kCol ? (1024 * (wave + 8 * j) + 16 * lane) / Piece::RB * ES : chunk16;
+      load_lds(from + off[j], kt == nk - 1 && before >= tail, to + j * 8192);
     }
   };
   auto fill_a = [&](int h, int kt) {
-    fill(Int<kACol>{}, baseA, step_a, p.lda, offA[h], h, kt);
+    fill(Int<kACol>{}, baseA, step_a, offA[h], h, kt);
   };
   auto fill_b = [&](int kt) {
-    fill(Int<kBCol>{}, baseB0, step_b, p.ldb, offB[0], 2, kt);
-    fill(Int<kBCol>{}, baseB1, step_b, p.ldb, offB[1], 3, kt);
+    fill(Int<kBCol>{}, baseB0, step_b, offB[0], 2, kt);
+    fill(Int<kBCol>{}, baseB1, step_b, offB[1], 3, kt);
   };
 
   bk_f32x4 acc[2][2][4][2];
@@ -596,31 +566,30 @@ __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
   };
   auto products = [&](int ha) {
     if constexpr (DT == kE4m3Exact) {
-      // Half a chunk pair at a time, A widened anew for each half of B: all of
+      // Eight values at a time, A widened anew for each half of B: all of
       // the widened fragments at once do not fit in the registers.
       __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          bk_bf16x8 wb[2][2];
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int q = 0; q < 2; ++q) {
+            bk_bf16x8 wb[2];
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-              wb[j][q] = widen(fb[hb][j][s][2 * q], fb[hb][j][s][2 * q + 1]);
+            for (int j = 0; j < 2; ++j)
+              wb[j] = widen(fb[hb][j][s][2 * q], fb[hb][j][s][2 * q + 1]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            bk_u32x4 v = fa[i][s];
-            asm volatile("" : "+v"(v));  // (no reuse of the other half's)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const bk_bf16x8 wa = widen(v[2 * q], v[2 * q + 1]);
+            for (int i = 0; i < 4; ++i) {
+              uint32_t lo = fa[i][s][2 * q], hi = fa[i][s][2 * q + 1];
+              asm volatile("" : "+v"(lo), "+v"(hi));  // (no reuse of the other half's)
+              const bk_bf16x8 wa = widen(lo, hi);
 #pragma unroll
               for (int j = 0; j < 2; ++j)
                 acc[ha][hb][i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    wb[j][q], wa, acc[ha][hb][i][j], 0, 0, 0);
+                    wb[j], wa, acc[ha][hb][i][j], 0, 0, 0);
             }
+            __builtin_amdgcn_sched_barrier(0);
           }
         }
       __builtin_amdgcn_s_setprio(0);
@@ -650,19 +619,6 @@ __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
     if constexpr (kLeft >= 1) fill_a(1, kt + 1);
     __builtin_amdgcn_s_waitcnt(wait_all_lds(kLeft >= 1 ? 8 : 0));
     slot_end();
-    if constexpr (kLeft == 0) {
-      bk_u32x4 keep[2];
-      keep_words<!kACol>(g, tail, keep);
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) fa[i][s] &= keep[s];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) fb[h][j][s] &= keep[s];
-      }
-    }
     products(0);
     slot_end();
 
@@ -673,12 +629,6 @@ __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
     }
     __builtin_amdgcn_s_waitcnt(wait_all_lds(kLeft >= 2 ? 8 : kLeft == 1 ? 2 : 0));
     slot_end();
-    if constexpr (kLeft == 0) {
-      bk_u32x4 keep[2];
-      keep_words<!kACol>(g, tail, keep);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) fa[i][0] &= keep[0], fa[i][1] &= keep[1];
-    }
     products(1);
     slot_end();
   };
@@ -732,15 +682,18 @@ void launch_ring(const GemmArgs& a, hipStream_t st) {
 
 template <int DT, Form kForm>
 int32_t launch_form(int shape, const GemmArgs& a, hipStream_t st) {
-  // gated: a wave has 64 rows of B, 32 columns' gate and up rows
+  // gated: a wave's rows of B are the gate and the up rows of the same columns
+  constexpr bool kGated = kForm == kGatedForm;
   if (shape == 0)
-    launch_ring<DT, kForm, 64, 64, kForm == kGatedForm ? 16 : 32, kForm == kGatedForm ? 64 : 32,
-                4>(a, st);
+    launch_ring<DT, kForm, 32, 32, 16, kGated ? 32 : 16, 6>(a, st);
   else if (shape == 1)
+    launch_ring<DT, kForm, 64, 64, kGated ? 16 : 32, kGated ? 64 : 32, 4>(a, st);
+  else if (shape == 2)
     launch_ring<DT, kForm, 128, 128, 64, 64, 3>(a, st);
-  else
-    hipLaunchKernelGGL((gemm_phase_kernel<DT, kForm>), dim3(a.whole + (a.tiles_m * a.tiles_n - a.whole) * a.splits),
-                       dim3(512), 0, st, a);
+  else {
+    const dim3 grid(a.whole + (a.tiles_m * a.tiles_n - a.whole) * a.splits);
+    hipLaunchKernelGGL((gemm_phase_kernel<DT, kForm>), grid, dim3(512), 0, st, a);
+  }
   return check_launch("product");
 }
 

@@ -1,6 +1,6 @@
 /* CPython binding of the per-call entry points (lora_apply, lora_apply_ranked,
- * lora_apply_device and the decoder-block operators): argument marshalling only.  A serving loop calls one of
- * these once per layer and step; through ctypes the conversion of their 14 to
+ * lora_apply_device and the decoder-block operators): argument marshalling
+ * only.  A serving loop calls one of these once per layer and step; through ctypes the conversion of their 14 to
  * 16 arguments costs more host time than the library's own plan for a small
  * decode batch, and the host then paces the GPU.  Here each argument is one
  * integer conversion.
@@ -9,8 +9,8 @@
  * point's address (ctypes.cast(lib.lora_apply, c_void_p).value) as its first
  * argument and calls through a pointer of the entry point's own type, so this
  * module links nothing and cannot bind a second copy of the library.  Pointer
- * arguments are Python ints (None is NULL); the return value is the entry
- * point's status.  The GIL is released around the call, as ctypes does. */
+ * arguments are Python ints, tensors or numpy arrays (None is NULL); the return
+ * value is the entry point's status.  The GIL is released around the call, as ctypes does. */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <stdint.h>
@@ -57,6 +57,36 @@ _Static_assert(__builtin_types_compatible_p(__typeof__(&lora_apply_device), appl
 /* kinds of argument */
 enum { P = 0, I32 = 1, I64 = 2 };
 
+static PyObject* name_data_ptr; /* "data_ptr", interned */
+
+/* An address: None is NULL, an int stands for itself, a tensor for its
+ * data_ptr(), a numpy array for its ctypes.data.  Sets *v; returns 0, or -1
+ * with a Python exception set. */
+static int address(PyObject* a, uint64_t* v) {
+  PyObject* n = NULL;
+  if (a == Py_None) {
+    *v = 0;
+    return 0;
+  }
+  if (PyLong_Check(a)) {
+    Py_INCREF(a);
+    n = a;
+  } else {
+    n = PyObject_CallMethodNoArgs(a, name_data_ptr);
+    if (!n && PyErr_ExceptionMatches(PyExc_AttributeError)) {
+      PyErr_Clear();
+      PyObject* c = PyObject_GetAttrString(a, "ctypes");
+      if (!c) return -1;
+      n = PyObject_GetAttrString(c, "data");
+      Py_DECREF(c);
+    }
+    if (!n) return -1;
+  }
+  *v = PyLong_AsUnsignedLongLong(n);
+  Py_DECREF(n);
+  return *v == (uint64_t)-1 && PyErr_Occurred() ? -1 : 0;
+}
+
 /* Converts args[0 .. n) by kind into out[]; returns 0, or -1 with a Python
  * exception set. */
 static int convert(PyObject* const* args, Py_ssize_t nargs, const char* name, const int* kinds,
@@ -68,13 +98,7 @@ static int convert(PyObject* const* args, Py_ssize_t nargs, const char* name, co
   for (int i = 0; i < n; ++i) {
     PyObject* a = args[i];
     if (kinds[i] == P) {
-      if (a == Py_None) {
-        out[i] = 0;
-        continue;
-      }
-      const unsigned long long v = PyLong_AsUnsignedLongLong(a);
-      if (v == (unsigned long long)-1 && PyErr_Occurred()) return -1;
-      out[i] = v;
+      if (address(a, &out[i])) return -1;
     } else {
       const long long v = PyLong_AsLongLong(a);
       if (v == -1 && PyErr_Occurred()) return -1;
@@ -240,4 +264,7 @@ static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_lora_call",
                                     "CPython binding of the per-call entry points", -1, methods,
                                     NULL, NULL, NULL, NULL};
 
-PyMODINIT_FUNC PyInit__lora_call(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__lora_call(void) {
+  name_data_ptr = PyUnicode_InternFromString("data_ptr");
+  return name_data_ptr ? PyModule_Create(&module) : NULL;
+}

@@ -189,7 +189,7 @@ def test_linear_exact_integers(dtype, od, T, K, O):
 
 # tile shapes, each with and without a K split (the plan would take some of
 # them at large sizes alone)
-SHAPES = ["0,1", "0,3", "1,1", "1,2", "2,1", "2,3"]
+SHAPES = ["0,1", "0,3", "1,1", "1,2", "2,1", "2,3", "3,1", "3,3"]
 
 
 @pytest.mark.parametrize("plan", SHAPES)
