@@ -129,17 +129,17 @@ GemmPlan gemm_plan(int32_t dtype, int32_t out_dtype, Form form, int64_t M, int64
       const int64_t want = only_parts ? only_parts : s;
       const int64_t per = (steps + want - 1) / want, parts = (steps + per - 1) / per;
       GemmPlan g{shape, (int32_t)t, 1, 0};
-      float us = 0.f;
+      float us = 0.f, join = 0.f;
       if (parts > 1 && rest) {
         const int64_t bytes = rest * parts * sh.bm * sh.bn * 4;
         if (bytes > kMaxPartials && !only_parts) break;
         g = {shape, (int32_t)(t - rest), (int32_t)parts, bytes};
-        us = round_time(c, shape, t - rest, steps) + round_time(c, shape, rest * parts, per) +
-             kJoinStart + parts * kJoinPart + bytes * kJoinPerByte;
-        us *= 1.03f;  // (a tie goes to one launch)
+        us = round_time(c, shape, t - rest, steps) + round_time(c, shape, rest * parts, per);
+        join = kJoinStart + parts * kJoinPart + bytes * kJoinPerByte;
       } else {
         us = round_time(c, shape, t, steps);
       }
+      if (join > 0.f) us = (us + join) * 1.03f;  // (a tie goes to one launch)
       if (best_us == 0.f || us < best_us) {
         best = g;
         best_us = us;
