@@ -125,21 +125,6 @@ __device__ __forceinline__ void tile_of(const GemmArgs& p, int b, int& tm, int& 
   tile_place(p, tile, tm, tn);
 }
 
-// Global row of B that LDS row `r` of a tile holds.  gated: a wave's WN rows
-// are WN / 2 gate rows, then the up rows of the same columns.
-template <bool kGated, int WN>
-__device__ __forceinline__ int b_row(int r, int n0, int N) {
-  if constexpr (kGated) {
-    const int wc = r / WN, rr = r % WN, up = rr >= WN / 2;
-    int n = n0 + wc * (WN / 2) + (up ? rr - WN / 2 : rr);
-    n = n < N ? n : N - 1;
-    return up ? N + n : n;
-  } else {
-    const int n = n0 + r;
-    return n < N ? n : N - 1;
-  }
-}
-
 template <int V>
 struct Int {
   static constexpr int value = V;
@@ -150,19 +135,31 @@ constexpr int type_size(int dt) { return dt == LORA_F32 ? 4 : dt == LORA_BF16 ? 
 // Loaded in place of what lies past the end of the reduction.
 static __device__ const uint32_t kZeros[4] __attribute__((aligned(16))) = {0, 0, 0, 0};
 
+// 16 bytes a lane from `base` (uniform) + `off`: one instruction and no vector
+// arithmetic, which the loops below do not hide (a 128 x 128 bf16 tile: 0.72 us
+// a step against 0.88 with addresses of 64 bits and a comparison a load).
+// kOnce: non-temporal.
 template <bool kOnce = false>
-__device__ __forceinline__ void load_lds(const char* from, bool past, char* to) {
-  from = past ? reinterpret_cast<const char*>(kZeros) : from;
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+__device__ __forceinline__ void load_lds(const char* base, uint32_t off, char* to) {
+  asm("" : "+s"(base), "+v"(off));  // (no 64-bit sums by lane are kept instead)
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(base + off),
                                    (__attribute__((address_space(3))) void*)to, 16, 0,
-                                   kOnce ? 2 : 0);  // 2: non-temporal
+                                   kOnce ? 2 : 0);
+}
+// the same where the reduction may end in the step.  The large kernel's waves
+// multiply in pairs, one while the other loads, which hides the sums; there it
+// is the faster form (8192^3 e4m3 428 us against 463).
+__device__ __forceinline__ void load_lds_end(const char* base, uint32_t off, bool past, char* to) {
+  const char* from = past ? reinterpret_cast<const char*>(kZeros) : base + off;
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                   (__attribute__((address_space(3))) void*)to, 16, 0, 0);
 }
 
 // A reduction-major tile of ROWS columns m: rows of RB bytes, one a k.
 template <int DT, int ROWS>
 struct ColTile {
   static constexpr int ES = type_size(DT), RB = ROWS * ES;
-  static_assert(DT == LORA_F32 ? RB >= 128 : RB == 64 || RB == 128 || RB == 256, "");
+  static_assert(DT == LORA_F32 ? RB >= 128 : RB == 32 || RB == 64 || RB == 128 || RB == 256, "");
   // position of column byte `c` of row k (its own inverse)
   static __device__ __forceinline__ int swizzle(int c, int k) {
     if constexpr (DT == LORA_F32) return c ^ (((k >> 2) & 1) << (RB == 128 ? 6 : 7));
@@ -298,7 +295,12 @@ __device__ __forceinline__ void finish_rows(const GemmArgs& p, const float* reg,
 // every wave and stage kt - 1 has been read by every wave, so its place takes
 // the loads of step kt + NST - 1.  The epilogue goes through LDS (a wave's own
 // region) so that it is a rolled loop over whole row pieces.
-template <int DT, Form kForm, int BM, int BN, int WM, int WN, int NST>
+//
+// kOnce: one row of tiles covers A, so that B is read once: the weights of a
+// decode step, which are gone from the caches before the next step wants them.
+// Its loads are non-temporal (1 x 14336 x 4096 bf16 26.7 -> 24.6 us, gated 1 x
+// 4096 x 14336 47.1 -> 42.8 us).
+template <int DT, Form kForm, int BM, int BN, int WM, int WN, int NST, bool kOnce>
 __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void gemm_ring_kernel(GemmArgs p) {
   constexpr bool kGated = kForm == kGatedForm, kACol = kForm == kGradW;
   constexpr bool kBCol = kForm == kGradX || kForm == kGradW;
@@ -325,58 +327,56 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void gemm_ring_kernel(Gem
   const int per = tile < p.whole ? nk_all : (nk_all + p.splits - 1) / p.splits;
   const int k_lo = sp * per, nk = (k_lo + per < nk_all ? k_lo + per : nk_all) - k_lo;
 
-  // a load's lanes: their address at this part's first step, and how many bytes
-  // of the reduction lie before theirs in the step
-  const char* src[P];
-  int before[P];
-  const int64_t step_a = kACol ? kStepBytes / ES * p.lda : kStepBytes;
-  const int64_t step_b = kBCol ? kStepBytes / ES * p.ldb : kStepBytes;
+  // Loads: the first half of the waves fills A, the other B.  A lane's offset
+  // from the tile's first stored row in the step, and how many bytes of the
+  // reduction lie before its own in the step.
+  static_assert(NW % 2 == 0 && BM == BN, "");
+  const bool of_a = wave < NW / 2;
+  const int run = of_a ? wave * P : wave * P - BM / 8;  // first 1 KB run of the operand's
+  const int64_t ld = of_a ? p.lda : p.ldb;
+  const int64_t advance =
+      (of_a ? kACol : kBCol) ? (int64_t)(kStepBytes / ES) * ld : (int64_t)kStepBytes;
+  const char* base = of_a ? p.A + (kACol ? (int64_t)m0 * ES : m0 * ld)
+                          : p.B + (kBCol ? (int64_t)n0 * ES : n0 * ld);
+  base += k_lo * advance;
+  const int64_t up = kGated && !of_a ? p.N * ld : 0;  // from a gate row to its up row
+  uint32_t off[P];
+  auto before = [&](int j) {
+    if constexpr (kACol && kBCol) return ((run + j) * 1024 + lane * 16) / TileA::RB * ES;
+    if constexpr (kBCol)
+      if (!of_a) return ((run + j) * 1024 + lane * 16) / TileB::RB * ES;
+    return 16 * ((lane & 7) ^ ((4 * (run + j) + (lane >> 4)) & 7));
+  };
+  // gated: a wave's WN rows of B are WN / 2 gate rows, then the up rows of the
+  // same columns
+  auto is_up = [&](int j) { return kGated && !of_a && (run + j) * 8 % WN >= WN / 2; };
 #pragma unroll
   for (int j = 0; j < P; ++j) {
-    const int o = (wave * P + j) * 1024 + lane * 16;
-    if (o < BM * kStepBytes) {
-      if constexpr (kACol) {
-        const int k = o / TileA::RB;
-        int c = TileA::swizzle(o % TileA::RB, k);
-        c = m0 + c / ES < p.M ? c : 0;
-        src[j] = p.A + (int64_t)m0 * ES + c + k_lo * step_a + k * p.lda;
-        before[j] = k * ES;
-      } else {
-        const int r = o / kStepBytes;
-        const int m = m0 + r < p.M ? m0 + r : p.M - 1;
-        before[j] = 16 * ((lane & 7) ^ ((r >> 1) & 7));
-        src[j] = p.A + (int64_t)m * p.lda + k_lo * step_a + before[j];
-      }
+    const int o = (run + j) * 1024 + lane * 16;
+    if (of_a ? kACol : kBCol) {
+      const int rb = of_a ? TileA::RB : TileB::RB, k = o / rb;
+      int c = of_a ? TileA::swizzle(o % rb, k) : TileB::swizzle(o % rb, k);
+      if ((of_a ? m0 : n0) + c / ES >= (of_a ? p.M : p.N)) c = 0;
+      off[j] = (uint32_t)c + (uint32_t)k * (uint32_t)ld;
     } else {
-      const int ob = o - BM * kStepBytes;
-      if constexpr (kBCol) {
-        const int k = ob / TileB::RB;
-        int c = TileB::swizzle(ob % TileB::RB, k);
-        c = n0 + c / ES < p.N ? c : 0;
-        src[j] = p.B + (int64_t)n0 * ES + c + k_lo * step_b + k * p.ldb;
-        before[j] = k * ES;
-      } else {
-        const int r = ob / kStepBytes;
-        before[j] = 16 * ((lane & 7) ^ ((r >> 1) & 7));
-        src[j] = p.B + (int64_t)b_row<kGated, WN>(r, n0, p.N) * p.ldb + k_lo * step_b + before[j];
-      }
+      int r = o / kStepBytes;
+      if (kGated && !of_a) r = r / WN * (WN / 2) + r % (WN / 2);
+      const int left = of_a ? p.M - m0 : p.N - n0;
+      off[j] = (uint32_t)(r < left ? r : left - 1) * (uint32_t)ld + before(j);
     }
   }
   auto issue = [&](int kt, int slot) {
     const int64_t left = p.kb - (int64_t)(k_lo + kt) * kStepBytes;
+    const char* from = base + kt * advance;
+    char* to = lds + slot * STAGE + wave * P * 1024;
+    if (left >= kStepBytes) {
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-      const bool of_a = (wave * P + j) * 1024 < BM * kStepBytes;
-      const char* from = src[j] + kt * (of_a ? step_a : step_b);
-      char* to = lds + slot * STAGE + (wave * P + j) * 1024;
-      // B is read once where one row of tiles covers A: the weights of a decode
-      // step, which are gone from the caches before the next step wants them
-      // (1 x 14336 x 4096 bf16 26.7 -> 24.6 us, gated e4m3 16 x 4096 x 14336
-      // 30.2 -> 28.3 us)
-      if (!of_a && p.tiles_m == 1)
-        load_lds<true>(from, before[j] >= left, to);
-      else
-        load_lds(from, before[j] >= left, to);
+      for (int j = 0; j < P; ++j)
+        load_lds<kOnce>(from + (is_up(j) ? up : 0), off[j], to + j * 1024);
+    } else {
+#pragma unroll
+      for (int j = 0; j < P; ++j)
+        load_lds_end(from + (is_up(j) ? up : 0), off[j], before(j) >= left, to + j * 1024);
     }
   };
 
@@ -487,7 +487,8 @@ __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
   const int nk_all = (int)((p.kb + kStepBytes - 1) / kStepBytes);
   const int per = tile < p.whole ? nk_all : (nk_all + p.splits - 1) / p.splits;
   const int k_lo = sp * per, nk = (k_lo + per < nk_all ? k_lo + per : nk_all) - k_lo;
-  const int tail = (int)(p.kb - (int64_t)(k_lo + nk - 1) * kStepBytes);  // of the last step
+  const int64_t rest = p.kb - (int64_t)(k_lo + nk - 1) * kStepBytes;
+  const int tail = rest < kStepBytes ? (int)rest : kStepBytes;  // bytes of the last step
 
   // loads: a wave fills 1 KB runs w and w + 8 of every piece, so the chunk of a
   // row that a lane takes is the same in every load of a row-major operand
@@ -524,7 +525,7 @@ __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int before = kCol ? (1024 * (wave + 8 * j) + 16 * lane) / Piece::RB * ES : chunk16;
-      load_lds(from + off[j], kt == nk - 1 && before >= tail, to + j * 8192);
+      load_lds_end(from, off[j], kt == nk - 1 && before >= tail, to + j * 8192);
     }
   };
   auto fill_a = [&](int h, int kt) {
@@ -685,8 +686,16 @@ __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
 
 template <int DT, Form kForm, int BM, int BN, int WM, int WN, int NST>
 void launch_ring(const GemmArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((gemm_ring_kernel<DT, kForm, BM, BN, WM, WN, NST>),
-                     dim3(a.whole + (a.tiles_m * a.tiles_n - a.whole) * a.splits), dim3(BM / WM * (BN / WN) * 64), 0, st,
+  const dim3 grid(a.whole + (a.tiles_m * a.tiles_n - a.whole) * a.splits);
+  const dim3 block(BM / WM * (BN / WN) * 64);
+  if constexpr ((kForm == kLinearForm || kForm == kGatedForm) && BM <= 64) {
+    if (a.tiles_m == 1) {
+      hipLaunchKernelGGL((gemm_ring_kernel<DT, kForm, BM, BN, WM, WN, NST, true>), grid, block, 0,
+                         st, a);
+      return;
+    }
+  }
+  hipLaunchKernelGGL((gemm_ring_kernel<DT, kForm, BM, BN, WM, WN, NST, false>), grid, block, 0, st,
                      a);
 }
 
