@@ -506,8 +506,8 @@ int32_t lora_apply_ranked(const lora_pool_desc* desc, const void* A_pool, const 
  * projection, gated feed-forward block and that block's gradients.  All
  * matrices are device memory, row-major and contiguous; every pointer is
  * 16-byte aligned; calls are asynchronous on `stream`, allocate nothing, and
- * can be captured in a graph.  T = 0 is a no-op (except that a gradient of the
- * weights over no tokens is zero).  Sums and statistics are kept in fp32 or
+ * can be captured in a graph.  T is at most 2^21; T = 0 is a no-op (except that
+ * a gradient of the weights over no tokens is zero).  Sums and statistics are kept in fp32 or
  * wider and every output is rounded once (nearest, ties to even).  The result
  * of a call does not depend on timing: no atomics, fixed orders.
  *

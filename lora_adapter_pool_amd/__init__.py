@@ -17,4 +17,5 @@ from ._lib import (  # noqa: F401
     lora_linear, lora_linear_workspace_bytes, lora_gated_ffn, lora_gated_ffn_workspace_bytes,
     lora_gated_ffn_backward, lora_gated_ffn_backward_workspace_bytes,
 )
+from .mlp import LoraMlp  # noqa: F401
 from .pool import LoraPool  # noqa: F401

@@ -69,6 +69,7 @@ constexpr int kNumShapes = 4;
 constexpr TileShape kShapes[kNumShapes] = {{32, 32}, {64, 64}, {128, 128}, {256, 256}};
 
 int32_t check_launch(const char* what);
+int32_t check_rows(int32_t T);
 
 #ifdef __HIPCC__
 

@@ -162,7 +162,7 @@ extern "C" int32_t lora_add_rms_norm(const lora_norm_desc* desc, const void* x,
     return fail(LORA_E_ALIGN, "hidden must be a multiple of 8, got %d", desc->hidden);
   if (!(desc->eps >= 0.f && desc->eps < __builtin_inff()))
     return fail(LORA_E_ARG, "eps must be finite and >= 0, got %g", (double)desc->eps);
-  if (T < 0) return fail(LORA_E_ARG, "T must be >= 0, got %d", T);
+  if (int32_t e = check_rows(T)) return e;
   if (T == 0) return LORA_OK;
   if (!x || !weight) return fail(LORA_E_ARG, "x and weight must not be NULL");
   if ((residual != nullptr) != (sum != nullptr))

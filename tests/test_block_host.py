@@ -40,7 +40,7 @@ def test_norm_refusals():
         (1, None, _lib.LORA_E_ARG), (3, None, _lib.LORA_E_ARG), (2, None, _lib.LORA_E_ARG),
         (4, None, _lib.LORA_E_ARG), (6, None, _lib.LORA_E_ARG), (7, None, _lib.LORA_E_ARG),
         (1, FAKE + 2, _lib.LORA_E_ALIGN), (6, FAKE + 8, _lib.LORA_E_ALIGN),
-        (8, -1, _lib.LORA_E_ARG)])
+        (8, -1, _lib.LORA_E_ARG), (8, (1 << 21) + 1, _lib.LORA_E_SHAPE)])
     assert status(L.lora_add_rms_norm, d, FAKE, None, FAKE, None, None, None, None, 4) == \
         _lib.LORA_E_ARG                                            # no output at all
     assert status(L.lora_add_rms_norm, d, *[None] * 7, 0) == 0     # T = 0
