@@ -135,26 +135,30 @@ __device__ __forceinline__ void act_apply(int act, float (&z)[NV]) {
   }
 }
 
-// An activation's value and derivative.
+// An activation's value and derivative.  Past the clamps every factor beside
+// z is 0 or 1 in fp32, and infinities get the curve's limits: 0 below, z and 1
+// above.  (A NaN reaches the result through p.)
 __device__ __forceinline__ void act_curve(int act, float z, float& value, float& slope) {
   value = z;
   slope = 1.f;
+  const float low = fmaxf(z, -0x1.fffffep127f);
+  const float near = fminf(fmaxf(z, -200.f), 200.f);
   if (act == LORA_ACT_SILU) {
     const float p = bk_logistic(z);
-    value = z * p;
-    slope = p * __builtin_fmaf(z, 1.f - p, 1.f);
+    value = low * p;
+    slope = p * __builtin_fmaf(near, 1.f - p, 1.f);
   } else if (act == LORA_ACT_GELU) {
     const float p = bk_phi(z);
-    value = z * p;
-    slope = __builtin_fmaf(z * 0.398942280401432678f, bk_exp(-0.5f * z * z), p);
+    value = low * p;
+    slope = __builtin_fmaf(near * 0.398942280401432678f, bk_exp(-0.5f * near * near), p);
   } else if (act == LORA_ACT_GELU_TANH) {
     const float p = bk_tanh_gate(z);
-    value = z * p;
-    slope = __builtin_fmaf(value * (1.f - p),
-                           2.f * kGeluC * __builtin_fmaf(3.f * kGeluA * z, z, 1.f), p);
+    value = low * p;
+    slope = __builtin_fmaf(near * p * (1.f - p),
+                           2.f * kGeluC * __builtin_fmaf(3.f * kGeluA * near, near, 1.f), p);
   } else if (act == LORA_ACT_RELU) {
     value = z < 0.f ? 0.f : z;
-    slope = z > 0.f ? 1.f : 0.f;
+    slope = z > 0.f ? 1.f : z < 0.f ? 0.f : z;  // 0 at 0; keeps NaN
   }
 }
 

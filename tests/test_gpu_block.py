@@ -390,6 +390,36 @@ def test_backward_activations(dtype, act):
     _check_backward(150, 200, 88, dtype, act, 5)
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh", "relu"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_activations_at_the_ends_of_their_range(dtype, act):
+    """Gates of zero, far values and infinities get the curve's limits, forward
+    and backward; NaN stays."""
+    inf, nan = float("inf"), float("nan")
+    gate = [0.0, -0.0, 3e-39, 150.0, -150.0, 2.5e19, -2.5e19, 3e38, -3e38, inf, -inf, nan]
+    I = 16
+    pre = torch.ones((1, 2 * I), dtype=TORCH[dtype], device="cuda")
+    pre[0, :len(gate)] = torch.tensor(gate).to(TORCH[dtype])
+    one = torch.ones((1, I), dtype=TORCH[dtype], device="cuda")
+    x = torch.zeros((1, 8), dtype=TORCH[dtype], device="cuda")
+    w = torch.zeros((2 * I, 8), dtype=TORCH[dtype], device="cuda")
+    dpre, _, _ = run_backward(one, pre, x, w, act, dtype, dx=False, dw=False)
+    out, _ = run_gated(x, w, None, None, pre, False, dtype, dtype, act)
+    z = pre[0, :len(gate)].double()
+    value = torch.where(z > 100, z, torch.where(z < -100, torch.zeros_like(z), z / 2))
+    slope = torch.where(z > 100, 1.0, torch.where(z < -100, 0.0, 0.5))
+    if act == "relu":
+        value = torch.where(z > 0, z, torch.zeros_like(z))
+        slope = (z > 0).double()
+    for got, want in ((out[0], value), (dpre[0, I:], value), (dpre[0, :I], slope)):
+        got = got[:len(gate)]
+        assert torch.isnan(got[-1])
+        bound = 2.0 ** -20 + HALF_STEP[dtype]
+        same = got[:-1].double() == want[:-1]
+        assert (same | ((got[:-1].double() - want[:-1]).abs() <= bound * want[:-1].abs() +
+                        2.0 ** -126)).all(), (act, got, want)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T,K,I", [(1030, 1032, 1304), (2500, 776, 520), (4099, 264, 136)])
 def test_backward_large(dtype, T, K, I):
