@@ -33,7 +33,39 @@ struct NormArgs {
   uint8_t* out8;
   float* scale;
   int32_t H;
-  double eps;
+  double over_h, eps;
+};
+
+// 1 / x and 1 / sqrt(x) to within a few steps of 64 bits: the hardware's
+// estimates (some 2^-26) and one step of third order.  Zero and infinity keep
+// the estimate's infinity and zero.
+__device__ __forceinline__ double reciprocal(double x) {
+  const double y = __builtin_amdgcn_rcp(x), e = __builtin_fma(-x, y, 1.0);
+  const double z = __builtin_fma(y, __builtin_fma(e, e, e), y);
+  return e == e ? z : y;
+}
+__device__ __forceinline__ double reciprocal_root(double x) {
+  const double y = __builtin_amdgcn_rsq(x), e = __builtin_fma(-x * y, y, 1.0);
+  const double z = __builtin_fma(y, e * __builtin_fma(0.375, e, 0.5), y);
+  return e == e ? z : y;
+}
+
+// A piece of eight elements as it is stored (the weights are fetched with the
+// row, and take their room before its statistic is known).
+template <int DT>
+struct Raw {
+  bk_u32x4 v[DT == LORA_F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* base, int64_t i) {
+    const bk_u32x4* p = reinterpret_cast<const bk_u32x4*>(
+        (const char*)base + i * (DT == LORA_F32 ? 4 : 2));
+    v[0] = p[0];
+    if constexpr (DT == LORA_F32) v[1] = p[1];
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (DT == LORA_F32) return __uint_as_float(v[i >> 2][i & 3]);
+    const uint32_t w = v[0][i >> 1];
+    return i & 1 ? bk_hi(w) : bk_lo(w);
+  }
 };
 
 // NP pieces of eight elements a thread, one row a workgroup.
@@ -44,12 +76,14 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs a) {
   const int tid = threadIdx.x, nt = blockDim.x, waves = nt >> 6;
   const int64_t base = (int64_t)blockIdx.x * a.H;
   float t[NP][8];
+  Raw<DT> weight[NP];
   double ss = 0.0;
 #pragma unroll
   for (int j = 0; j < NP; ++j) {
     const int c = (tid + j * nt) * 8;
     if (c < a.H) {
       load8(a.x, base + c, 8, DT, t[j]);
+      weight[j].load(a.weight, c);
       if (a.residual) {
         float r[8];
         load8(a.residual, base + c, 8, DT, r);
@@ -80,18 +114,16 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs a) {
     ss = 0.0;
     for (int i = 0; i < waves; ++i) ss += sums[i];  // same order in every thread
   }
-  const float rstd = (float)(1.0 / __builtin_sqrt(ss / a.H + a.eps));
+  const float rstd = (float)reciprocal_root(__builtin_fma(ss, a.over_h, a.eps));
 
   uint32_t top = 0;  // largest |n| by its bits, which also keeps a NaN
 #pragma unroll
   for (int j = 0; j < NP; ++j) {
     const int c = (tid + j * nt) * 8;
     if (c < a.H) {
-      float w[8];
-      load8(a.weight, c, 8, DT, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        t[j][i] = t[j][i] * rstd * w[i];
+        t[j][i] = t[j][i] * rstd * weight[j].at(i);
         const uint32_t b = __float_as_uint(t[j][i]) & 0x7fffffffu;
         top = b > top ? b : top;
       }
@@ -109,9 +141,9 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs a) {
     __syncthreads();
     for (int i = 0; i < waves; ++i) top = tops[i] > top ? tops[i] : top;
   }
-  float scale = (float)((double)__uint_as_float(top) / 448.0);
+  float scale = (float)((double)__uint_as_float(top) * (1.0 / 448.0));
   scale = scale < 0x1p-126f ? 0x1p-126f : scale;  // keeps NaN
-  const float inv = (float)(1.0 / (double)scale);
+  const float inv = (float)reciprocal(scale);
   if (tid == 0) a.scale[blockIdx.x] = scale;
 #pragma unroll
   for (int j = 0; j < NP; ++j) {
@@ -175,7 +207,7 @@ extern "C" int32_t lora_add_rms_norm(const lora_norm_desc* desc, const void* x,
     if (!aligned16(p))
       return fail(LORA_E_ALIGN, "every buffer of the norm must be 16-byte aligned");
   const NormArgs a{x,     residual, weight, sum, out, (uint8_t*)out8,
-                   scale, desc->hidden, (double)desc->eps};
+                   scale, desc->hidden, 1.0 / desc->hidden, (double)desc->eps};
   if (desc->dtype == LORA_BF16)
     launch_norm<LORA_BF16>(a, T, (hipStream_t)stream);
   else
