@@ -9,9 +9,10 @@
 // x and the residual once in, every output once out.  The row's statistic
 // is summed in 64 bits: the rounding of n / scale to 8 bits has borders, and a
 // statistic that is right to 32 bits leaves n with the three roundings of its
-// products alone.  The workgroup size is the row's: enough threads that each
-// holds one or two pieces, because a row's latency (load, two reductions,
-// store) is what a small batch waits for.
+// products alone.  The workgroup size is the row's, because a row's latency
+// (load, two reductions, store) is what a small batch waits for; large batches
+// run at the rate of a copy (8960 x 4096 bf16 with residual and 8-bit output:
+// 330 MB in 61 us, 5.4 TB/s).
 #include <hip/hip_runtime.h>
 
 #include "lora_block.h"
@@ -163,9 +164,12 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs a) {
 template <int DT>
 void launch_norm(const NormArgs& a, int T, hipStream_t st) {
   const int pieces = a.H / 8;
-  // two pieces a thread where that fills a workgroup of 64 to 512 threads
+  // One piece a thread up to 512 threads (64 rows of 4096: 3.7 us against 4.3
+  // with two, 8960 rows 61 against 64), then two (8960 rows of 8192 bf16: 68 us
+  // against 95 with 1024 threads of one), then 1024 threads.
   int nt = 64;
-  while (nt < kMaxThreads && nt * 2 < pieces) nt *= 2;
+  while (nt < 512 && nt < pieces) nt *= 2;
+  if (nt * 2 < pieces) nt = kMaxThreads;
   const int np = (pieces + nt - 1) / nt;
   if (np == 1)
     hipLaunchKernelGGL((norm_kernel<DT, 1>), dim3(T), dim3(nt), 0, st, a);
