@@ -616,13 +616,29 @@ __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
       return;
     }
     __builtin_amdgcn_s_setprio(1);
+    if constexpr (DT == LORA_BF16) {
+      // one operand for four instructions, and never the sum of the one before
+      // (gradients of 4096 x 4096 x 14336 1484 -> 1470 us)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int hb = 0; hb < 2; ++hb)
+        for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          acc[ha][hb][i][j] = mma<DT>(fb[hb][j], fa[i], acc[ha][hb][i][j]);
+          for (int i0 = 0; i0 < 4; ++i0) {
+            const int hb = q >> 1, j = q & 1, i = j ? 3 - i0 : i0;
+            acc[ha][hb][i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                __builtin_bit_cast(bk_bf16x8, fb[hb][j][c]), __builtin_bit_cast(bk_bf16x8, fa[i][c]),
+                acc[ha][hb][i][j], 0, 0, 0);
+          }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            acc[ha][hb][i][j] = mma<DT>(fb[hb][j], fa[i], acc[ha][hb][i][j]);
+    }
     __builtin_amdgcn_s_setprio(0);
   };
   auto slot_end = [&]() {
