@@ -51,15 +51,20 @@ struct GemmPlan {
   int32_t whole;   // tiles that are not split
   int32_t splits;  // parts of each of the others
   int64_t ws_bytes;  // fp32 partials
+  float us;        // estimate
 };
 GemmPlan gemm_plan(int32_t dtype, int32_t out_dtype, Form form, int64_t M, int64_t N,
                    int64_t kb);
 int32_t gemm_run(int32_t dtype, Form form, const GemmPlan& plan, GemmArgs a, void* ws,
                  hipStream_t st);
+// the shapes that the gradients' products may share a launch with: the ring's
+constexpr int kPairShapes = 3;
 // per type (each in its own source file)
 int32_t gemm_launch_bf16(Form form, int shape, const GemmArgs& a, hipStream_t st);
 int32_t gemm_launch_e4m3(Form form, int shape, const GemmArgs& a, hipStream_t st);
 int32_t gemm_launch_f32(Form form, int shape, const GemmArgs& a, hipStream_t st);
+int32_t gemm_launch_pair_bf16(int shape, const GemmArgs& x, const GemmArgs& w, hipStream_t st);
+int32_t gemm_launch_pair_f32(int shape, const GemmArgs& x, const GemmArgs& w, hipStream_t st);
 
 struct TileShape {
   int bm, bn;  // rows of A and rows of B a workgroup covers

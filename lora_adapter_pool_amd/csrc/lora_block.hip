@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <cstdlib>
+#include <cstring>
 
 #include "lora_block.h"
 
@@ -116,7 +117,6 @@ GemmPlan gemm_plan(int32_t dtype, int32_t out_dtype, Form form, int64_t M, int64
     if (parts >= 1 && parts <= 64) only_parts = (int)parts;
   }
   GemmPlan best{};
-  float best_us = 0.f;
   for (int shape = 0; shape < kNumShapes; ++shape) {
     if (only_shape >= 0 && shape != only_shape) continue;
     const TileShape& sh = kShapes[shape];
@@ -128,42 +128,42 @@ GemmPlan gemm_plan(int32_t dtype, int32_t out_dtype, Form form, int64_t M, int64
     for (int64_t s = 1; s <= 16; ++s) {
       const int64_t want = only_parts ? only_parts : s;
       const int64_t per = (steps + want - 1) / want, parts = (steps + per - 1) / per;
-      GemmPlan g{shape, (int32_t)t, 1, 0};
+      GemmPlan g{shape, (int32_t)t, 1, 0, 0.f};
       float us = 0.f, join = 0.f;
       if (parts > 1 && rest) {
         const int64_t bytes = rest * parts * sh.bm * sh.bn * 4;
         if (bytes > kMaxPartials && !only_parts) break;
-        g = {shape, (int32_t)(t - rest), (int32_t)parts, bytes};
+        g = {shape, (int32_t)(t - rest), (int32_t)parts, bytes, 0.f};
         us = round_time(c, shape, t - rest, steps) + round_time(c, shape, rest * parts, per);
         join = kJoinStart + parts * kJoinPart + bytes * kJoinPerByte;
       } else {
         us = round_time(c, shape, t, steps);
       }
-      if (join > 0.f) us = (us + join) * 1.03f;  // (a tie goes to one launch)
-      if (best_us == 0.f || us < best_us) {
-        best = g;
-        best_us = us;
-      }
+      if (join > 0.f) us += join + 0.3f;  // (a tie goes to one launch)
+      g.us = us;
+      if (best.us == 0.f || us < best.us) best = g;
       if (only_parts || rest == 0 || rest * s > 4 * kComputeUnits) break;
     }
   }
   return best;
 }
 
-int32_t gemm_run(int32_t dtype, Form form, const GemmPlan& plan, GemmArgs a, void* ws,
-                 hipStream_t st) {
-  const bool gated = form == kGatedForm;
+namespace {
+
+void fill_plan(GemmArgs& a, const GemmPlan& plan, Form form, void* ws) {
   const TileShape sh = kShapes[plan.shape];
-  const int width = gated ? 2 * a.N : a.N;
+  const int width = form == kGatedForm ? 2 * a.N : a.N;
   a.tiles_m = (a.M + sh.bm - 1) / sh.bm;
   a.tiles_n = (width + sh.bn - 1) / sh.bn;
   a.whole = plan.whole;
   a.splits = plan.splits;
   a.part = (float*)ws;
-  int32_t e = dtype == LORA_BF16   ? gemm_launch_bf16(form, plan.shape, a, st)
-              : dtype == LORA_E4M3 ? gemm_launch_e4m3(form, plan.shape, a, st)
-                                   : gemm_launch_f32(form, plan.shape, a, st);
-  if (e || plan.splits == 1) return e;
+}
+
+int32_t join_parts(const GemmArgs& a, const GemmPlan& plan, Form form, hipStream_t st) {
+  if (plan.splits == 1) return LORA_OK;
+  const TileShape sh = kShapes[plan.shape];
+  const bool gated = form == kGatedForm;
   const int rest = a.tiles_m * a.tiles_n - a.whole;
   const dim3 grid((unsigned)((rest * (sh.bm * (gated ? sh.bn / 2 : sh.bn) / 8) + 255) / 256));
   if (gated)
@@ -171,6 +171,17 @@ int32_t gemm_run(int32_t dtype, Form form, const GemmPlan& plan, GemmArgs a, voi
   else
     hipLaunchKernelGGL(join_kernel<false>, grid, dim3(256), 0, st, a, sh.bm, sh.bn);
   return check_launch("join of the K splits");
+}
+
+}  // namespace
+
+int32_t gemm_run(int32_t dtype, Form form, const GemmPlan& plan, GemmArgs a, void* ws,
+                 hipStream_t st) {
+  fill_plan(a, plan, form, ws);
+  int32_t e = dtype == LORA_BF16   ? gemm_launch_bf16(form, plan.shape, a, st)
+              : dtype == LORA_E4M3 ? gemm_launch_e4m3(form, plan.shape, a, st)
+                                   : gemm_launch_f32(form, plan.shape, a, st);
+  return e ? e : join_parts(a, plan, form, st);
 }
 
 namespace {
@@ -211,22 +222,79 @@ __global__ __launch_bounds__(256) void clear_kernel(bk_u32x4* p, int64_t n) {
     p[i] = bk_u32x4{0, 0, 0, 0};
 }
 
-// The two products run one after the other and share the workspace.
+// The two products: one after the other (they share the workspace), or in one
+// launch (each has its own part).
 struct BackwardPlan {
+  bool pair;
   GemmPlan dx, dw;
-  int64_t total;
+  int64_t dw_at, total;
 };
+
+// What separate launches cost beside their products: the gap between them, in
+// which the compute units drain and fill.
+constexpr float kLaunchGap = 2.f;
+
+// Both products in tiles of one shape, each split into up to eight parts: the
+// time of the longest workgroup, or of all of them dealt over the units.
+// `only`: a forced choice, "shape,i,j" with 2^i and 2^j parts.
+BackwardPlan pair_plan(int32_t dtype, const int64_t (&M)[2], int64_t N, const int64_t (&kb)[2],
+                       const char* only) {
+  BackwardPlan best{};
+  float best_us = 0.f;
+  for (int shape = 0; shape < kPairShapes; ++shape) {
+    if (only && only[0] != '0' + shape) continue;
+    const TileShape& sh = kShapes[shape];
+    const ShapeCost& c = kCosts[dtype][shape];
+    const float cap = (float)((shape < 2 ? 3 - shape : 1) * kComputeUnits);
+    GemmPlan g[2][4];
+    float longest[2][4], work[2][4], join[2][4];
+    for (int p = 0; p < 2; ++p) {
+      const int64_t t = ((M[p] + sh.bm - 1) / sh.bm) * ((N + sh.bn - 1) / sh.bn);
+      const int64_t steps = (kb[p] + kStepBytes - 1) / kStepBytes, rest = t % kComputeUnits;
+      for (int i = 0; i < 4; ++i) {
+        const int64_t per = (steps + (1 << i) - 1) >> i, parts = (steps + per - 1) / per;
+        const bool split = parts > 1 && rest;
+        const int64_t bytes = split ? rest * parts * sh.bm * sh.bn * 4 : 0;
+        g[p][i] = {shape, (int32_t)(split ? t - rest : t), (int32_t)(split ? parts : 1), bytes, 0.f};
+        const float whole = c.start + steps * c.step_all, part = c.start + per * c.step_all;
+        longest[p][i] = c.start + (t >= kComputeUnits || !split ? steps : per) * c.step_few;
+        work[p][i] = split ? (t - rest) * whole + rest * parts * part : t * whole;
+        join[p][i] = split ? kJoinStart + parts * kJoinPart + bytes * kJoinPerByte : 0.f;
+      }
+    }
+    for (int i = 0; i < 4; ++i)
+      for (int j = 0; j < 4; ++j) {
+        if (only ? only[2] != '0' + i || only[4] != '0' + j
+                 : g[0][i].ws_bytes + g[1][j].ws_bytes > kMaxPartials)
+          continue;
+        const float us = std::max(std::max(longest[0][i], longest[1][j]),
+                                  (work[0][i] + work[1][j]) / cap) +
+                         join[0][i] + join[1][j];
+        if (best_us == 0.f || us < best_us * 0.97f) {
+          best = {true, g[0][i], g[1][j], align_up(g[0][i].ws_bytes, 256), 0};
+          best.dx.us = best_us = us;
+        }
+      }
+  }
+  best.total = best.dw_at + best.dw.ws_bytes;
+  return best;
+}
 
 BackwardPlan backward_plan(const lora_gated_desc& d, int64_t T, bool dx, bool dw) {
   BackwardPlan b{};
   const int64_t e = esize(d.dtype), K = d.in_features, I2 = 2 * (int64_t)d.inter_features;
-  if (dx) {
-    b.dx = gemm_plan(d.dtype, d.dtype, kGradX, T, K, e * I2);
-    b.total = std::max(b.total, b.dx.ws_bytes);
-  }
-  if (dw) {
-    b.dw = gemm_plan(d.dtype, d.dtype, kGradW, I2, K, e * T);
-    b.total = std::max(b.total, b.dw.ws_bytes);
+  if (dx) b.dx = gemm_plan(d.dtype, d.dtype, kGradX, T, K, e * I2);
+  if (dw) b.dw = gemm_plan(d.dtype, d.dtype, kGradW, I2, K, e * T);
+  b.total = std::max(b.dx.ws_bytes, b.dw.ws_bytes);
+  if (dx && dw) {
+    // tuning overrides: "shape,i,j", or anything else for separate launches
+    const char* f = std::getenv("LORA_GRAD_PAIR");
+    const bool forced = f && std::strlen(f) == 5 && f[0] >= '0' && f[0] < '0' + kPairShapes &&
+                        f[2] >= '0' && f[2] < '4' && f[4] >= '0' && f[4] < '4';
+    if (!forced && (f || std::getenv("LORA_GEMM_PLAN"))) return b;
+    BackwardPlan p = pair_plan(d.dtype, {T, I2}, K, {e * I2, e * T}, forced ? f : nullptr);
+    p.total = std::max(p.total, b.total);  // (either gradient alone fits as well)
+    if (forced || p.dx.us < b.dx.us + b.dw.us + kLaunchGap) return p;
   }
   return b;
 }
@@ -469,19 +537,29 @@ int32_t lora_gated_ffn_backward(const lora_gated_desc* desc, const void* dout, c
   a.ldb = K * es;
   a.out_dtype = desc->dtype;
   a.act = LORA_ACT_NONE;
+  GemmArgs ax = a, aw = a;
+  ax.B = (const char*)w;
+  ax.out = dx;
+  ax.M = T;
+  ax.kb = 2 * I * es;
+  aw.B = (const char*)x;
+  aw.out = dw;
+  aw.M = 2 * I;
+  aw.kb = T * es;
+  if (b.pair) {
+    fill_plan(ax, b.dx, kGradX, ws);
+    fill_plan(aw, b.dw, kGradW, (char*)ws + b.dw_at);
+    if (int32_t e = desc->dtype == LORA_BF16 ? gemm_launch_pair_bf16(b.dx.shape, ax, aw, st)
+                                             : gemm_launch_pair_f32(b.dx.shape, ax, aw, st))
+      return e;
+    if (int32_t e = join_parts(ax, b.dx, kGradX, st)) return e;
+    return join_parts(aw, b.dw, kGradW, st);
+  }
   if (dx) {
-    a.B = (const char*)w;
-    a.out = dx;
-    a.M = T;
-    a.kb = 2 * I * es;
-    if (int32_t e = gemm_run(desc->dtype, kGradX, b.dx, a, ws, st)) return e;
+    if (int32_t e = gemm_run(desc->dtype, kGradX, b.dx, ax, ws, st)) return e;
   }
   if (dw) {
-    a.B = (const char*)x;
-    a.out = dw;
-    a.M = 2 * I;
-    a.kb = T * es;
-    if (int32_t e = gemm_run(desc->dtype, kGradW, b.dw, a, ws, st)) return e;
+    if (int32_t e = gemm_run(desc->dtype, kGradW, b.dw, aw, ws, st)) return e;
   }
   return LORA_OK;
 }

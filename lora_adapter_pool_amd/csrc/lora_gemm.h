@@ -309,8 +309,14 @@ __device__ __forceinline__ void finish_rows(const GemmArgs& p, const float* reg,
 // decode step, which are gone from the caches before the next step wants them.
 // Its loads are non-temporal (1 x 14336 x 4096 bf16 26.7 -> 24.6 us, gated 1 x
 // 4096 x 14336 47.1 -> 42.8 us).
+template <int BM, int BN, int WM, int WN, int NST>
+constexpr int ring_bytes() {
+  constexpr int stages = (BM + BN) * kStepBytes * NST;
+  constexpr int epilogue = BM / WM * (BN / WN) * WM * (WN + 4) * 4;
+  return stages > epilogue ? stages : epilogue;
+}
 template <int DT, Form kForm, int BM, int BN, int WM, int WN, int NST, bool kOnce>
-__global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void gemm_ring_kernel(GemmArgs p) {
+__device__ __forceinline__ void ring_tile(const GemmArgs& p, int block, char* lds) {
   constexpr bool kGated = kForm == kGatedForm, kACol = kForm == kGradW;
   constexpr bool kBCol = kForm == kGradX || kForm == kGradW;
   constexpr int ES = type_size(DT);
@@ -321,12 +327,9 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void gemm_ring_kernel(Gem
   constexpr int P = (BM + BN) / 8 / NW;  // loads a wave makes for a stage
   static_assert(P * NW * 8 == BM + BN, "rows divide over the waves");
   constexpr int LDE = WN + 4;            // floats a row of the epilogue's region
-  constexpr int EPI = NW * WM * LDE * 4;
-  constexpr int BYTES = STAGE * NST > EPI ? STAGE * NST : EPI;
-  __shared__ __align__(1024) char lds[BYTES];
 
   int tm, tn, tile, sp;
-  tile_of(p, blockIdx.x, tm, tn, tile, sp);
+  tile_of(p, block, tm, tn, tile, sp);
   const int m0 = tm * BM, n0 = tn * (kGated ? BN / 2 : BN);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -453,6 +456,28 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void gemm_ring_kernel(Gem
   constexpr int WCOLS = kGated ? WN / 2 : WN;  // output columns of a wave
   finish_rows<kGated, BM, BN, WM, WCOLS, LDE>(p, reg, lane, m0 + wr * WM, n0 + wc * WCOLS, tile,
                                               sp, wr * WM, wc * WCOLS);
+}
+
+template <int DT, Form kForm, int BM, int BN, int WM, int WN, int NST, bool kOnce>
+__global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void gemm_ring_kernel(GemmArgs p) {
+  __shared__ __align__(1024) char lds[ring_bytes<BM, BN, WM, WN, NST>()];
+  ring_tile<DT, kForm, BM, BN, WM, WN, NST, kOnce>(p, blockIdx.x, lds);
+}
+
+// Both gradients' products in one launch: they need each other's results for
+// nothing, and together they fill compute units that either leaves idle.
+// `first` workgroups belong to the product with the longer reduction.
+template <int DT, int BM, int BN, int WM, int WN, int NST>
+__global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void gemm_pair_kernel(GemmArgs x,
+                                                                             GemmArgs w,
+                                                                             int first,
+                                                                             bool x_first) {
+  __shared__ __align__(1024) char lds[ring_bytes<BM, BN, WM, WN, NST>()];
+  const int b = blockIdx.x;
+  if ((b < first) == x_first)
+    ring_tile<DT, kGradX, BM, BN, WM, WN, NST, false>(x, b < first ? b : b - first, lds);
+  else
+    ring_tile<DT, kGradW, BM, BN, WM, WN, NST, false>(w, b < first ? b : b - first, lds);
 }
 
 // The large product: a 256 x 256 tile, 8 waves of 128 x 64 (two a SIMD), and
@@ -739,6 +764,25 @@ int32_t launch_form(int shape, const GemmArgs& a, hipStream_t st) {
     hipLaunchKernelGGL((gemm_phase_kernel<DT, kForm>), grid, dim3(512), 0, st, a);
   }
   return check_launch("product");
+}
+
+template <int DT, int BM, int BN, int WM, int WN, int NST>
+void launch_pair_of(const GemmArgs& x, const GemmArgs& w, hipStream_t st) {
+  const int nx = x.whole + (x.tiles_m * x.tiles_n - x.whole) * x.splits;
+  const int nw = w.whole + (w.tiles_m * w.tiles_n - w.whole) * w.splits;
+  const bool x_first = x.kb / x.splits >= w.kb / w.splits;
+  hipLaunchKernelGGL((gemm_pair_kernel<DT, BM, BN, WM, WN, NST>), dim3(nx + nw),
+                     dim3(BM / WM * (BN / WN) * 64), 0, st, x, w, x_first ? nx : nw, x_first);
+}
+template <int DT>
+int32_t launch_pair(int shape, const GemmArgs& x, const GemmArgs& w, hipStream_t st) {
+  if (shape == 0)
+    launch_pair_of<DT, 32, 32, 16, 16, 6>(x, w, st);
+  else if (shape == 1)
+    launch_pair_of<DT, 64, 64, 32, 32, 4>(x, w, st);
+  else
+    launch_pair_of<DT, 128, 128, 64, 64, 3>(x, w, st);
+  return check_launch("products of the gradients");
 }
 
 // the forms of the forward pass, and those of the gradients

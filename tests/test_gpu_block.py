@@ -348,6 +348,17 @@ def test_backward_every_shape(dtype, plan, monkeypatch):
         _check_backward(T, K, I, dtype, "silu", 30 + k)
 
 
+@pytest.mark.parametrize("pair", ["0,0,0", "0,2,1", "1,0,0", "1,1,3", "2,0,0", "2,3,1", "off"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_backward_in_one_launch(dtype, pair, monkeypatch):
+    """Both products in one launch, every tile shape with and without K splits
+    (bf16 rounds sums of another order: the bounds, not each other)."""
+    monkeypatch.setenv("LORA_GRAD_PAIR", pair)
+    for k, (T, K, I) in enumerate(((1, 8, 8), (31, 264, 136), (257, 520, 264), (600, 304, 72),
+                                   (67, 72, 520), (1500, 40, 1600))):
+        _check_backward(T, K, I, dtype, "silu", 60 + k, inplace=k == 1)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_backward_exact_integers(dtype):
     # relu over positive gates: dpre, and with it every product, is whole
