@@ -739,7 +739,7 @@ void launch_ring(const GemmArgs& a, hipStream_t st) {
   const dim3 grid(a.whole + (a.tiles_m * a.tiles_n - a.whole) * a.splits);
   const dim3 block(BM / WM * (BN / WN) * 64);
   if constexpr ((kForm == kLinearForm || kForm == kGatedForm) && BM <= 64) {
-    if (a.tiles_m == 1) {
+    if (a.tiles_m == 1 && a.ldb % kStepBytes == 0) {
       hipLaunchKernelGGL((gemm_ring_kernel<DT, kForm, BM, BN, WM, WN, NST, true>), grid, block, 0,
                          st, a);
       return;
