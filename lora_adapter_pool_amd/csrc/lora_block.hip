@@ -65,38 +65,52 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs p, int bm, int bn) {
 namespace {
 
 // What a workgroup of a tile shape takes, in microseconds: a start and an end,
-// and a step of kStepBytes, where few compute units run and where all do.
-// Fitted to 1300 times of products of 1 to 8960 rows and 256 to 14336 columns
-// and terms under every shape and split (rms error 7 to 15%).  Of those the
-// plan that the model picks is on average 2 to 3% slower than the best; the
-// largest shape that fills the compute units, else a split that does, was 18%
-// slower in bf16 (700 x 14336 x 4096: 178 us against 86).
+// and a step of kStepBytes.  A compute unit holds up to three workgroups of the
+// smallest shape and two of the next: their step with one, two and three on the
+// busiest unit.  It holds one of the others: their step where few units run and
+// where all do.  Fitted to 5800 times of products of 1 to 8960 rows and 256 to
+// 20000 columns and terms, rows of whole cache lines and not, under every shape
+// and split.  The plan that the model picks is on average 0.5 to 3% slower
+// than the best of them; the largest shape that fills the units, else a split
+// that does, was 18% slower in bf16 (700 x 14336 x 4096: 178 us against 86).
 struct ShapeCost {
-  float start, step_few, step_all;
+  float start, step[3];
 };
 constexpr ShapeCost kCosts[4][kNumShapes] = {
-    {{1.9f, 0.26f, 0.53f}, {1.8f, 0.65f, 1.15f}, {2.2f, 2.15f, 2.15f}, {3.4f, 7.0f, 7.0f}},   // fp32
-    {{1.4f, 0.22f, 0.30f}, {2.1f, 0.32f, 0.41f}, {3.6f, 0.64f, 0.70f}, {6.3f, 0.81f, 1.40f}},  // bf16
+    // fp32
+    {{1.6f, {0.27f, 0.41f, 0.54f}}, {1.5f, {0.64f, 1.18f}}, {2.3f, {1.95f, 2.22f}}, {5.0f, {7.4f, 8.0f}}},
+    // bf16
+    {{1.2f, {0.19f, 0.27f, 0.36f}}, {1.6f, {0.32f, 0.50f}}, {2.6f, {0.56f, 0.68f}}, {4.7f, {0.86f, 1.42f}}},
     // e4m3 with bf16 outputs, with fp32 outputs
-    {{1.7f, 0.21f, 0.30f}, {2.4f, 0.31f, 0.41f}, {4.2f, 0.64f, 0.71f}, {7.0f, 0.79f, 1.46f}},
-    {{1.4f, 0.27f, 0.45f}, {2.3f, 0.42f, 0.63f}, {3.5f, 1.04f, 1.15f}, {5.2f, 3.20f, 3.50f}}};
-constexpr float kJoinStart = 2.4f;        // a second launch
-constexpr float kJoinPart = 0.15f;        // a part of a tile
-constexpr float kJoinPerByte = 0.26e-6f;  // partials written and read again
+    {{1.4f, {0.18f, 0.27f, 0.35f}}, {1.9f, {0.33f, 0.48f}}, {2.8f, {0.57f, 0.69f}}, {4.0f, {0.79f, 1.50f}}},
+    {{1.8f, {0.29f, 0.36f, 0.39f}}, {2.2f, {0.35f, 0.60f}}, {2.3f, {1.05f, 1.14f}}, {4.3f, {3.4f, 3.7f}}}};
+// Where B is read once and does not fit a cache, a compute unit loads no more
+// than this a microsecond (a probe that only loads: 46 KB from memory).
+constexpr float kColdRate = 55e3f;
+constexpr float kColdBytes = 50e6f;
+// The smallest gated tile has two waves to load with, not four.
+constexpr float kGatedSmall = 1.4f;
+constexpr float kJoinStart = 2.6f;       // a second launch
+constexpr float kJoinPart = 0.1f;        // a part of a tile
+constexpr float kJoinPerByte = 0.2e-6f;  // partials written and read again
+
+// workgroups of a shape that a compute unit holds
+constexpr int units_hold(int shape) { return shape < 2 ? 3 - shape : 1; }
+// a step where all units hold what they can
+constexpr float full_step(const ShapeCost& c, int shape) { return c.step[shape == 0 ? 2 : 1]; }
 
 constexpr int64_t kMaxPartials = 64 << 20;  // bytes
 
-// `n` workgroups of `steps` steps.  A compute unit holds three of the smallest
-// shape, two of the next and one of the others; the last round is cheaper the
-// fewer it has.
+// `n` workgroups of `steps` steps.
 float round_time(const ShapeCost& c, int shape, int64_t n, int64_t steps) {
-  const int64_t cap = (shape < 2 ? 3 - shape : 1) * kComputeUnits;
+  const int64_t cap = (int64_t)units_hold(shape) * kComputeUnits;
   const int64_t full = n / cap, rest = n % cap;
-  float us = full * (c.start + steps * c.step_all);
+  float us = full * (c.start + steps * full_step(c, shape));
   if (rest) {
-    const float idle = shape < 2 ? 128.f : 0.f;  // alone on its unit, or nearly
-    const float load = std::max(0.f, rest - idle) / (cap - idle);
-    us += c.start + steps * (c.step_few + (c.step_all - c.step_few) * load);
+    const float step = units_hold(shape) > 1
+                           ? c.step[(rest - 1) / kComputeUnits]
+                           : c.step[0] + (c.step[1] - c.step[0]) * rest / kComputeUnits;
+    us += c.start + steps * step;
   }
   return us;
 }
@@ -120,7 +134,12 @@ GemmPlan gemm_plan(int32_t dtype, int32_t out_dtype, Form form, int64_t M, int64
   for (int shape = 0; shape < kNumShapes; ++shape) {
     if (only_shape >= 0 && shape != only_shape) continue;
     const TileShape& sh = kShapes[shape];
-    const ShapeCost& c = kCosts[type][shape];
+    ShapeCost c = kCosts[type][shape];
+    if (M <= sh.bm && (float)(M + width) * (float)kb > kColdBytes)
+      for (int k = 0; k < units_hold(shape); ++k)
+        c.step[k] = std::max(c.step[k], (k + 1) * (sh.bm + sh.bn) * kStepBytes / kColdRate);
+    if (form == kGatedForm && shape == 0)
+      for (float& step : c.step) step *= kGatedSmall;
     const int64_t t = ((M + sh.bm - 1) / sh.bm) * ((width + sh.bn - 1) / sh.bn);
     // Whole rounds of tiles, one a compute unit, are not split; the tiles of the
     // last round may be, where they leave compute units idle.
@@ -245,7 +264,7 @@ BackwardPlan pair_plan(int32_t dtype, const int64_t (&M)[2], int64_t N, const in
     if (only && only[0] != '0' + shape) continue;
     const TileShape& sh = kShapes[shape];
     const ShapeCost& c = kCosts[dtype][shape];
-    const float cap = (float)((shape < 2 ? 3 - shape : 1) * kComputeUnits);
+    const float cap = (float)(units_hold(shape) * kComputeUnits), step = full_step(c, shape);
     GemmPlan g[2][4];
     float longest[2][4], work[2][4], join[2][4];
     for (int p = 0; p < 2; ++p) {
@@ -256,8 +275,8 @@ BackwardPlan pair_plan(int32_t dtype, const int64_t (&M)[2], int64_t N, const in
         const bool split = parts > 1 && rest;
         const int64_t bytes = split ? rest * parts * sh.bm * sh.bn * 4 : 0;
         g[p][i] = {shape, (int32_t)(split ? t - rest : t), (int32_t)(split ? parts : 1), bytes, 0.f};
-        const float whole = c.start + steps * c.step_all, part = c.start + per * c.step_all;
-        longest[p][i] = c.start + (t >= kComputeUnits || !split ? steps : per) * c.step_few;
+        const float whole = c.start + steps * step, part = c.start + per * step;
+        longest[p][i] = c.start + (t >= kComputeUnits || !split ? steps : per) * c.step[0];
         work[p][i] = split ? (t - rest) * whole + rest * parts * part : t * whole;
         join[p][i] = split ? kJoinStart + parts * kJoinPart + bytes * kJoinPerByte : 0.f;
       }
