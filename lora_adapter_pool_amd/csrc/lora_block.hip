@@ -94,6 +94,12 @@ constexpr float kJoinStart = 2.6f;       // a second launch
 constexpr float kJoinPart = 0.1f;        // a part of a tile
 constexpr float kJoinPerByte = 0.2e-6f;  // partials written and read again
 
+// Reduction-major bf16 tiles against row-major ones, by shape: a row of the
+// smallest is 64 bytes, half a cache line; the middle one's workgroups, two a
+// unit, share most of what they load (gradients of 300 x 2048 x 2048 in one
+// launch: 57, 32 and 41 us in the three shapes).
+constexpr float kColumnsCost[kNumShapes] = {1.7f, 0.85f, 1.2f, 1.05f};
+
 // workgroups of a shape that a compute unit holds
 constexpr int units_hold(int shape) { return shape < 2 ? 3 - shape : 1; }
 // a step where all units hold what they can
@@ -140,6 +146,8 @@ GemmPlan gemm_plan(int32_t dtype, int32_t out_dtype, Form form, int64_t M, int64
         c.step[k] = std::max(c.step[k], (k + 1) * (sh.bm + sh.bn) * kStepBytes / kColdRate);
     if (form == kGatedForm && shape == 0)
       for (float& step : c.step) step *= kGatedSmall;
+    if ((form == kGradX || form == kGradW) && dtype == LORA_BF16)
+      for (float& step : c.step) step *= kColumnsCost[shape];
     const int64_t t = ((M + sh.bm - 1) / sh.bm) * ((width + sh.bn - 1) / sh.bn);
     // Whole rounds of tiles, one a compute unit, are not split; the tiles of the
     // last round may be, where they leave compute units idle.
@@ -249,9 +257,10 @@ struct BackwardPlan {
   int64_t dw_at, total;
 };
 
-// What separate launches cost beside their products: the gap between them, in
-// which the compute units drain and fill.
-constexpr float kLaunchGap = 2.f;
+// What separate launches cost beside the estimates of their products: the gap
+// between them, in which the compute units drain and fill (measured 3 to 18 us
+// at 300 to 2567 rows).
+constexpr float kLaunchGap = 10.f;
 
 // Both products in tiles of one shape, each split into up to eight parts: the
 // time of the longest workgroup, or of all of them dealt over the units.
@@ -263,7 +272,9 @@ BackwardPlan pair_plan(int32_t dtype, const int64_t (&M)[2], int64_t N, const in
   for (int shape = 0; shape < kPairShapes; ++shape) {
     if (only && only[0] != '0' + shape) continue;
     const TileShape& sh = kShapes[shape];
-    const ShapeCost& c = kCosts[dtype][shape];
+    ShapeCost c = kCosts[dtype][shape];
+    if (dtype == LORA_BF16)
+      for (float& s : c.step) s *= kColumnsCost[shape];
     const float cap = (float)(units_hold(shape) * kComputeUnits), step = full_step(c, shape);
     GemmPlan g[2][4];
     float longest[2][4], work[2][4], join[2][4];
