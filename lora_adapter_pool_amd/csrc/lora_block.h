@@ -36,6 +36,7 @@ struct GemmArgs {
   int32_t M, N;
   int32_t whole;          // tiles that are not split: the first ones
   int32_t splits;         // parts of each other tile
+  int32_t lines;          // load whole cache lines where rows do not start at one
   int32_t out_dtype;      // of bias, delta, residual, pre and out
   int32_t act;
   int32_t tiles_m, tiles_n;

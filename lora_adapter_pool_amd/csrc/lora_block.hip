@@ -105,6 +105,9 @@ constexpr int units_hold(int shape) { return shape < 2 ? 3 - shape : 1; }
 // a step where all units hold what they can
 constexpr float full_step(const ShapeCost& c, int shape) { return c.step[shape == 0 ? 2 : 1]; }
 
+// Operands from which on whole cache lines are worth loading.
+constexpr float kLineBytes = 30e6f;
+
 constexpr int64_t kMaxPartials = 64 << 20;  // bytes
 
 // `n` workgroups of `steps` steps.
@@ -185,6 +188,8 @@ void fill_plan(GemmArgs& a, const GemmPlan& plan, Form form, void* ws) {
   a.whole = plan.whole;
   a.splits = plan.splits;
   a.part = (float*)ws;
+  const char* force = std::getenv("LORA_GEMM_LINES");  // tuning override: 0 or 1
+  a.lines = force ? *force == '1' : (float)(a.M + width) * (float)a.kb > kLineBytes;
 }
 
 int32_t join_parts(const GemmArgs& a, const GemmPlan& plan, Form form, hipStream_t st) {

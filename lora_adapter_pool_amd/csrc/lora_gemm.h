@@ -309,13 +309,23 @@ __device__ __forceinline__ void finish_rows(const GemmArgs& p, const float* reg,
 // decode step, which are gone from the caches before the next step wants them.
 // Its loads are non-temporal (1 x 14336 x 4096 bf16 26.7 -> 24.6 us, gated 1 x
 // 4096 x 14336 47.1 -> 42.8 us).
+//
+// kLines: rows that do not start at a cache line.  Loads of 128 bytes from a
+// row's start would touch every line twice, a step apart.  Stage L holds whole
+// lines instead, from 16 sh bytes before the row's chunk 8 L on, where sh =
+// (address / 16) mod 8 repeats every eight rows, and step kt reads its chunks
+// from stages kt and kt + 1.  The swizzle stays free of conflicts: (x + 2 n q)
+// mod 8, then xor q, is a permutation of 0 .. 7 in q for every x and n.  This
+// pays where the loads come from memory (gated bf16 44 x 9112 x 9408 93 -> 82
+// us, 64 x 4104 x 4096 16.4 -> 14.5 us) and costs a short product time (gated
+// 777 x 1032 x 520 9.6 -> 11.3 us): the plan decides by the operands' size.
 template <int BM, int BN, int WM, int WN, int NST>
 constexpr int ring_bytes() {
   constexpr int stages = (BM + BN) * kStepBytes * NST;
   constexpr int epilogue = BM / WM * (BN / WN) * WM * (WN + 4) * 4;
   return stages > epilogue ? stages : epilogue;
 }
-template <int DT, Form kForm, int BM, int BN, int WM, int WN, int NST, bool kOnce>
+template <int DT, Form kForm, int BM, int BN, int WM, int WN, int NST, bool kOnce, bool kLines>
 __device__ __forceinline__ void ring_tile(const GemmArgs& p, int block, char* lds) {
   constexpr bool kGated = kForm == kGatedForm, kACol = kForm == kGradW;
   constexpr bool kBCol = kForm == kGradX || kForm == kGradW;
@@ -351,13 +361,20 @@ __device__ __forceinline__ void ring_tile(const GemmArgs& p, int block, char* ld
   const char* base = of_a ? p.A + (kACol ? (int64_t)m0 * ES : m0 * ld)
                           : p.B + (kBCol ? (int64_t)n0 * ES : n0 * ld);
   base += k_lo * advance;
+  // (chunk units; the tile's first row and a wave's tiles are multiples of
+  // eight rows apart)
+  auto shift_of = [&](const char* at, int64_t stride, int row) {
+    return kLines ? (int)(((uintptr_t)at >> 4) + row * (stride >> 4)) & 7 : 0;
+  };
+  const int sh = shift_of(base, ld, lane >> 3);
+  const int lines = kLines ? nk + 1 : nk;  // stages to load
   const int64_t up = kGated && !of_a ? p.N * ld : 0;  // from a gate row to its up row
   uint32_t off[P];
   auto before = [&](int j) {
     if constexpr (kACol && kBCol) return ((run + j) * 1024 + lane * 16) / TileA::RB * ES;
     if constexpr (kBCol)
       if (!of_a) return ((run + j) * 1024 + lane * 16) / TileB::RB * ES;
-    return 16 * ((lane & 7) ^ ((4 * (run + j) + (lane >> 4)) & 7));
+    return 16 * (((lane & 7) ^ ((4 * (run + j) + (lane >> 4)) & 7)) - sh);
   };
   // gated: a wave's WN rows of B are WN / 2 gate rows, then the up rows of the
   // same columns
@@ -374,14 +391,23 @@ __device__ __forceinline__ void ring_tile(const GemmArgs& p, int block, char* ld
       int r = o / kStepBytes;
       if (kGated && !of_a) r = r / WN * (WN / 2) + r % (WN / 2);
       const int left = of_a ? p.M - m0 : p.N - n0;
-      off[j] = (uint32_t)(r < left ? r : left - 1) * (uint32_t)ld + before(j);
+      // (kLines: from a line before the row, so that it is not negative)
+      off[j] = (uint32_t)(r < left ? r : left - 1) * (uint32_t)ld +
+               (uint32_t)(before(j) + (kLines ? kStepBytes : 0));
     }
   }
   auto issue = [&](int kt, int slot) {
     const int64_t left = p.kb - (int64_t)(k_lo + kt) * kStepBytes;
-    const char* from = base + kt * advance;
+    const char* from = base + kt * advance - (kLines ? kStepBytes : 0);
     char* to = lds + slot * STAGE + wave * P * 1024;
-    if (left >= kStepBytes) {
+    if (kLines && k_lo + kt == 0) {  // what lies before the row is not read
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        const int b = before(j);
+        load_lds_end(from + (is_up(j) ? up : 0), off[j] + (b < 0 ? -b : 0), b >= left,
+                     to + j * 1024);
+      }
+    } else if (left >= kStepBytes) {
 #pragma unroll
       for (int j = 0; j < P; ++j)
         load_lds<kOnce>(from + (is_up(j) ? up : 0), off[j], to + j * 1024);
@@ -401,19 +427,29 @@ __device__ __forceinline__ void ring_tile(const GemmArgs& p, int block, char* ld
 
 #pragma unroll
   for (int s = 0; s < NST - 1; ++s)
-    if (s < nk) issue(s, s);
+    if (s < lines) issue(s, s);
+
+  // a lane's two chunks: place in a stage's row, and whether in the next stage
+  const int sha = shift_of(p.A + m0 * p.lda, p.lda, l16);
+  const int shb = shift_of(p.B + n0 * p.ldb, p.ldb, l16);
+  auto place = [&](int chunk) { return ((chunk & 7) ^ (l16 >> 1)) * 16; };
+  const int a0 = place(g + sha), a1 = place(g + 4 + sha);
+  const int b0 = place(g + shb), b1 = place(g + 4 + shb);
 
   int slot = 0;
   for (int kt = 0; kt < nk; ++kt) {
-    if (kt + NST - 1 <= nk)
-      __builtin_amdgcn_s_waitcnt(wait_vm((NST - 2) * P));
+    // (kLines: stage kt + 1 has landed too)
+    if (kt + NST - 1 <= lines)
+      __builtin_amdgcn_s_waitcnt(wait_vm((NST - (kLines ? 3 : 2)) * P));
     else
       __builtin_amdgcn_s_waitcnt(wait_vm(0));
     barrier();
-    if (kt + NST - 1 < nk) issue(kt + NST - 1, slot == 0 ? NST - 1 : slot - 1);
+    if (kt + NST - 1 < lines) issue(kt + NST - 1, slot == 0 ? NST - 1 : slot - 1);
 
     const char* stage = lds + slot * STAGE;
-    const int c0 = (g ^ (l16 >> 1)) * 16, c1 = c0 ^ 64;
+    const int next = kLines ? (slot == NST - 1 ? -(NST - 1) * STAGE : STAGE) : 0;
+    const int at_a0 = a0 + (g + sha > 7 ? next : 0), at_a1 = a1 + (g + sha > 3 ? next : 0);
+    const int at_b0 = b0 + (g + shb > 7 ? next : 0), at_b1 = b1 + (g + shb > 3 ? next : 0);
     bk_u32x4 fa[WM / 16][2], fb[WN / 16][2];
     if constexpr (kACol) {
       TileA::read(stage, wr * WM, l16, g, fa);
@@ -421,8 +457,8 @@ __device__ __forceinline__ void ring_tile(const GemmArgs& p, int block, char* ld
       const char* sA = stage + (wr * WM + l16) * kStepBytes;
 #pragma unroll
       for (int i = 0; i < WM / 16; ++i) {
-        fa[i][0] = *reinterpret_cast<const bk_u32x4*>(sA + i * 16 * kStepBytes + c0);
-        fa[i][1] = *reinterpret_cast<const bk_u32x4*>(sA + i * 16 * kStepBytes + c1);
+        fa[i][0] = *reinterpret_cast<const bk_u32x4*>(sA + i * 16 * kStepBytes + at_a0);
+        fa[i][1] = *reinterpret_cast<const bk_u32x4*>(sA + i * 16 * kStepBytes + at_a1);
       }
     }
     if constexpr (kBCol) {
@@ -431,8 +467,8 @@ __device__ __forceinline__ void ring_tile(const GemmArgs& p, int block, char* ld
       const char* sB = stage + (BM + wc * WN + l16) * kStepBytes;
 #pragma unroll
       for (int j = 0; j < WN / 16; ++j) {
-        fb[j][0] = *reinterpret_cast<const bk_u32x4*>(sB + j * 16 * kStepBytes + c0);
-        fb[j][1] = *reinterpret_cast<const bk_u32x4*>(sB + j * 16 * kStepBytes + c1);
+        fb[j][0] = *reinterpret_cast<const bk_u32x4*>(sB + j * 16 * kStepBytes + at_b0);
+        fb[j][1] = *reinterpret_cast<const bk_u32x4*>(sB + j * 16 * kStepBytes + at_b1);
       }
     }
 #pragma unroll
@@ -458,10 +494,10 @@ __device__ __forceinline__ void ring_tile(const GemmArgs& p, int block, char* ld
                                               sp, wr * WM, wc * WCOLS);
 }
 
-template <int DT, Form kForm, int BM, int BN, int WM, int WN, int NST, bool kOnce>
+template <int DT, Form kForm, int BM, int BN, int WM, int WN, int NST, bool kOnce, bool kLines>
 __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void gemm_ring_kernel(GemmArgs p) {
   __shared__ __align__(1024) char lds[ring_bytes<BM, BN, WM, WN, NST>()];
-  ring_tile<DT, kForm, BM, BN, WM, WN, NST, kOnce>(p, blockIdx.x, lds);
+  ring_tile<DT, kForm, BM, BN, WM, WN, NST, kOnce, kLines>(p, blockIdx.x, lds);
 }
 
 // Both gradients' products in one launch: they need each other's results for
@@ -475,9 +511,9 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void gemm_pair_kernel(Gem
   __shared__ __align__(1024) char lds[ring_bytes<BM, BN, WM, WN, NST>()];
   const int b = blockIdx.x;
   if ((b < first) == x_first)
-    ring_tile<DT, kGradX, BM, BN, WM, WN, NST, false>(x, b < first ? b : b - first, lds);
+    ring_tile<DT, kGradX, BM, BN, WM, WN, NST, false, false>(x, b < first ? b : b - first, lds);
   else
-    ring_tile<DT, kGradW, BM, BN, WM, WN, NST, false>(w, b < first ? b : b - first, lds);
+    ring_tile<DT, kGradW, BM, BN, WM, WN, NST, false, false>(w, b < first ? b : b - first, lds);
 }
 
 // The large product: a 256 x 256 tile, 8 waves of 128 x 64 (two a SIMD), and
@@ -734,19 +770,29 @@ __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
   }
 }
 
-template <int DT, Form kForm, int BM, int BN, int WM, int WN, int NST>
+template <int DT, Form kForm, int BM, int BN, int WM, int WN, int NST, bool kOnce, bool kLines>
+void launch_ring_as(const GemmArgs& a, hipStream_t st) {
+  hipLaunchKernelGGL((gemm_ring_kernel<DT, kForm, BM, BN, WM, WN, NST, kOnce, kLines>),
+                     dim3(a.whole + (a.tiles_m * a.tiles_n - a.whole) * a.splits),
+                     dim3(BM / WM * (BN / WN) * 64), 0, st, a);
+}
+// NSL: stages with kLines, where one more is in use
+template <int DT, Form kForm, int BM, int BN, int WM, int WN, int NST, int NSL>
 void launch_ring(const GemmArgs& a, hipStream_t st) {
-  const dim3 grid(a.whole + (a.tiles_m * a.tiles_n - a.whole) * a.splits);
-  const dim3 block(BM / WM * (BN / WN) * 64);
-  if constexpr ((kForm == kLinearForm || kForm == kGatedForm) && BM <= 64) {
-    if (a.tiles_m == 1 && a.ldb % kStepBytes == 0) {
-      hipLaunchKernelGGL((gemm_ring_kernel<DT, kForm, BM, BN, WM, WN, NST, true>), grid, block, 0,
-                         st, a);
-      return;
-    }
+  if constexpr (kForm == kLinearForm || kForm == kGatedForm) {
+    const bool off_lines = ((uintptr_t)a.A | (uintptr_t)a.B | (uint64_t)a.kb) % kStepBytes != 0;
+    // (fp32, and e4m3 that is widened, are bound by their products there)
+    constexpr bool kMay = BM >= 64 && (DT == LORA_BF16 || DT == LORA_E4M3);
+    const bool lines = kMay && off_lines && a.lines;
+    const bool once = BM <= 64 && a.tiles_m == 1 && (lines || !off_lines);
+    if constexpr (kMay && BM == 64)
+      if (once && lines) return launch_ring_as<DT, kForm, BM, BN, WM, WN, NSL, true, true>(a, st);
+    if constexpr (BM <= 64)
+      if (once) return launch_ring_as<DT, kForm, BM, BN, WM, WN, NST, true, false>(a, st);
+    if constexpr (kMay)
+      if (lines) return launch_ring_as<DT, kForm, BM, BN, WM, WN, NSL, false, true>(a, st);
   }
-  hipLaunchKernelGGL((gemm_ring_kernel<DT, kForm, BM, BN, WM, WN, NST, false>), grid, block, 0, st,
-                     a);
+  launch_ring_as<DT, kForm, BM, BN, WM, WN, NST, false, false>(a, st);
 }
 
 template <int DT, Form kForm>
@@ -754,11 +800,11 @@ int32_t launch_form(int shape, const GemmArgs& a, hipStream_t st) {
   // gated: a wave's rows of B are the gate and the up rows of the same columns
   constexpr bool kGated = kForm == kGatedForm;
   if (shape == 0)
-    launch_ring<DT, kForm, 32, 32, 16, kGated ? 32 : 16, 6>(a, st);
+    launch_ring<DT, kForm, 32, 32, 16, kGated ? 32 : 16, 6, 6>(a, st);
   else if (shape == 1)
-    launch_ring<DT, kForm, 64, 64, kGated ? 16 : 32, kGated ? 64 : 32, 4>(a, st);
+    launch_ring<DT, kForm, 64, 64, kGated ? 16 : 32, kGated ? 64 : 32, 4, 5>(a, st);
   else if (shape == 2)
-    launch_ring<DT, kForm, 128, 128, 64, 64, 3>(a, st);
+    launch_ring<DT, kForm, 128, 128, 64, 64, 3, 4>(a, st);
   else {
     const dim3 grid(a.whole + (a.tiles_m * a.tiles_n - a.whole) * a.splits);
     hipLaunchKernelGGL((gemm_phase_kernel<DT, kForm>), grid, dim3(512), 0, st, a);

@@ -231,6 +231,39 @@ def test_linear_inf_and_nan_stay_in_their_rows():
         within(got[rows][:, cols], z, product_bound(K, mag), "f32", "finite part")
 
 
+@pytest.mark.parametrize("plan", [None, "0,1", "0,3", "1,1", "1,2", "2,1", "2,2", "3,1"])
+@pytest.mark.parametrize("dtype,od", TYPES)
+def test_rows_off_the_cache_lines(dtype, od, plan, monkeypatch):
+    """Every distance of a row from a cache line, by odd row lengths and by
+    operands that start 16 bytes apart; what lies around them is not a number."""
+    if plan:
+        monkeypatch.setenv("LORA_GEMM_PLAN", plan)
+        monkeypatch.setenv("LORA_GEMM_LINES", "1")
+    es = {"bf16": 2, "e4m3": 1, "f32": 4}[dtype]
+    g = gen(11)
+
+    def placed(t, chunks):
+        n = t.numel() * es
+        buf = torch.full((n + 512,), 255, dtype=torch.uint8, device="cuda")   # NaN in every type
+        view = buf[128 + 16 * chunks:128 + 16 * chunks + n]
+        view.copy_(t.contiguous().view(torch.uint8).reshape(-1))
+        return view.view(t.dtype).view(t.shape)
+
+    for k, (T, chunks, O) in enumerate(((1, 1, 16), (5, 7, 32), (33, 13, 48), (70, 33, 96),
+                                        (130, 70, 144), (64, 66, 80))):
+        K = chunks * 16 // es
+        K = max(8, K // 8 * 8)    # (fp32 rows are multiples of 32 bytes)
+        for da, db in ((0, 0), (k + 1, 0), (3, (k + 5) % 8)):
+            x, xs = operand(g, T, K, dtype, 1.0, integer=True)
+            w, ws = operand(g, 2 * O, K, dtype, 1.0, integer=True)
+            z = x.double() @ w.double().t()
+            x, w = placed(x, da), placed(w, db)
+            got = run_linear(x, w, xs, ws, None, None, None, dtype, od, "none")
+            assert torch.equal(got, z.to(got.dtype)), (T, K, O, da, db)
+            got, _ = run_gated(x, w, xs, ws, None, False, dtype, od, "none")
+            assert torch.equal(got, (z[:, :O] * z[:, O:]).to(got.dtype)), (T, K, O, da, db)
+
+
 def test_linear_output_past_32_bit_offsets():
     T, K, O = 70001, 64, 16387     # 4.6 GB of fp32 outputs, odd rows
     g = gen(4)
