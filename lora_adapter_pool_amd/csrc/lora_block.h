@@ -110,6 +110,7 @@ __device__ __forceinline__ float bk_exp(float z) {
 __device__ __forceinline__ float bk_logistic(float z) {
   return __builtin_amdgcn_rcpf(1.f + bk_exp(-z));
 }
+// gelu in its tanh form: 0.5 (1 + tanh u) = logistic(2 u)
 constexpr float kGeluC = 0.797884560802865356f;  // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 // the normal distribution's cumulative function; through erfc, which keeps
@@ -117,24 +118,51 @@ constexpr float kGeluA = 0.044715f;
 __device__ __forceinline__ float bk_phi(float z) {
   return 0.5f * erfcf(-0.707106781186547524f * z);
 }
-// gelu in its tanh form: 0.5 (1 + tanh u) = logistic(2 u)
-__device__ __forceinline__ float bk_tanh_gate(float z) {
-  return bk_logistic(2.f * kGeluC * __builtin_fmaf(kGeluA * z * z, z, z));
+// The same for results that are rounded to bf16: without the correction of the
+// exponent (2^-17 of the result at |z| = 100, half a step of bf16 is 2^-9).
+// Activations are a large tile's epilogue: 65536 of them on one compute unit.
+__device__ __forceinline__ float bk_logistic_short(float z) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896341f * z));
+}
+// Phi by the Chebyshev fit of erfc in "Numerical Recipes" (erfcc): t e^(-x^2 +
+// P(t)), t = 1 / (1 + x / 2), to 1.2e-7 of the result for x >= 0 (and 2^-23 x^2
+// of it for the rounding of x^2); no branches.
+__device__ __forceinline__ float bk_phi_short(float z) {
+  const float x = __builtin_fabsf(0.707106781186547524f * z);
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.5f, x, 1.f));
+  float q = 0.17087277f;
+  q = __builtin_fmaf(q, t, -0.82215223f);
+  q = __builtin_fmaf(q, t, 1.48851587f);
+  q = __builtin_fmaf(q, t, -1.13520398f);
+  q = __builtin_fmaf(q, t, 0.27886807f);
+  q = __builtin_fmaf(q, t, -0.18628806f);
+  q = __builtin_fmaf(q, t, 0.09678418f);
+  q = __builtin_fmaf(q, t, 0.37409196f);
+  q = __builtin_fmaf(q, t, 1.00002368f);
+  q = __builtin_fmaf(q, t, __builtin_fmaf(-x, x, -1.26551223f));
+  const float half = 0.5f * t * __builtin_amdgcn_exp2f(1.44269504088896341f * q);
+  return z < 0.f ? half : 1.f - half;  // (a NaN is one in `half`)
 }
 
-// Applies an activation to eight values.  z * 0 of an infinite z far below
-// zero is no number, so the products with a vanishing factor are taken as 0.
-template <int NV>
+// Applies an activation to eight values; kShort: for results in bf16.  z = -inf
+// would give -inf 0: the factor below is finite, and 0 times it is 0.
+template <bool kShort, int NV>
 __device__ __forceinline__ void act_apply(int act, float (&z)[NV]) {
+  constexpr float kLowest = -0x1.fffffep127f;
   if (act == LORA_ACT_SILU) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) z[i] = z[i] == -__builtin_inff() ? 0.f : z[i] * bk_logistic(z[i]);
+    for (int i = 0; i < NV; ++i)
+      z[i] = fmaxf(z[i], kLowest) * (kShort ? bk_logistic_short(z[i]) : bk_logistic(z[i]));
   } else if (act == LORA_ACT_GELU) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) z[i] = z[i] == -__builtin_inff() ? 0.f : z[i] * bk_phi(z[i]);
+    for (int i = 0; i < NV; ++i)
+      z[i] = fmaxf(z[i], kLowest) * (kShort ? bk_phi_short(z[i]) : bk_phi(z[i]));
   } else if (act == LORA_ACT_GELU_TANH) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) z[i] = z[i] == -__builtin_inff() ? 0.f : z[i] * bk_tanh_gate(z[i]);
+    for (int i = 0; i < NV; ++i) {
+      const float v = 2.f * kGeluC * __builtin_fmaf(kGeluA * z[i] * z[i], z[i], z[i]);
+      z[i] = fmaxf(z[i], kLowest) * (kShort ? bk_logistic_short(v) : bk_logistic(v));
+    }
   } else if (act == LORA_ACT_RELU) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) z[i] = z[i] < 0.f ? 0.f : z[i];  // keeps NaN
@@ -144,21 +172,25 @@ __device__ __forceinline__ void act_apply(int act, float (&z)[NV]) {
 // An activation's value and derivative.  Past the clamps every factor beside
 // z is 0 or 1 in fp32, and infinities get the curve's limits: 0 below, z and 1
 // above.  (A NaN reaches the result through p.)
+template <bool kShort>
 __device__ __forceinline__ void act_curve(int act, float z, float& value, float& slope) {
   value = z;
   slope = 1.f;
   const float low = fmaxf(z, -0x1.fffffep127f);
   const float near = fminf(fmaxf(z, -200.f), 200.f);
   if (act == LORA_ACT_SILU) {
-    const float p = bk_logistic(z);
+    const float p = kShort ? bk_logistic_short(z) : bk_logistic(z);
     value = low * p;
     slope = p * __builtin_fmaf(near, 1.f - p, 1.f);
   } else if (act == LORA_ACT_GELU) {
-    const float p = bk_phi(z);
+    const float p = kShort ? bk_phi_short(z) : bk_phi(z);
+    const float e = kShort ? __builtin_amdgcn_exp2f(-0.5f * 1.44269504088896341f * near * near)
+                           : bk_exp(-0.5f * near * near);
     value = low * p;
-    slope = __builtin_fmaf(near * 0.398942280401432678f, bk_exp(-0.5f * near * near), p);
+    slope = __builtin_fmaf(near * 0.398942280401432678f, e, p);
   } else if (act == LORA_ACT_GELU_TANH) {
-    const float p = bk_tanh_gate(z);
+    const float v = 2.f * kGeluC * __builtin_fmaf(kGeluA * z * z, z, z);
+    const float p = kShort ? bk_logistic_short(v) : bk_logistic(v);
     value = low * p;
     slope = __builtin_fmaf(near * p * (1.f - p),
                            2.f * kGeluC * __builtin_fmaf(3.f * kGeluA * near, near, 1.f), p);
@@ -305,7 +337,10 @@ __device__ __forceinline__ void epilogue8(const GemmArgs& p, int m, int n, float
       store8(p.pre, at, left, od, z);
       store8(p.pre, at + p.N, left, od, u);
     }
-    act_apply(p.act, z);
+    if (od == LORA_BF16)
+      act_apply<true>(p.act, z);
+    else
+      act_apply<false>(p.act, z);
 #pragma unroll
     for (int j = 0; j < 8; ++j) z[j] *= u[j];
     store8(p.out, (int64_t)m * p.N + n, left, od, z);
@@ -318,7 +353,10 @@ __device__ __forceinline__ void epilogue8(const GemmArgs& p, int m, int n, float
       else
         add8(z, p.delta, at, left, od);
     }
-    act_apply(p.act, z);
+    if (od == LORA_BF16)
+      act_apply<true>(p.act, z);
+    else
+      act_apply<false>(p.act, z);
     if (p.residual) {
       if constexpr (kFetched)
         add8(z, x.r);

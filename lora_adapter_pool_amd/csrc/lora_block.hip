@@ -243,7 +243,7 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(const void* dout, const 
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       float value, slope;
-      act_curve(act, g[j], value, slope);
+      act_curve<DT == LORA_BF16>(act, g[j], value, slope);
       g[j] = d[j] * u[j] * slope;
       u[j] = d[j] * value;
     }
