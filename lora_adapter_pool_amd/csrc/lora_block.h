@@ -73,6 +73,8 @@ struct TileShape {
 // shapes, smallest first: three of gemm_ring_kernel, then gemm_phase_kernel's
 constexpr int kNumShapes = 4;
 constexpr TileShape kShapes[kNumShapes] = {{32, 32}, {64, 64}, {128, 128}, {256, 256}};
+// and gemm_rows_kernel, for few rows, and its waves
+constexpr int kRowsShape = kNumShapes, kMostRows = 32, kRowsWaves = 8;
 
 int32_t check_launch(const char* what);
 int32_t check_rows(int32_t T);

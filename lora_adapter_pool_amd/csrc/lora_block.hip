@@ -97,6 +97,14 @@ constexpr float kJoinStart = 2.6f;       // a second launch
 constexpr float kJoinPart = 0.1f;        // a part of a tile
 constexpr float kJoinPerByte = 0.2e-6f;  // partials written and read again
 
+// gemm_rows_kernel: its start, a step of each of its waves for 16 rows of B and
+// for a row of A (fp32: more products a byte), and what it reads of B a
+// microsecond at most.  Fitted to 750 times of 1 to 32 rows against the other
+// shapes': the pick is on average 1.4% slower than the better of the two, and at
+// worst 18% slower than the other shapes alone.
+constexpr float kRowsStart = 0.5f, kRowsStepB = 0.6f, kRowsStepA = 0.028f, kRowsF32 = 1.5f;
+constexpr float kRowsRate = 4.4e6f;
+
 // Reduction-major bf16 tiles against row-major ones, by shape: a row of the
 // smallest is 64 bytes, half a cache line; the middle one's workgroups, two a
 // unit, share most of what they load (gradients of 300 x 2048 x 2048 in one
@@ -127,6 +135,16 @@ float round_time(const ShapeCost& c, int shape, int64_t n, int64_t steps) {
   return us;
 }
 
+// few rows
+float rows_time(Form form, int type, int64_t M, int64_t N, int64_t kb) {
+  const int64_t rounds = ((N + 15) / 16 + kComputeUnits - 1) / kComputeUnits;
+  const int64_t turns = (kb + kRowsWaves * kStepBytes - 1) / (kRowsWaves * kStepBytes);
+  const int each = form == kGatedForm ? 2 : 1;
+  const float a = M * kRowsStepA * (type == LORA_F32 ? kRowsF32 : 1.f);
+  return std::max(rounds * (kRowsStart + turns * (each * kRowsStepB + a)),
+                  (float)(each * N) * (float)kb / kRowsRate);
+}
+
 }  // namespace
 
 GemmPlan gemm_plan(int32_t dtype, int32_t out_dtype, Form form, int64_t M, int64_t N,
@@ -134,15 +152,19 @@ GemmPlan gemm_plan(int32_t dtype, int32_t out_dtype, Form form, int64_t M, int64
   const int64_t width = form == kGatedForm ? 2 * N : N;  // rows of B
   const int64_t steps = (kb + kStepBytes - 1) / kStepBytes;
   const int type = dtype == LORA_E4M3 && out_dtype == LORA_F32 ? 3 : dtype;
+  const bool few = M <= kMostRows && (form == kLinearForm || form == kGatedForm);
   int only_shape = -1, only_parts = 0;
   if (const char* e = std::getenv("LORA_GEMM_PLAN")) {  // tuning override: shape,parts
     char* end = nullptr;
     const long shape = std::strtol(e, &end, 10);
     const long parts = *end == ',' ? std::strtol(end + 1, nullptr, 10) : 0;
-    if (shape >= 0 && shape < kNumShapes) only_shape = (int)shape;
+    if (shape >= 0 && shape < kNumShapes + few) only_shape = (int)shape;
     if (parts >= 1 && parts <= 64) only_parts = (int)parts;
   }
   GemmPlan best{};
+  if (few && (only_shape < 0 || only_shape == kRowsShape))
+    best = {kRowsShape, 1, 1, 0, rows_time(form, type, M, N, kb)};
+  if (only_shape == kRowsShape) return best;
   for (int shape = 0; shape < kNumShapes; ++shape) {
     if (only_shape >= 0 && shape != only_shape) continue;
     const TileShape& sh = kShapes[shape];
@@ -184,6 +206,7 @@ GemmPlan gemm_plan(int32_t dtype, int32_t out_dtype, Form form, int64_t M, int64
 namespace {
 
 void fill_plan(GemmArgs& a, const GemmPlan& plan, Form form, void* ws) {
+  if (plan.shape == kRowsShape) return;
   const TileShape sh = kShapes[plan.shape];
   const int width = form == kGatedForm ? 2 * a.N : a.N;
   a.tiles_m = (a.M + sh.bm - 1) / sh.bm;

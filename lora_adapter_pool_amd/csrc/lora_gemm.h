@@ -770,6 +770,113 @@ __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
   }
 }
 
+// Few rows: 16 MT rows by 16 columns a workgroup (gated: their gate and up
+// rows of B).  The eight waves share the reduction: wave w takes steps w, w + 8,
+// ..., straight from memory into the fragments (a row of B is wanted by this
+// workgroup alone, so LDS has nothing to share), and one sum over the waves
+// through LDS ends in the epilogue.  No second launch joins parts, and a
+// workgroup is 16 columns, so that few of them fill the compute units.  What
+// bounds it is its own loads: 26 KB of B a microsecond, and A once more for
+// every 16 columns.  Against the ring and its join, bf16: 1 x 4096 x 4096
+// 9.3 us (ring 11.1), gated 1 x 4096 x 4096 16.3 (19.6), 16 x 2048 x 2048 6.4
+// (8.8), but 1 x 14336 x 4096 27 (23) and 32 x 14336 x 4096 50 (28); e4m3 1 x
+// 4096 x 4096 7.2 (10.7).
+template <int DT, Form kForm, int MT>
+__global__ __launch_bounds__(64 * kRowsWaves) void gemm_rows_kernel(GemmArgs p) {
+  constexpr bool kGated = kForm == kGatedForm;
+  constexpr int NB = kGated ? 2 : 1, NF = MT * NB;
+  constexpr int U = MT + NB <= 3 ? 4 : 2;  // steps in flight a wave
+  __shared__ bk_f32x4 sums[kRowsWaves][NF][64];
+  const int n0 = blockIdx.x * 16;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l16 = lane & 15, g = lane >> 4;
+  const int nk = (int)((p.kb + kStepBytes - 1) / kStepBytes);
+
+  uint32_t offa[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int m = 16 * i + l16;
+    offa[i] = (uint32_t)(m < p.M ? m : p.M - 1) * (uint32_t)p.lda + 16 * g;
+  }
+  const uint32_t offb = (uint32_t)(n0 + l16 < p.N ? l16 : p.N - 1 - n0) * (uint32_t)p.ldb + 16 * g;
+  const char* gate = p.B + n0 * p.ldb;
+  const char* up = gate + p.N * p.ldb;
+
+  bk_f32x4 acc[MT][NB];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) acc[i][j] = bk_f32x4{0.f, 0.f, 0.f, 0.f};
+
+  for (int k0 = wave; k0 < nk; k0 += kRowsWaves * U) {
+    bk_u32x4 fa[U][MT][2], fb[U][NB][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + kRowsWaves * u;
+      if (k >= nk) break;
+      const int64_t at = (int64_t)k * kStepBytes, left = p.kb - at;
+      auto get = [&](const char* base, uint32_t off, bk_u32x4 (&f)[2], bool once) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          // past the reduction's end: zeros, from the step's first chunk
+          const bool past = 16 * g + 64 * s >= left;
+          const bk_u32x4* from = reinterpret_cast<const bk_u32x4*>(
+              base + at + (past ? off - 16 * g : off + 64 * s));
+          f[s] = once ? __builtin_nontemporal_load(from) : *from;
+          if (left < kStepBytes) f[s] = past ? bk_u32x4{0, 0, 0, 0} : f[s];
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < MT; ++i) get(p.A, offa[i], fa[u][i], false);
+      get(gate, offb, fb[u][0], true);
+      if constexpr (kGated) get(up, offb, fb[u][1], true);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (k0 + kRowsWaves * u >= nk) break;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) acc[i][j] = mma<DT>(fb[u][j], fa[u][i], acc[i][j]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) sums[wave][i * NB + j][lane] = acc[i][j];
+  __syncthreads();
+  // eight columns a thread: lanes 16 (2 h) + m and 16 (2 h + 1) + m of a tile
+  const int t = threadIdx.x;
+  if (t >= MT * 32) return;
+  const int m16 = t & 15, h = t >> 4 & 1, i = t >> 5;
+  const int m = 16 * i + m16, n = n0 + 8 * h;
+  if (m >= p.M || n >= p.N) return;
+  float z[8], u[8];
+  auto total = [&](int f, float (&v)[8]) {
+    bk_f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
+#pragma unroll
+    for (int w = 0; w < kRowsWaves; ++w) {
+      lo += sums[w][f][32 * h + m16];
+      hi += sums[w][f][32 * h + 16 + m16];
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = lo[r], v[4 + r] = hi[r];
+  };
+  total(i * NB, z);
+  if constexpr (kGated) total(i * NB + 1, u);
+  epilogue8<kGated, false>(p, m, n, z, u, Extra<kGated>{});
+}
+
+template <int DT, Form kForm>
+void launch_rows(const GemmArgs& a, hipStream_t st) {
+  const dim3 grid((a.N + 15) / 16);
+  if (a.M <= 16)
+    hipLaunchKernelGGL((gemm_rows_kernel<DT, kForm, 1>), grid, dim3(64 * kRowsWaves), 0, st, a);
+  else
+    hipLaunchKernelGGL((gemm_rows_kernel<DT, kForm, 2>), grid, dim3(64 * kRowsWaves), 0, st, a);
+}
+
 template <int DT, Form kForm, int BM, int BN, int WM, int WN, int NST, bool kOnce, bool kLines>
 void launch_ring_as(const GemmArgs& a, hipStream_t st) {
   hipLaunchKernelGGL((gemm_ring_kernel<DT, kForm, BM, BN, WM, WN, NST, kOnce, kLines>),
@@ -799,6 +906,12 @@ template <int DT, Form kForm>
 int32_t launch_form(int shape, const GemmArgs& a, hipStream_t st) {
   // gated: a wave's rows of B are the gate and the up rows of the same columns
   constexpr bool kGated = kForm == kGatedForm;
+  if constexpr (kForm == kLinearForm || kForm == kGatedForm) {
+    if (shape == kRowsShape) {
+      launch_rows<DT, kForm>(a, st);
+      return check_launch("product of few rows");
+    }
+  }
   if (shape == 0)
     launch_ring<DT, kForm, 32, 32, 16, kGated ? 32 : 16, 6, 6>(a, st);
   else if (shape == 1)

@@ -211,6 +211,32 @@ def test_every_shape(dtype, od, plan, monkeypatch):
         assert torch.equal(got, (x.double() @ w.double().t()).to(got.dtype))
 
 
+@pytest.mark.parametrize("T", [1, 15, 16, 17, 32])
+@pytest.mark.parametrize("dtype,od", TYPES)
+def test_few_rows(dtype, od, T, monkeypatch):
+    """The kernel of up to 32 rows: reductions of less than a step, that end inside
+    one, and of more steps than its waves take at once; more workgroups than the
+    compute units hold; columns that end inside a tile; NaN around the operands."""
+    monkeypatch.setenv("LORA_GEMM_PLAN", "4,1")
+    unit, es = {"bf16": (8, 2), "e4m3": (16, 1), "f32": (8, 4)}[dtype]
+    g = gen(500 + T)
+    for k, (K, O) in enumerate(((unit, 1), (64, 17), (272, 513), (2064, 250), (8208, 40),
+                                (144, 16391))):
+        _check_linear(T, K, O, dtype, od, "gelu", k % 2 == 0, k % 3 == 0, k % 2 == 1, T + k)
+        _check_gated(T, K, (O + 15) // 16 * 16, dtype, od, "silu", k % 2 == 0, k % 3 != 1, T + k)
+        x, xs = operand(g, T, K, dtype, 1.0, integer=True)
+        w, ws = operand(g, O, K, dtype, 1.0, integer=True)
+        around = []
+        for t in (x, w):
+            n = t.numel() * es
+            buf = torch.full((n + 512,), 255, dtype=torch.uint8, device="cuda")  # NaN in every type
+            view = buf[240:240 + n]
+            view.copy_(t.contiguous().view(torch.uint8).reshape(-1))
+            around.append(view.view(t.dtype).view(t.shape))
+        got = run_linear(*around, xs, ws, None, None, None, dtype, od, "none")
+        assert torch.equal(got, (x.double() @ w.double().t()).to(got.dtype)), (T, K, O)
+
+
 def test_linear_inf_and_nan_stay_in_their_rows():
     # K ends inside a tile step and T inside a tile: what lies past a row's end
     # is the next row, whose infinities and NaN must not come in
