@@ -105,8 +105,9 @@ __device__ __forceinline__ float bk_exp(float z) {
   const float p = z * kL;
   const float r = __builtin_fmaf(z, kLlo, __builtin_fmaf(z, kL, -p));
   const float e = __builtin_amdgcn_exp2f(p);
-  // past the range p is infinite and r no number: e alone is right there
-  return __builtin_fabsf(p) < 160.f ? __builtin_fmaf(e, r * 0.693147180559945309f, e) : e;
+  // From p = 128 on e is infinite, and with a residual of zero or below the
+  // correction would make a NaN of it: e alone is right there (a logistic of 0).
+  return __builtin_fabsf(p) < 128.f ? __builtin_fmaf(e, r * 0.693147180559945309f, e) : e;
 }
 // 1 / (1 + e^-z)
 __device__ __forceinline__ float bk_logistic(float z) {
