@@ -73,9 +73,13 @@ namespace {
 // and split.  The plan that the model picks is on average 0.5 to 3% slower
 // than the best of them; the largest shape that fills the units, else a split
 // that does, was 18% slower in bf16 (700 x 14336 x 4096: 178 us against 86).
-// Where memory and caches want different plans the middle is taken (256 x 4096
-// x 6144 bf16: one round of 64 x 64 tiles 25 us with operands in the last-level
-// cache, 37.5 from memory; 128 x 128 tiles in two parts 30 and 33.8).
+// Where memory and caches want different plans, memory's is taken: a layer's
+// weights are read from there, the other layers' having passed through the
+// caches since.  A step of 0.42 for two 64 x 64 bf16 tiles a unit, as measured
+// from the caches, changes 47 of 360 plans of 33 to 2048 rows; they are 10%
+// slower from memory on average and 5% faster from the caches (256 x 4096 x 6144:
+// one round of 64 x 64 tiles 35.5 and 25.1 us, 128 x 128 tiles in two parts 31.8
+// and 29.9; gated 300 x 4096 x 6144 69.5 and 55.2, 57.2 and 52.3).
 struct ShapeCost {
   float start, step[3];
 };
@@ -83,7 +87,7 @@ constexpr ShapeCost kCosts[4][kNumShapes] = {
     // fp32
     {{1.6f, {0.27f, 0.41f, 0.54f}}, {1.5f, {0.64f, 1.18f}}, {2.3f, {1.95f, 2.22f}}, {5.0f, {7.4f, 8.0f}}},
     // bf16
-    {{1.2f, {0.19f, 0.27f, 0.36f}}, {1.6f, {0.32f, 0.42f}}, {2.6f, {0.56f, 0.68f}}, {4.7f, {0.86f, 1.42f}}},
+    {{1.2f, {0.19f, 0.27f, 0.36f}}, {1.6f, {0.32f, 0.50f}}, {2.6f, {0.56f, 0.68f}}, {4.7f, {0.86f, 1.42f}}},
     // e4m3 with bf16 outputs, with fp32 outputs
     {{1.4f, {0.18f, 0.27f, 0.35f}}, {1.9f, {0.33f, 0.48f}}, {2.8f, {0.57f, 0.69f}}, {4.0f, {0.79f, 1.50f}}},
     {{1.8f, {0.29f, 0.36f, 0.39f}}, {2.2f, {0.35f, 0.60f}}, {2.3f, {1.05f, 1.14f}}, {4.3f, {3.4f, 3.7f}}}};
@@ -109,7 +113,7 @@ constexpr float kRowsRate = 4.4e6f;
 // smallest is 64 bytes, half a cache line; the middle one's workgroups, two a
 // unit, share most of what they load (gradients of 300 x 2048 x 2048 in one
 // launch: 57, 32 and 41 us in the three shapes).
-constexpr float kColumnsCost[kNumShapes] = {1.7f, 0.97f, 1.2f, 1.05f};
+constexpr float kColumnsCost[kNumShapes] = {1.7f, 0.85f, 1.2f, 1.05f};
 
 // workgroups of a shape that a compute unit holds
 constexpr int units_hold(int shape) { return shape < 2 ? 3 - shape : 1; }
