@@ -512,8 +512,10 @@ int32_t lora_apply_ranked(const lora_pool_desc* desc, const void* A_pool, const 
  * of a call does not depend on timing: no atomics, fixed orders.
  *
  * A call's workspace size depends on the descriptor and T alone; 0 means that
- * ws may be NULL.  Its contents need no preparation and mean nothing after
- * the call. */
+ * ws may be NULL.  It does not shrink as T grows: a workspace for the largest T
+ * serves every smaller one, and one for both gradients serves either alone.  It
+ * is at most 64 MiB + 256 bytes.  Its contents need no preparation and mean
+ * nothing after the call. */
 
 typedef enum {
   LORA_ACT_NONE = 0,       /* z */

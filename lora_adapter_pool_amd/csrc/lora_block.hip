@@ -1,8 +1,8 @@
 // Entry points of the decoder block's products: the base projection with its
 // epilogue, the gated feed-forward block and its gradients.  Every argument is
 // checked before the first HIP call; the plan of a product (tile shape, K
-// split) depends on sizes and types alone, so the workspace query and the call
-// agree.
+// split) and the workspace asked for depend on sizes and types alone (and on the
+// tuning overrides), so the workspace query and the call agree.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -124,6 +124,8 @@ constexpr float full_step(const ShapeCost& c, int shape) { return c.step[shape =
 constexpr float kLineBytes = 30e6f;
 
 constexpr int64_t kMaxPartials = 64 << 20;  // bytes
+constexpr int64_t kMostParts = 16;          // of a tile
+constexpr int kPairParts = 4;               // choices of them in one launch: 1, 2, 4, 8
 
 // `n` workgroups of `steps` steps.
 float round_time(const ShapeCost& c, int shape, int64_t n, int64_t steps) {
@@ -138,6 +140,10 @@ float round_time(const ShapeCost& c, int shape, int64_t n, int64_t steps) {
   }
   return us;
 }
+
+// A tile of 128 or 256 rows for at most 64 of them is never the fastest (none of
+// 400000 random products' plans had one), and its partials are the largest.
+bool shape_allowed(int shape, int64_t M) { return shape < 2 || M > 64; }
 
 // few rows
 float rows_time(Form form, int type, int64_t M, int64_t N, int64_t kb) {
@@ -170,7 +176,7 @@ GemmPlan gemm_plan(int32_t dtype, int32_t out_dtype, Form form, int64_t M, int64
     best = {kRowsShape, 1, 1, 0, rows_time(form, type, M, N, kb)};
   if (only_shape == kRowsShape) return best;
   for (int shape = 0; shape < kNumShapes; ++shape) {
-    if (only_shape >= 0 && shape != only_shape) continue;
+    if (only_shape >= 0 ? shape != only_shape : !shape_allowed(shape, M)) continue;
     const TileShape& sh = kShapes[shape];
     ShapeCost c = kCosts[type][shape];
     if (M <= sh.bm && (float)(M + width) * (float)kb > kColdBytes)
@@ -184,7 +190,7 @@ GemmPlan gemm_plan(int32_t dtype, int32_t out_dtype, Form form, int64_t M, int64
     // Whole rounds of tiles, one a compute unit, are not split; the tiles of the
     // last round may be, where they leave compute units idle.
     const int64_t rest = t % kComputeUnits;
-    for (int64_t s = 1; s <= 16; ++s) {
+    for (int64_t s = 1; s <= kMostParts; ++s) {
       const int64_t want = only_parts ? only_parts : s;
       const int64_t per = (steps + want - 1) / want, parts = (steps + per - 1) / per;
       GemmPlan g{shape, (int32_t)t, 1, 0, 0.f};
@@ -205,6 +211,35 @@ GemmPlan gemm_plan(int32_t dtype, int32_t out_dtype, Form form, int64_t M, int64
     }
   }
   return best;
+}
+
+// What the partials of a product take at most, over the plans of all M up to this
+// one and all reductions up to kb bytes: of one launched by itself (a split is
+// not refined once it makes more than four workgroups a unit), or of one that
+// shares its launch.
+static int64_t partials_bound(Form form, int64_t M, int64_t N, int64_t kb, bool pair) {
+  const int64_t width = form == kGatedForm ? 2 * N : N;
+  const int64_t steps = (kb + kStepBytes - 1) / kStepBytes;
+  const int64_t parts = std::min<int64_t>(pair ? 1 << (kPairParts - 1) : kMostParts, steps);
+  int64_t bytes = 0;
+  if (parts < 2) return 0;
+  for (int shape = 0; shape < (pair ? kPairShapes : kNumShapes); ++shape) {
+    if (!pair && !shape_allowed(shape, M)) continue;
+    const TileShape& sh = kShapes[shape];
+    const int64_t t = ((M + sh.bm - 1) / sh.bm) * ((width + sh.bn - 1) / sh.bn);
+    const int64_t rest = std::min<int64_t>(t, kComputeUnits - 1);
+    const int64_t n = pair ? rest * parts : std::min(rest * parts, 4 * kComputeUnits + rest);
+    bytes = std::max(bytes, n * sh.bm * sh.bn * 4);
+  }
+  return std::min(bytes, kMaxPartials);
+}
+
+// The workspace that a product asks for: enough for every M up to this one, so
+// that a buffer for the largest batch serves the smaller ones, whose plans may
+// split more.
+static int64_t gemm_workspace(const GemmPlan& plan, Form form, int64_t M, int64_t N, int64_t kb) {
+  return std::max(plan.ws_bytes,  // (a forced plan may take more)
+                  partials_bound(form, M, N, kb, false));
 }
 
 namespace {
@@ -311,12 +346,12 @@ BackwardPlan pair_plan(int32_t dtype, const int64_t (&M)[2], int64_t N, const in
     if (dtype == LORA_BF16)
       for (float& s : c.step) s *= kColumnsCost[shape];
     const float cap = (float)(units_hold(shape) * kComputeUnits), step = full_step(c, shape);
-    GemmPlan g[2][4];
-    float longest[2][4], work[2][4], join[2][4];
+    GemmPlan g[2][kPairParts];
+    float longest[2][kPairParts], work[2][kPairParts], join[2][kPairParts];
     for (int p = 0; p < 2; ++p) {
       const int64_t t = ((M[p] + sh.bm - 1) / sh.bm) * ((N + sh.bn - 1) / sh.bn);
       const int64_t steps = (kb[p] + kStepBytes - 1) / kStepBytes, rest = t % kComputeUnits;
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kPairParts; ++i) {
         const int64_t per = (steps + (1 << i) - 1) >> i, parts = (steps + per - 1) / per;
         const bool split = parts > 1 && rest;
         const int64_t bytes = split ? rest * parts * sh.bm * sh.bn * 4 : 0;
@@ -327,8 +362,8 @@ BackwardPlan pair_plan(int32_t dtype, const int64_t (&M)[2], int64_t N, const in
         join[p][i] = split ? kJoinStart + parts * kJoinPart + bytes * kJoinPerByte : 0.f;
       }
     }
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 4; ++j) {
+    for (int i = 0; i < kPairParts; ++i)
+      for (int j = 0; j < kPairParts; ++j) {
         if (only ? only[2] != '0' + i || only[4] != '0' + j
                  : g[0][i].ws_bytes + g[1][j].ws_bytes > kMaxPartials)
           continue;
@@ -355,13 +390,29 @@ BackwardPlan backward_plan(const lora_gated_desc& d, int64_t T, bool dx, bool dw
     // tuning overrides: "shape,i,j", or anything else for separate launches
     const char* f = std::getenv("LORA_GRAD_PAIR");
     const bool forced = f && std::strlen(f) == 5 && f[0] >= '0' && f[0] < '0' + kPairShapes &&
-                        f[2] >= '0' && f[2] < '4' && f[4] >= '0' && f[4] < '4';
+                        f[2] >= '0' && f[2] < '0' + kPairParts && f[4] >= '0' && f[4] < '0' + kPairParts;
     if (!forced && (f || std::getenv("LORA_GEMM_PLAN"))) return b;
     BackwardPlan p = pair_plan(d.dtype, {T, I2}, K, {e * I2, e * T}, forced ? f : nullptr);
     p.total = std::max(p.total, b.total);  // (either gradient alone fits as well)
     if (forced || p.dx.us < b.dx.us + b.dw.us + kLaunchGap) return p;
   }
   return b;
+}
+
+// What the gradients ask for: enough for every T up to this one, and for either
+// gradient alone.
+int64_t backward_workspace(const BackwardPlan& plan, const lora_gated_desc& d, int64_t T, bool dx,
+                           bool dw) {
+  const int64_t e = esize(d.dtype), K = d.in_features, I2 = 2 * (int64_t)d.inter_features;
+  int64_t n = plan.total;  // (a forced plan may take more)
+  if (dx) n = std::max(n, partials_bound(kGradX, T, K, e * I2, false));
+  if (dw) n = std::max(n, partials_bound(kGradW, I2, K, e * T, false));
+  if (dx && dw) {
+    const int64_t both = align_up(partials_bound(kGradX, T, K, e * I2, true), 256) +
+                         partials_bound(kGradW, I2, K, e * T, true);
+    n = std::max(n, std::min(both, kMaxPartials + 256));
+  }
+  return n;
 }
 
 // ------------------------------------------------------------------ checks
@@ -455,9 +506,10 @@ int64_t lora_linear_workspace_bytes(const lora_linear_desc* desc, int32_t T) {
   if (int32_t e = check_linear(desc)) return e;
   if (int32_t e = check_rows(T)) return e;
   if (T == 0) return 0;
-  return gemm_plan(desc->dtype, desc->out_dtype, kLinearForm, T, desc->out_features,
-                   desc->in_features * esize(desc->dtype))
-      .ws_bytes;
+  const int64_t kb = desc->in_features * esize(desc->dtype);
+  return gemm_workspace(
+      gemm_plan(desc->dtype, desc->out_dtype, kLinearForm, T, desc->out_features, kb), kLinearForm,
+      T, desc->out_features, kb);
 }
 
 int32_t lora_linear(const lora_linear_desc* desc, const void* x, const void* w,
@@ -477,7 +529,9 @@ int32_t lora_linear(const lora_linear_desc* desc, const void* x, const void* w,
   if (int32_t e = need(out, "out")) return e;
   const int64_t kb = desc->in_features * esize(desc->dtype);
   const GemmPlan plan = gemm_plan(desc->dtype, desc->out_dtype, kLinearForm, T, desc->out_features, kb);
-  if (int32_t e = check_ws(ws, ws_bytes, plan.ws_bytes)) return e;
+  if (int32_t e = check_ws(ws, ws_bytes,
+                           gemm_workspace(plan, kLinearForm, T, desc->out_features, kb)))
+    return e;
   GemmArgs a{};
   a.A = (const char*)x;
   a.B = (const char*)w;
@@ -500,9 +554,10 @@ int64_t lora_gated_ffn_workspace_bytes(const lora_gated_desc* desc, int32_t T) {
   if (int32_t e = check_gated(desc)) return e;
   if (int32_t e = check_rows(T)) return e;
   if (T == 0) return 0;
-  return gemm_plan(desc->dtype, desc->out_dtype, kGatedForm, T, desc->inter_features,
-                   desc->in_features * esize(desc->dtype))
-      .ws_bytes;
+  const int64_t kb = desc->in_features * esize(desc->dtype);
+  return gemm_workspace(
+      gemm_plan(desc->dtype, desc->out_dtype, kGatedForm, T, desc->inter_features, kb), kGatedForm,
+      T, desc->inter_features, kb);
 }
 
 int32_t lora_gated_ffn(const lora_gated_desc* desc, const void* x, const void* w,
@@ -520,7 +575,9 @@ int32_t lora_gated_ffn(const lora_gated_desc* desc, const void* x, const void* w
   if (int32_t e = need(out, "out")) return e;
   const int64_t kb = desc->in_features * esize(desc->dtype);
   const GemmPlan plan = gemm_plan(desc->dtype, desc->out_dtype, kGatedForm, T, desc->inter_features, kb);
-  if (int32_t e = check_ws(ws, ws_bytes, plan.ws_bytes)) return e;
+  if (int32_t e = check_ws(ws, ws_bytes,
+                           gemm_workspace(plan, kGatedForm, T, desc->inter_features, kb)))
+    return e;
   GemmArgs a{};
   a.A = (const char*)x;
   a.B = (const char*)w;
@@ -552,7 +609,8 @@ int64_t lora_gated_ffn_backward_workspace_bytes(const lora_gated_desc* desc, int
   if (int32_t e = check_backward(desc)) return e;
   if (int32_t e = check_rows(T)) return e;
   if (T == 0) return 0;
-  return backward_plan(*desc, T, need_dx != 0, need_dw != 0).total;
+  const bool dx = need_dx != 0, dw = need_dw != 0;
+  return backward_workspace(backward_plan(*desc, T, dx, dw), *desc, T, dx, dw);
 }
 
 int32_t lora_gated_ffn_backward(const lora_gated_desc* desc, const void* dout, const void* pre,
@@ -583,7 +641,9 @@ int32_t lora_gated_ffn_backward(const lora_gated_desc* desc, const void* dout, c
     if (int32_t e = need(w, "w")) return e;
   }
   const BackwardPlan b = backward_plan(*desc, T, dx != nullptr, dw != nullptr);
-  if (int32_t e = check_ws(ws, ws_bytes, b.total)) return e;
+  if (int32_t e = check_ws(ws, ws_bytes,
+                           backward_workspace(b, *desc, T, dx != nullptr, dw != nullptr)))
+    return e;
 
   // (a grid holds less than 2^32 threads)
   const dim3 grid((unsigned)std::min<int64_t>(((int64_t)T * (I / 8) + 255) / 256, 1 << 23));
