@@ -10,6 +10,10 @@ deltas are LoraPool.apply onto zeros; they join the base products before the
 activation, inside the products' epilogues.  LoraMlp owns the descriptors and
 one workspace; weights and pools belong to the caller.  Calls run on the current
 stream, and those of one LoraMlp share its workspace: use one per stream.
+
+A call that needs a larger workspace gets a new one, and the old one is kept as
+long as the LoraMlp: a graph that was captured before holds its address.  Keep
+the LoraMlp, then, as long as the graphs that its calls were captured in.
 """
 from __future__ import annotations
 
@@ -63,11 +67,16 @@ class LoraMlp:
         self.grad_desc = L.make_gated_desc(self.dtype, self.dtype, self.H, self.I, act)
         self.down_desc = L.make_linear_desc(self.dtype, self.dtype, self.I, self.H)
         self._ws = None
+        self._outgrown = []
         self._saved = None
 
     def _workspace(self, need: int):
-        if self._ws is None or self._ws.numel() < need:
-            self._ws = self.torch.empty(max(need, 256), dtype=self.torch.uint8,
+        have = 0 if self._ws is None else self._ws.numel()
+        if have < max(need, 1):
+            if have:
+                self._outgrown.append(self._ws)
+            # at least twice as large: the outgrown ones add up to no more than the last
+            self._ws = self.torch.empty(max(need, 2 * have, 256), dtype=self.torch.uint8,
                                         device=self.w_down.device)
         return self._ws
 

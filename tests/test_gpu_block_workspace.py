@@ -46,3 +46,34 @@ def test_one_workspace_for_all_batches(dtype, K, I):
                                   need)
         assert torch.equal(dw, run_backward(dout, pre, x, w, "silu", dtype, dx=False)[2])
         assert (buf[need:] == 90).all(), T
+
+
+def test_a_captured_forward_outlives_a_larger_call():
+    """A graph of a small batch, then an eager call of a larger one, whose
+    workspace is larger: the graph's replays are still right, and write into
+    nobody else's memory."""
+    H, I, T = 2048, 512, 8
+    g = gen(21)
+    w = [normal(g, (H,), "bf16"), normal(g, (2 * I, H), "bf16", H ** -0.5),
+         normal(g, (H, I), "bf16", I ** -0.5)]
+    mlp = L.LoraMlp(*w)
+    x, r = normal(g, (T, H), "bf16"), normal(g, (T, H), "bf16")
+    mlp.forward(x, r)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = mlp.forward(x, r)
+    before = mlp._ws.numel()
+    xl = normal(g, (600, H), "bf16")
+    mlp.forward(xl, torch.zeros_like(xl))
+    assert mlp._ws.numel() > before
+    # takes what the allocator has to give back of the old workspace's size
+    others = [torch.full((before,), 85, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    for k in range(4):
+        x.copy_(normal(g, (T, H), "bf16"))
+        y.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = y.clone()
+        assert torch.equal(got, L.LoraMlp(*w).forward(x, r)), k
+        assert all((t == 85).all() for t in others), k

@@ -1,4 +1,7 @@
 """LoraMlp's checks of weights, pools and rows, on the CPU (nothing is launched)."""
+import gc
+import weakref
+
 import pytest
 import torch
 
@@ -58,3 +61,17 @@ def test_row_refusals():
     assert e.value.status == _lib.LORA_E_ARG
     with pytest.raises(L.LoraError):
         m.gate_up_backward(torch.zeros(4, 72, dtype=torch.bfloat16))        # nothing kept
+
+
+def test_an_outgrown_workspace_lives_as_long_as_the_block():
+    """A captured graph holds its address: the memory must not go to another
+    tensor when a later call needs more."""
+    m = L.LoraMlp(*weights())
+    sizes = (0, 300, 100, 301, 5000, 4000, 70000)
+    held = [weakref.ref(m._workspace(n)) for n in sizes]
+    assert all(m._workspace(n).numel() >= n for n in sizes)
+    gc.collect()
+    assert all(r() is not None for r in held)
+    assert held[1]() is held[2]() and held[4]() is held[5]()       # grown only where needed
+    kept = {id(r()): r().numel() for r in held}
+    assert sum(kept.values()) <= 2 * m._workspace(0).numel()       # and not without end
