@@ -190,7 +190,9 @@ def pycall():
     apply, apply_ranked, apply_device and the decoder-block operators), built
     beside the library; raise if it was not built.  Each function takes the
     entry point's address (see entry_address) and then that entry point's
-    arguments: ints, tensors or numpy arrays for pointers, None for NULL."""
+    arguments: ints for pointers, None for NULL.  The decoder-block operators
+    also take tensors; one that is not GPU memory, not contiguous or smaller than
+    the call takes it to be is refused with a LoraError."""
     global _pycall
     if _pycall is None:
         try:
@@ -199,6 +201,7 @@ def pycall():
             raise RuntimeError(
                 "the _lora_call binding is missing: build it with "
                 "`python -m lora_adapter_pool_amd.build`") from e
+        _lora_call.set_error(LoraError)
         _pycall = _lora_call
     return _pycall
 

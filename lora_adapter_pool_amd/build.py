@@ -5,6 +5,7 @@ Usage: python -m lora_adapter_pool_amd.build   (or build_library() from Python)
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -93,14 +94,17 @@ def pycall_path() -> str:
 
 
 def build_pycall(verbose: bool = False) -> str:
-    """The CPython binding of the per-call entry points (host code, gcc)."""
+    """The CPython binding of the per-call entry points (host code, gcc); torch's
+    headers hold the C interface to its tensors."""
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
     cc = shutil.which("gcc") or shutil.which("cc")
     if not cc:
         raise RuntimeError("gcc not found")
     out = pycall_path()
     tmp = out + ".tmp"
     cmd = [cc, "-O2", "-std=gnu11", "-shared", "-fPIC", "-Wall", "-Werror",
-           f"-I{sysconfig.get_paths()['include']}", f"-I{INCLUDE}", PYCALL_SRC, "-o", tmp]
+           f"-I{sysconfig.get_paths()['include']}", f"-I{INCLUDE}", "-isystem",
+           os.path.join(torch_dir, "include"), PYCALL_SRC, "-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
