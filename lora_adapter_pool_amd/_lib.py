@@ -522,21 +522,43 @@ _DTYPE_CODES = {"f32": LORA_F32, "fp32": LORA_F32, "float32": LORA_F32,
                 "e4m3": LORA_E4M3, "float8_e4m3fn": LORA_E4M3}
 
 
+def _choice(table: dict, key, what: str, status: int) -> int:
+    if key not in table:
+        raise LoraError(status, f"unknown {what} {key!r}: one of {', '.join(table)}")
+    return table[key]
+
+
+def _dtype(name) -> int:
+    return _choice(_DTYPE_CODES, name, "dtype", LORA_E_DTYPE)
+
+
+def _act(name) -> int:
+    return _choice(ACTS, name, "activation", LORA_E_ARG)
+
+
+def _features(n, what: str) -> int:
+    if int(n) != n or not -1 << 31 <= n < 1 << 31:   # (a field of the descriptor would wrap)
+        raise LoraError(LORA_E_SHAPE, f"{what} must be a whole number of 32 bits, got {n!r}")
+    return int(n)
+
+
 def make_norm_desc(dtype: str, hidden: int, eps: float) -> lora_norm_desc:
     """Descriptor of lora_add_rms_norm (keep it: it is read at every call)."""
-    return lora_norm_desc(_DTYPE_CODES[dtype], int(hidden), float(eps), 0)
+    return lora_norm_desc(_dtype(dtype), _features(hidden, "hidden"), float(eps), 0)
 
 
 def make_linear_desc(dtype: str, out_dtype: str, in_features: int, out_features: int,
                      act: str = "none") -> lora_linear_desc:
-    return lora_linear_desc(_DTYPE_CODES[dtype], _DTYPE_CODES[out_dtype], int(in_features),
-                            int(out_features), ACTS[act], 0)
+    return lora_linear_desc(_dtype(dtype), _dtype(out_dtype),
+                            _features(in_features, "in_features"),
+                            _features(out_features, "out_features"), _act(act), 0)
 
 
 def make_gated_desc(dtype: str, out_dtype: str, in_features: int, inter_features: int,
                     act: str = "silu") -> lora_gated_desc:
-    return lora_gated_desc(_DTYPE_CODES[dtype], _DTYPE_CODES[out_dtype], int(in_features),
-                           int(inter_features), ACTS[act], 0)
+    return lora_gated_desc(_dtype(dtype), _dtype(out_dtype),
+                           _features(in_features, "in_features"),
+                           _features(inter_features, "inter_features"), _act(act), 0)
 
 
 def lora_add_rms_norm(desc, x, residual, weight, sum, out, out8, scale, T, stream=None) -> None:

@@ -44,6 +44,8 @@ class LoraMlp:
                               "an e4m3 w_gate_up needs gate_up_scale and bf16 activations")
         if not self.eight and w_gate_up.dtype != w_down.dtype:
             raise L.LoraError(L.LORA_E_DTYPE, "w_gate_up must be e4m3 or of w_down's dtype")
+        if w_down.dim() != 2:
+            raise L.LoraError(L.LORA_E_SHAPE, "w_down must be [H, I]")
         self.H, self.I = int(w_down.shape[0]), int(w_down.shape[1])
         if tuple(w_gate_up.shape) != (2 * self.I, self.H) or tuple(norm_weight.shape) != (self.H,):
             raise L.LoraError(L.LORA_E_SHAPE, "w_gate_up must be [2 I, H] and norm_weight [H]")
