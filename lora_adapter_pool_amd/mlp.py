@@ -9,7 +9,8 @@ Every row names its adapter slot in each pool, or none (-1).  The adapters'
 deltas are LoraPool.apply onto zeros; they join the base products before the
 activation, inside the products' epilogues.  LoraMlp owns the descriptors and
 one workspace; weights and pools belong to the caller.  Calls run on the current
-stream, and those of one LoraMlp share its workspace: use one per stream.
+stream of the weights' GPU, whichever GPU is the current one, and those of one
+LoraMlp share its workspace: use one per stream.
 
 A call that needs a larger workspace gets a new one, and the old one is kept as
 long as the LoraMlp: a graph that was captured before holds its address.  Keep
@@ -56,6 +57,8 @@ class LoraMlp:
             if pool is not None and (pool.K != K or pool.out_features != outs or
                                      pool.dtype != self.dtype):
                 raise L.LoraError(L.LORA_E_SHAPE, "a pool does not fit the block")
+            if pool is not None and pool.A.device != w_down.device:
+                raise L.LoraError(L.LORA_E_ARG, "a pool is not on the weights' device")
         for t in (norm_weight, w_gate_up, w_down, gate_up_scale):
             if t is not None and not t.is_contiguous():
                 raise L.LoraError(L.LORA_E_SHAPE, "weights must be contiguous")
@@ -86,6 +89,14 @@ class LoraMlp:
         if not self.w_down.is_cuda:
             raise L.LoraError(L.LORA_E_ARG, "the block's weights are not on a GPU")
 
+    def _on_device(self, call, *args):
+        """call(*args) with the weights' GPU as the current one (launches go to the
+        current GPU's stream)."""
+        if self.torch.cuda.current_device() == self.w_down.device.index:
+            return call(*args)
+        with self.torch.cuda.device(self.w_down.device):
+            return call(*args)
+
     def _check_rows(self, t, width: int, name: str):
         if t.dtype != self.w_down.dtype or t.device != self.w_down.device:
             raise L.LoraError(L.LORA_E_DTYPE, f"{name} must have the weights' dtype and device")
@@ -93,14 +104,18 @@ class LoraMlp:
             raise L.LoraError(L.LORA_E_SHAPE, f"{name} must be a contiguous [T, {width}]")
 
     def forward(self, x, residual, ids=None, prefill=None, keep: bool = False):
-        """y [T][H] on the current stream.  ids, prefill: as LoraPool.apply takes
-        them (None: no adapters).  keep: hold what gate_up_backward needs."""
-        torch = self.torch
+        """y [T][H] on the current stream of the weights' GPU.  ids, prefill: as
+        LoraPool.apply takes them (None: no adapters).  keep: hold what
+        gate_up_backward needs."""
         self._check_rows(x, self.H, "x")
         self._check_rows(residual, self.H, "residual")
         if residual.shape != x.shape:
             raise L.LoraError(L.LORA_E_SHAPE, "x and residual must have the same shape")
         self._check_device()
+        return self._on_device(self._forward, x, residual, ids, prefill, keep)
+
+    def _forward(self, x, residual, ids, prefill, keep):
+        torch = self.torch
         T, H, I = int(x.shape[0]), self.H, self.I
         new = lambda *s: torch.empty(s, dtype=x.dtype, device=x.device)  # noqa: E731
         s, n, h, y = new(T, H), new(T, H), new(T, I), new(T, H)
@@ -134,12 +149,15 @@ class LoraMlp:
             raise L.LoraError(L.LORA_E_ARG, "no forward pass was kept (keep=True)")
         if self.eight:
             raise L.LoraError(L.LORA_E_DTYPE, "the gradients take weights in fp32 or bf16")
+        self._check_rows(dh, self.I, "dh")
+        if dh.shape[0] != self._saved[0].shape[0]:
+            raise L.LoraError(L.LORA_E_SHAPE, "dh must have the kept pass's rows")
+        return self._on_device(self._gate_up_backward, dh, need_dw)
+
+    def _gate_up_backward(self, dh, need_dw):
+        torch = self.torch
         n, pre = self._saved
         T = int(n.shape[0])
-        self._check_rows(dh, self.I, "dh")
-        if dh.shape[0] != T:
-            raise L.LoraError(L.LORA_E_SHAPE, "dh must have the kept pass's rows")
-        torch = self.torch
         dpre, dn = torch.empty_like(pre), torch.empty_like(n)
         dw = torch.empty_like(self.w_gate_up) if need_dw else None
         ws = self._workspace(L.lora_gated_ffn_backward_workspace_bytes(self.grad_desc, T, True,
