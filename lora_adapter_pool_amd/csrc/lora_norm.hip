@@ -115,7 +115,18 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs a) {
     ss = 0.0;
     for (int i = 0; i < waves; ++i) ss += sums[i];  // same order in every thread
   }
-  const float rstd = (float)reciprocal_root(__builtin_fma(ss, a.over_h, a.eps));
+  const double root = reciprocal_root(__builtin_fma(ss, a.over_h, a.eps));
+  float rstd = (float)root;
+  // A row of numbers below 2^-128, or near the largest, has a factor that fp32
+  // does not hold, or not with all its bits: part of it goes to the row first.
+  if (root > 0x1p120 || root < 0x1p-120) {
+    const float part = root > 1.0 ? 0x1p64f : 0x1p-64f;
+    rstd = (float)(root * (root > 1.0 ? 0x1p-64 : 0x1p64));
+#pragma unroll
+    for (int j = 0; j < NP; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[j][i] *= part;
+  }
 
   uint32_t top = 0;  // largest |n| by its bits, which also keeps a NaN
 #pragma unroll
