@@ -118,7 +118,10 @@ class LoraMlp:
         torch = self.torch
         T, H, I = int(x.shape[0]), self.H, self.I
         new = lambda *s: torch.empty(s, dtype=x.dtype, device=x.device)  # noqa: E731
-        s, n, h, y = new(T, H), new(T, H), new(T, I), new(T, H)
+        # n in the activations' type is read by the adapters, or by 16- and 32-bit weights
+        adapters = self.gate_up is not None and ids is not None
+        n = new(T, H) if adapters or not self.eight else None
+        s, h, y = new(T, H), new(T, I), new(T, H)
         n8 = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=x.device) if self.eight else None
         scale = torch.empty(T, device=x.device) if self.eight else None
         pre = new(T, 2 * I) if keep else None
