@@ -507,15 +507,24 @@ int32_t lora_apply_ranked(const lora_pool_desc* desc, const void* A_pool, const 
  * matrices are device memory, row-major and contiguous; every pointer is
  * 16-byte aligned; calls are asynchronous on `stream`, allocate nothing, and
  * can be captured in a graph.  T is at most 2^21; T = 0 is a no-op (except that
- * a gradient of the weights over no tokens is zero).  Sums and statistics are kept in fp32 or
- * wider and every output is rounded once (nearest, ties to even).  The result
- * of a call does not depend on timing: no atomics, fixed orders.
+ * a gradient of the weights over no tokens is zero).  Sums and statistics are
+ * kept in fp32 or wider and every output is rounded once (nearest, ties to even).
+ * The result of a call does not depend on timing: no atomics, fixed orders.
  *
- * A call's workspace size depends on the descriptor and T alone; 0 means that
- * ws may be NULL.  It does not shrink as T grows: a workspace for the largest T
- * serves every smaller one, and one for both gradients serves either alone.  It
- * is at most 64 MiB + 256 bytes.  Its contents need no preparation and mean
- * nothing after the call. */
+ * A call's workspace size depends on the descriptor and T alone (and on the
+ * tuning overrides below); 0 means that ws may be NULL.  It does not shrink as T
+ * grows: a workspace for the largest T serves every smaller one, and one for
+ * both gradients serves either alone.  It is at most 64 MiB + 256 bytes.  Its
+ * contents need no preparation and mean nothing after the call.
+ *
+ * Tuning overrides, read from the environment at every query and call, for
+ * measurements and tests: LORA_GEMM_PLAN=shape,parts (tile shape 0 to 3, or 4 for
+ * up to 32 rows; parts of the reduction), LORA_GEMM_LINES=0 or 1 (loads of whole
+ * cache lines), LORA_GRAD_PAIR=shape,i,j (both gradients in one launch, in 2^i and
+ * 2^j parts) or off.  A forced split may need more than 64 MiB, and a call refuses
+ * a workspace that was sized under another setting and is too small.  As for
+ * every environment variable, no thread may change them while another is in a
+ * call. */
 
 typedef enum {
   LORA_ACT_NONE = 0,       /* z */
@@ -555,7 +564,9 @@ typedef struct {
  *   t = round_dtype(x + residual)          (t = x without a residual)
  *   n = t * (mean_H(t^2) + eps)^(-1/2) * weight
  *   sum = t;  out = round_dtype(n)
- *   scale[t] = max(max_H |n| / 448, 2^-126);  out8 = e4m3(n / scale[t])
+ *   scale[t] = max(max_H |n| / 448, 2^-126);  out8 = e4m3(n r[t]),
+ *   r[t] = 1 / scale[t] rounded to fp32 (so out8 differs from e4m3(n / scale[t])
+ *   only where the quotient is within 2^-22 of itself of a rounding border)
  *   x, residual, sum, out [T][H], weight [H], out8 [T][H] e4m3, scale [T] fp32
  * residual and sum are given together or both NULL; out8 and scale likewise;
  * out may be NULL where out8 is given.  sum and out may be x or residual

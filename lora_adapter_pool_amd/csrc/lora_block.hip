@@ -68,11 +68,13 @@ namespace {
 // and a step of kStepBytes.  A compute unit holds up to three workgroups of the
 // smallest shape and two of the next: their step with one, two and three on the
 // busiest unit.  It holds one of the others: their step where few units run and
-// where all do.  Fitted to 5800 times of products of 1 to 8960 rows and 256 to
-// 20000 columns and terms, rows of whole cache lines and not, under every shape
-// and split.  The plan that the model picks is on average 0.5 to 3% slower
-// than the best of them; the largest shape that fills the units, else a split
-// that does, was 18% slower in bf16 (700 x 14336 x 4096: 178 us against 86).
+// where all do.  Fitted to times of products of 1 to 8960 rows, rows of whole
+// cache lines and not, under every shape and split.  Over 600 random products
+// with their weights in memory the plan that the model picks is 0.6 to 4.6%
+// slower than the best shape and split (means by type and rows), and at worst
+// 38% (978 x 256 x 4160 bf16: four steps a tile).  The largest shape that fills
+// the units, else a split that does, takes 178 us instead of 86 for 700 x 14336
+// x 4096 bf16.
 // Where memory and caches want different plans, memory's is taken: a layer's
 // weights are read from there, the other layers' having passed through the
 // caches since.  A step of 0.42 for two 64 x 64 bf16 tiles a unit, as measured
@@ -103,9 +105,9 @@ constexpr float kJoinPerByte = 0.2e-6f;  // partials written and read again
 
 // gemm_rows_kernel: its start, a step of each of its waves for 16 rows of B and
 // for a row of A (fp32: more products a byte), and what it reads of B a
-// microsecond at most.  Fitted to 750 times of 1 to 32 rows against the other
-// shapes': the pick is on average 1.4% slower than the better of the two, and at
-// worst 18% slower than the other shapes alone.
+// microsecond at most.  Fitted to times of 1 to 32 rows beside the other shapes':
+// over 260 random products of such rows the pick is 0.6 to 2.3% slower than the
+// best (means by type), and at worst 27% (3 x 11776 x 14976 e4m3 to fp32).
 constexpr float kRowsStart = 0.5f, kRowsStepB = 0.6f, kRowsStepA = 0.028f, kRowsF32 = 1.5f;
 constexpr float kRowsRate = 4.4e6f;
 

@@ -780,7 +780,10 @@ __global__ __launch_bounds__(512, 2) void gemm_phase_kernel(GemmArgs p) {
 // every 16 columns.  Against the ring and its join, bf16: 1 x 4096 x 4096
 // 9.3 us (ring 11.1), gated 1 x 4096 x 4096 16.3 (19.6), 16 x 2048 x 2048 6.4
 // (8.8), but 1 x 14336 x 4096 27 (23) and 32 x 14336 x 4096 50 (28); e4m3 1 x
-// 4096 x 4096 7.2 (10.7).
+// 4096 x 4096 7.2 (10.7).  B's loads are non-temporal also where rows do not start at a
+// cache line and two waves share one, unlike the ring's: 15 such sizes take the
+// same time within 1% either way, from memory and from the caches (1 x 4104 x
+// 4096 bf16 9.0 and 6.6 us).
 template <int DT, Form kForm, int MT>
 __global__ __launch_bounds__(64 * kRowsWaves) void gemm_rows_kernel(GemmArgs p) {
   constexpr bool kGated = kForm == kGatedForm;

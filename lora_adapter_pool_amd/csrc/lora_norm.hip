@@ -2,14 +2,16 @@
 //
 //   t = round(x + residual)                      (the stream the next layer reads)
 //   n = t * (mean(t^2) + eps)^(-1/2) * weight
-//   out = round(n);  scale = max(max |n| / 448, 2^-126);  out8 = e4m3(n / scale)
+//   out = round(n);  scale = max(max |n| / 448, 2^-126);  out8 = e4m3(n r),
+//   r = 1 / scale rounded to fp32
 //
 // One pass over memory: a row stays in registers (up to four pieces of eight
 // elements a thread) between the statistic and the outputs, so the bytes are
 // x and the residual once in, every output once out.  The row's statistic
-// is summed in 64 bits: the rounding of n / scale to 8 bits has borders, and a
+// is summed in 64 bits: the rounding of n r to 8 bits has borders, and a
 // statistic that is right to 32 bits leaves n with the three roundings of its
-// products alone.  The workgroup size is the row's, because a row's latency
+// products alone.  (n r differs from n / scale in its last bits, so from e4m3 of
+// the quotient only at such a border.)  The workgroup size is the row's, because a row's latency
 // (load, two reductions, store) is what a small batch waits for; large batches
 // run at the rate of a copy (8960 x 4096 bf16 with residual and 8-bit output:
 // 330 MB in 61 us, 5.4 TB/s).
