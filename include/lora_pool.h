@@ -619,6 +619,59 @@ int32_t lora_gated_ffn_backward(const lora_gated_desc* desc, const void* dout, c
                                 const void* x, const void* w, void* dpre, void* dx, void* dw,
                                 int32_t T, void* ws, int64_t ws_bytes, void* stream);
 
+/* What joins a block's output to the residual stream and opens the next block
+ * (models with a norm after the block, a gate or scales on its branch):
+ *   p = y (mean_H(y^2) + eps)^(-1/2) post_weight             (p = y without one)
+ *   t = round_dtype(residual_scale residual + block_scale gate p)
+ *   n = t (mean_H(t^2) + eps)^(-1/2) pre_weight
+ *   sum = t;  out = round_dtype(n);  out8 and scale from n as lora_add_rms_norm's
+ *   y, residual, sum, out [T][H], post_weight, pre_weight [H], out8 [T][H] e4m3,
+ *   scale [T] fp32; gate: none (1), one a channel [H], or one an element [T][H]
+ * post_weight may be NULL; pre_weight is given where out or out8 is, and else
+ * NULL; out8 and scale go together.  sum and out may be y, residual or an
+ * element gate themselves (in place), and not each other; other overlaps are not
+ * allowed. */
+typedef enum { LORA_GATE_NONE = 0, LORA_GATE_CHANNEL = 1, LORA_GATE_ELEMENT = 2 } lora_gate;
+
+typedef struct {
+  int32_t dtype;         /* LORA_F32 or LORA_BF16: every array but out8 and scale */
+  int32_t hidden;        /* H: a multiple of 8, at most 16384 */
+  float eps;
+  int32_t gate;          /* lora_gate */
+  float residual_scale;  /* finite */
+  float block_scale;     /* finite */
+  int32_t reserved[2];   /* 0 */
+} lora_block_norm_desc;
+
+int32_t lora_block_norm(const lora_block_norm_desc* desc, const void* y, const void* residual,
+                        const void* gate, const void* post_weight, const void* pre_weight,
+                        void* sum, void* out, void* out8, float* scale, int32_t T, void* stream);
+
+/* Its gradients, from dout (of out), dsum (of sum by what else reads the stream)
+ * and the y and sum of the forward pass (sum as it was rounded):
+ *   dt = dsum + d out / d t applied to dout
+ *   dresidual = residual_scale dt,  dgate = block_scale dt p,
+ *   dy = d p / d y applied to block_scale gate dt
+ * and the weights' gradients, each from the unrounded values.
+ *   dout, dsum, dy, dresidual [T][H] of the descriptor's dtype; dgate: [T][H] of
+ *   that dtype for an element gate, fp32 [H] for a channel gate; dpost_weight,
+ *   dpre_weight fp32 [H]
+ * dout goes with pre_weight and needs sum; dsum may be NULL where dout is given;
+ * y may be NULL without post_weight and gate.  dgate, dpost_weight and
+ * dpre_weight may be NULL.  The fp32 sums over the rows are overwritten, or added
+ * to what is there where accumulate is 1 (for T = 0: zero, or left).  With
+ * residual_scale = block_scale = 1, no gate and no post_weight these are the
+ * gradients of lora_add_rms_norm (of out; dy = dresidual).  In place: dy may be y,
+ * dout or dsum, dresidual may be dout or dsum (each another one), and dgate an
+ * element gate; other overlaps are not allowed. */
+int64_t lora_block_norm_backward_workspace_bytes(const lora_block_norm_desc* desc, int32_t T);
+int32_t lora_block_norm_backward(const lora_block_norm_desc* desc, const void* dout,
+                                 const void* dsum, const void* y, const void* sum,
+                                 const void* gate, const void* post_weight,
+                                 const void* pre_weight, void* dy, void* dresidual, void* dgate,
+                                 float* dpost_weight, float* dpre_weight, int32_t accumulate,
+                                 int32_t T, void* ws, int64_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

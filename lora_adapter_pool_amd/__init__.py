@@ -16,6 +16,8 @@ from ._lib import (  # noqa: F401
     LORA_E4M3, make_norm_desc, make_linear_desc, make_gated_desc, lora_add_rms_norm,
     lora_linear, lora_linear_workspace_bytes, lora_gated_ffn, lora_gated_ffn_workspace_bytes,
     lora_gated_ffn_backward, lora_gated_ffn_backward_workspace_bytes,
+    make_block_norm_desc, lora_block_norm, lora_block_norm_backward,
+    lora_block_norm_backward_workspace_bytes,
 )
 from .mlp import LoraMlp  # noqa: F401
 from .pool import LoraPool  # noqa: F401

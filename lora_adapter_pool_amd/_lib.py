@@ -35,6 +35,7 @@ LORA_F32 = 0
 LORA_BF16 = 1
 LORA_E4M3 = 2
 ACTS = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3, "relu": 4}
+GATES = {"none": 0, "channel": 1, "element": 2}
 LORA_MAX_SLICES = 8
 LORA_BGMV_MAX_RANK_DEFAULT = 64
 
@@ -55,6 +56,12 @@ class lora_pool_desc(ctypes.Structure):
 class lora_norm_desc(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("hidden", ctypes.c_int32), ("eps", ctypes.c_float),
                 ("reserved", ctypes.c_int32)]
+
+
+class lora_block_norm_desc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("hidden", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("gate", ctypes.c_int32), ("residual_scale", ctypes.c_float),
+                ("block_scale", ctypes.c_float), ("reserved", ctypes.c_int32 * 2)]
 
 
 class lora_linear_desc(ctypes.Structure):
@@ -104,6 +111,7 @@ _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _DP = ctypes.POINTER(lora_pool_desc)
 _NP = ctypes.POINTER(lora_norm_desc)
+_BP = ctypes.POINTER(lora_block_norm_desc)
 _LP = ctypes.POINTER(lora_linear_desc)
 _GP = ctypes.POINTER(lora_gated_desc)
 
@@ -143,6 +151,9 @@ _SIGNATURES = {
     "lora_apply_ranked": (_I32, [_DP, _P, _P, _P, _P, _I32, _P, _P, _I32, _P, _P, _I64, _P, _I64,
                                  _P]),
     "lora_add_rms_norm": (_I32, [_NP, _P, _P, _P, _P, _P, _P, _P, _I32, _P]),
+    "lora_block_norm": (_I32, [_BP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I32, _P]),
+    "lora_block_norm_backward_workspace_bytes": (_I64, [_BP, _I32]),
+    "lora_block_norm_backward": (_I32, [_BP] + [_P] * 12 + [_I32, _I32, _P, _I64, _P]),
     "lora_linear_workspace_bytes": (_I64, [_LP, _I32]),
     "lora_linear": (_I32, [_LP, _P, _P, _P, _P, _P, _P, _P, _P, _I32, _P, _I64, _P]),
     "lora_gated_ffn_workspace_bytes": (_I64, [_GP, _I32]),
@@ -547,6 +558,15 @@ def make_norm_desc(dtype: str, hidden: int, eps: float) -> lora_norm_desc:
     return lora_norm_desc(_dtype(dtype), _features(hidden, "hidden"), float(eps), 0)
 
 
+def make_block_norm_desc(dtype: str, hidden: int, eps: float, gate: str = "none",
+                         residual_scale: float = 1.0,
+                         block_scale: float = 1.0) -> lora_block_norm_desc:
+    """Descriptor of lora_block_norm and its gradients; gate: "none", "channel" or "element"."""
+    return lora_block_norm_desc(_dtype(dtype), _features(hidden, "hidden"), float(eps),
+                                _choice(GATES, gate, "gate", LORA_E_ARG), float(residual_scale),
+                                float(block_scale))
+
+
 def make_linear_desc(dtype: str, out_dtype: str, in_features: int, out_features: int,
                      act: str = "none") -> lora_linear_desc:
     return lora_linear_desc(_dtype(dtype), _dtype(out_dtype),
@@ -566,6 +586,30 @@ def lora_add_rms_norm(desc, x, residual, weight, sum, out, out8, scale, T, strea
     _check(pycall().add_rms_norm(entry_address("lora_add_rms_norm"), ctypes.addressof(desc),
                                  x, residual, weight, sum, out,
                                  out8, scale, T, _stream(stream)))
+
+
+def lora_block_norm(desc, y, residual, gate, post_weight, pre_weight, sum, out, out8, scale, T,
+                    stream=None) -> None:
+    """sum = residual_scale residual + block_scale gate rms_norm(y); out = rms_norm(sum);
+    out8 / scale the same in e4m3."""
+    _check(pycall().block_norm(entry_address("lora_block_norm"), ctypes.addressof(desc), y,
+                               residual, gate, post_weight, pre_weight, sum, out, out8, scale, T,
+                               _stream(stream)))
+
+
+def lora_block_norm_backward_workspace_bytes(desc, T: int) -> int:
+    return _check(lib().lora_block_norm_backward_workspace_bytes(ctypes.byref(desc), int(T)))
+
+
+def lora_block_norm_backward(desc, dout, dsum, y, sum, gate, post_weight, pre_weight, dy,
+                             dresidual, dgate, dpost_weight, dpre_weight, accumulate, T, ws,
+                             ws_bytes, stream=None) -> None:
+    """Gradients of lora_block_norm; the fp32 sums over the rows (a channel gate's,
+    the weights') are added to what is there where accumulate is true."""
+    _check(pycall().block_norm_backward(
+        entry_address("lora_block_norm_backward"), ctypes.addressof(desc), dout, dsum, y, sum,
+        gate, post_weight, pre_weight, dy, dresidual, dgate, dpost_weight, dpre_weight,
+        int(accumulate), T, ws, ws_bytes, _stream(stream)))
 
 
 def lora_linear_workspace_bytes(desc, T: int) -> int:

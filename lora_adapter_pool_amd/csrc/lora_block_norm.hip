@@ -1,0 +1,549 @@
+// What joins a block's output to the residual stream and opens the next block,
+// and its gradients.
+//
+//   p = y (mean(y^2) + eps)^(-1/2) post_weight          (p = y without one)
+//   t = round(alpha residual + beta gate p)             (the stream)
+//   n = t (mean(t^2) + eps)^(-1/2) pre_weight, out = round(n), out8 and scale
+//       as lora_add_rms_norm's
+//
+// One pass over memory: a row stays in registers between the two statistics.
+// The row's second statistic depends on its first, so a row waits for two
+// reductions over the workgroup; with several rows a compute unit in flight the
+// loads of the others fill that time.
+//
+// Backwards, with a hat for the normalised rows (t_hat = t r_t, r_t the root's
+// reciprocal) and < > for a row's mean:
+//   dt = dsum + r_t (dout w_pre - t_hat <dout w_pre t_hat>)
+//   dresidual = alpha dt,  dgate = beta dt p,  dp = beta gate dt
+//   dy = r_y (dp w_post - y_hat <dp w_post y_hat>)
+//   dw_pre = sum_rows dout t_hat,  dw_post = sum_rows dp y_hat, and dgate's sum
+//   over the rows where the gate is one a channel
+// The statistics are made again from y and the stream, which have to be read
+// anyhow, so that the forward pass keeps nothing else.  A workgroup takes every
+// n-th row and keeps the columns' sums in registers; their partials are added in
+// a second launch, in an order that depends on the sizes alone.
+#include <hip/hip_runtime.h>
+
+#include "lora_norm.h"
+
+namespace lora {
+
+namespace {
+
+constexpr int kMaxHidden = 16384;
+constexpr int kForwardThreads = 1024, kBackwardThreads = 512;
+// workgroups that keep sums over rows, two a compute unit
+constexpr int kSumGroups = 512;
+
+struct JoinArgs {
+  const void* y;
+  const void* residual;
+  const void* gate;
+  const void* post;
+  const void* pre;
+  void* sum;
+  void* out;
+  uint8_t* out8;
+  float* scale;
+  int64_t gate_row;  // elements from a row's gate to the next: H, or 0
+  int32_t H;
+  float alpha, beta;
+  double over_h, eps;
+};
+
+// A statistic's factor, in two parts: fp32 does not hold the factor of a row of
+// numbers below 2^-128, or near the largest, or not with all its bits.
+struct Factor {
+  float part, rest;
+  __device__ __forceinline__ float of(float x) const { return x * part * rest; }
+};
+__device__ __forceinline__ Factor factor_of(double root) {
+  if (root > 0x1p120) return {0x1p64f, (float)(root * 0x1p-64)};
+  if (root < 0x1p-120) return {0x1p-64f, (float)(root * 0x1p64)};
+  return {1.f, (float)root};
+}
+
+// Sums over the workgroup, the same in every thread.  `room` is not read again
+// before another barrier has passed.
+template <int N>
+__device__ __forceinline__ void sum_over(double (&v)[N], double (*room)[N]) {
+  const int tid = threadIdx.x, waves = blockDim.x >> 6;
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+#pragma unroll
+    for (int d = 32; d; d >>= 1) v[k] += __shfl_xor(v[k], d);
+  if (waves == 1) return;
+  if ((tid & 63) == 0)
+#pragma unroll
+    for (int k = 0; k < N; ++k) room[tid >> 6][k] = v[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = 0.0;
+  for (int i = 0; i < waves; ++i)
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] += room[i][k];
+}
+
+__device__ __forceinline__ double square_plus(float x, double s) {
+  return __builtin_fma((double)x, (double)x, s);
+}
+
+template <int DT, int NP>
+__global__ __launch_bounds__(kForwardThreads) void join_kernel(JoinArgs a) {
+  __shared__ double first[kForwardThreads / 64][1], second[kForwardThreads / 64][1];
+  __shared__ uint32_t tops[kForwardThreads / 64];
+  const int tid = threadIdx.x, nt = blockDim.x, waves = nt >> 6;
+  const int64_t base = (int64_t)blockIdx.x * a.H, gate = blockIdx.x * a.gate_row;
+  float t[NP][8];
+  Raw<DT> residual[NP], post[NP], pre[NP], g[NP];
+  double ss[1] = {0.0};
+#pragma unroll
+  for (int j = 0; j < NP; ++j) {
+    const int c = (tid + j * nt) * 8;
+    if (c < a.H) {
+      load8(a.y, base + c, 8, DT, t[j]);
+      residual[j].load(a.residual, base + c);
+      if (a.post) post[j].load(a.post, c);
+      if (a.gate) g[j].load(a.gate, gate + c);
+      if (a.pre) pre[j].load(a.pre, c);
+      if (a.post)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss[0] = square_plus(t[j][i], ss[0]);
+    }
+  }
+  if (a.post) {
+    sum_over(ss, first);
+    const Factor f = factor_of(reciprocal_root(__builtin_fma(ss[0], a.over_h, a.eps)));
+#pragma unroll
+    for (int j = 0; j < NP; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[j][i] = f.of(t[j][i]) * post[j].at(i);
+  }
+  ss[0] = 0.0;
+#pragma unroll
+  for (int j = 0; j < NP; ++j) {
+    const int c = (tid + j * nt) * 8;
+    if (c < a.H) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (a.gate) t[j][i] *= g[j].at(i);
+        t[j][i] = residual[j].at(i) * a.alpha + t[j][i] * a.beta;
+      }
+      if constexpr (DT == LORA_BF16) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          const uint32_t w = bk_pack(t[j][i], t[j][i + 1]);
+          t[j][i] = bk_lo(w);
+          t[j][i + 1] = bk_hi(w);
+        }
+      }
+      store8(a.sum, base + c, 8, DT, t[j]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss[0] = square_plus(t[j][i], ss[0]);
+    }
+  }
+  if (!a.pre) return;
+  sum_over(ss, second);
+  const Factor f = factor_of(reciprocal_root(__builtin_fma(ss[0], a.over_h, a.eps)));
+  uint32_t top = 0;  // largest |n| by its bits, which also keeps a NaN
+#pragma unroll
+  for (int j = 0; j < NP; ++j) {
+    const int c = (tid + j * nt) * 8;
+    if (c < a.H) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        t[j][i] = f.of(t[j][i]) * pre[j].at(i);
+        const uint32_t b = __float_as_uint(t[j][i]) & 0x7fffffffu;
+        top = b > top ? b : top;
+      }
+      if (a.out) store8(a.out, base + c, 8, DT, t[j]);
+    }
+  }
+  if (!a.out8) return;
+#pragma unroll
+  for (int d = 32; d; d >>= 1) {
+    const uint32_t o = __shfl_xor(top, d);
+    top = o > top ? o : top;
+  }
+  if (waves > 1) {
+    if ((tid & 63) == 0) tops[tid >> 6] = top;
+    __syncthreads();
+    for (int i = 0; i < waves; ++i) top = tops[i] > top ? tops[i] : top;
+  }
+  float scale = (float)((double)__uint_as_float(top) * (1.0 / 448.0));
+  scale = scale < 0x1p-126f ? 0x1p-126f : scale;  // keeps NaN
+  const float inv = (float)reciprocal(scale);
+  if (tid == 0) a.scale[blockIdx.x] = scale;
+#pragma unroll
+  for (int j = 0; j < NP; ++j) {
+    const int c = (tid + j * nt) * 8;
+    if (c < a.H) {
+      int lo = 0, hi = 0;
+      lo = __builtin_amdgcn_cvt_pk_fp8_f32(t[j][0] * inv, t[j][1] * inv, lo, false);
+      lo = __builtin_amdgcn_cvt_pk_fp8_f32(t[j][2] * inv, t[j][3] * inv, lo, true);
+      hi = __builtin_amdgcn_cvt_pk_fp8_f32(t[j][4] * inv, t[j][5] * inv, hi, false);
+      hi = __builtin_amdgcn_cvt_pk_fp8_f32(t[j][6] * inv, t[j][7] * inv, hi, true);
+      *reinterpret_cast<uint64_t*>(a.out8 + base + c) =
+          (uint32_t)lo | (uint64_t)(uint32_t)hi << 32;
+    }
+  }
+}
+
+// The row's threads: one piece of eight elements a thread up to `most`.
+inline int threads_of(int H, int most) {
+  int nt = 64;
+  while (nt < most && nt < H / 8) nt *= 2;
+  return nt;
+}
+
+template <int DT>
+void launch_join(const JoinArgs& a, int T, hipStream_t st) {
+  const int nt = threads_of(a.H, 512) * (a.H > 8192 ? 2 : 1);
+  if (a.H / 8 <= nt)
+    hipLaunchKernelGGL((join_kernel<DT, 1>), dim3(T), dim3(nt), 0, st, a);
+  else
+    hipLaunchKernelGGL((join_kernel<DT, 2>), dim3(T), dim3(nt), 0, st, a);
+}
+
+struct BackArgs {
+  const void* dout;
+  const void* dsum;
+  const void* y;
+  const void* sum;
+  const void* gate;
+  const void* post;
+  const void* pre;
+  void* dy;
+  void* dresidual;
+  void* dgate;   // [T][H], or nullptr
+  float* part;   // [kinds][workgroups][H]: sums over a workgroup's rows
+  int32_t k_pre, k_post, k_gate;  // which kind each sum is, or -1
+  int64_t gate_row;
+  int32_t H, T;
+  float alpha, beta;
+  double over_h, eps;
+};
+
+template <int DT, int NP>
+__global__ __launch_bounds__(kBackwardThreads) void join_backward_kernel(BackArgs a) {
+  // by the row's parity: a row's reductions may meet the next row's writes
+  __shared__ double first[2][kBackwardThreads / 64][3], second[2][kBackwardThreads / 64][1];
+  // Four pieces a thread leave no registers to hold a row over the reductions: it
+  // is read again, from the caches.
+  constexpr int kHeld = NP < 4 ? NP : 1;
+  const int tid = threadIdx.x, nt = blockDim.x;
+  float w_pre[NP][8] = {}, w_post[NP][8] = {}, w_gate[NP][8] = {};  // sums over the rows
+  int parity = 0;
+  for (int row = blockIdx.x; row < a.T; row += gridDim.x, parity ^= 1) {
+    const int64_t base = (int64_t)row * a.H, gate = row * a.gate_row;
+    Raw<DT> y[kHeld], t[kHeld], dout[kHeld], pre[kHeld];
+    auto load_y = [&](int j, int c) {
+      if (a.post || a.gate) y[j % kHeld].load(a.y, base + c);
+    };
+    auto load = [&](int j, int c) {
+      if (!a.pre) return;
+      t[j % kHeld].load(a.sum, base + c);
+      dout[j % kHeld].load(a.dout, base + c);
+      pre[j % kHeld].load(a.pre, c);
+    };
+    auto stat = [&](int j, double (&s)[3]) {
+      if (a.pre)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float x = t[j % kHeld].at(i);
+          s[0] = square_plus(x, s[0]);
+          s[1] = __builtin_fma((double)(dout[j % kHeld].at(i) * pre[j % kHeld].at(i)), (double)x,
+                               s[1]);
+        }
+      if (a.post)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[2] = square_plus(y[j % kHeld].at(i), s[2]);
+    };
+    double s[3] = {0.0, 0.0, 0.0};  // of t^2, dout w_pre t and y^2
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const int c = (tid + j * nt) * 8;
+      if (c < a.H) {
+        load_y(j, c);
+        load(j, c);
+        if constexpr (kHeld < NP) stat(j, s);
+      }
+    }
+    if constexpr (kHeld == NP)
+#pragma unroll
+      for (int j = 0; j < NP; ++j)
+        if ((tid + j * nt) * 8 < a.H) stat(j, s);
+    if (a.pre || a.post) sum_over(s, first[parity]);
+    const double rt = reciprocal_root(__builtin_fma(s[0], a.over_h, a.eps));
+    const double ry = reciprocal_root(__builtin_fma(s[2], a.over_h, a.eps));
+    const Factor ft = factor_of(rt), fy = factor_of(ry);
+    const float ct = (float)(s[1] * rt * a.over_h);
+    float dp[NP][8];
+    double s2[1] = {0.0};
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const int c = (tid + j * nt) * 8;
+      if (c < a.H) {
+        Raw<DT> dsum, g, post;
+        if (a.dsum) dsum.load(a.dsum, base + c);
+        if (a.gate) g.load(a.gate, gate + c);
+        if (a.post) post.load(a.post, c);
+        if constexpr (kHeld < NP) {
+          __builtin_amdgcn_sched_barrier(0);  // (a piece's loads and no more at a time)
+          load_y(j, c);
+          load(j, c);
+        }
+        float dres[8], dg[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float d = 0.f;
+          if (a.pre) {
+            const float hat = ft.of(t[j % kHeld].at(i)), o = dout[j % kHeld].at(i);
+            w_pre[j][i] += o * hat;
+            d = ft.of(o * pre[j % kHeld].at(i) - hat * ct);
+          }
+          if (a.dsum) d += dsum.at(i);
+          dres[i] = a.alpha * d;
+          d *= a.beta;
+          const float hat = a.post ? fy.of(y[j % kHeld].at(i)) : a.gate ? y[j % kHeld].at(i) : 0.f;
+          if (a.gate) {
+            dg[i] = d * (a.post ? hat * post.at(i) : hat);
+            w_gate[j][i] += dg[i];
+            d *= g.at(i);
+          }
+          if (a.post) {
+            w_post[j][i] += d * hat;
+            d *= post.at(i);
+            s2[0] = __builtin_fma((double)d, (double)y[j % kHeld].at(i), s2[0]);
+          }
+          dp[j][i] = d;
+        }
+        store8(a.dresidual, base + c, 8, DT, dres);
+        if (a.dgate) store8(a.dgate, base + c, 8, DT, dg);
+        if (!a.post) store8(a.dy, base + c, 8, DT, dp[j]);
+      }
+    }
+    if (a.post) {
+      sum_over(s2, second[parity]);
+      const float cy = (float)(s2[0] * ry * a.over_h);
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const int c = (tid + j * nt) * 8;
+        if (c < a.H) {
+          float d[8];
+          if constexpr (kHeld < NP) load_y(j, c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) d[i] = fy.of(dp[j][i] - fy.of(y[j % kHeld].at(i)) * cy);
+          store8(a.dy, base + c, 8, DT, d);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NP; ++j) {
+    const int c = (tid + j * nt) * 8;
+    if (c < a.H) {
+      const int64_t n = gridDim.x, at = (int64_t)blockIdx.x * a.H + c;
+      if (a.k_pre >= 0) store8(a.part, a.k_pre * n * a.H + at, 8, LORA_F32, w_pre[j]);
+      if (a.k_post >= 0) store8(a.part, a.k_post * n * a.H + at, 8, LORA_F32, w_post[j]);
+      if (a.k_gate >= 0) store8(a.part, a.k_gate * n * a.H + at, 8, LORA_F32, w_gate[j]);
+    }
+  }
+}
+
+// The partials' sums.  A workgroup takes 64 columns of one kind; its 16 waves
+// take every 16th partial.
+struct SumArgs {
+  const float* part;
+  float* to[3];
+  int32_t groups, H, accumulate;
+};
+__global__ __launch_bounds__(1024) void column_sums(SumArgs a) {
+  __shared__ float room[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane;
+  const float* from = a.part + (int64_t)blockIdx.y * a.groups * a.H + c;
+  float s = 0.f;
+  if (c < a.H)
+    for (int r = wave; r < a.groups; r += 16) s += from[(int64_t)r * a.H];
+  room[wave][lane] = s;
+  __syncthreads();
+  if (wave || c >= a.H) return;
+  s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s += room[i][lane];
+  float* to = blockIdx.y == 0 ? a.to[0] : blockIdx.y == 1 ? a.to[1] : a.to[2];
+  to[c] = a.accumulate ? to[c] + s : s;
+}
+
+template <int DT>
+void launch_backward(const BackArgs& a, int groups, hipStream_t st) {
+  const int nt = threads_of(a.H, kBackwardThreads), np = (a.H / 8 + nt - 1) / nt;
+  if (np == 1)
+    hipLaunchKernelGGL((join_backward_kernel<DT, 1>), dim3(groups), dim3(nt), 0, st, a);
+  else if (np == 2)
+    hipLaunchKernelGGL((join_backward_kernel<DT, 2>), dim3(groups), dim3(nt), 0, st, a);
+  else
+    hipLaunchKernelGGL((join_backward_kernel<DT, 4>), dim3(groups), dim3(nt), 0, st, a);
+}
+
+int32_t check_join(const lora_block_norm_desc* d) {
+  if (!d) return fail(LORA_E_ARG, "descriptor is NULL");
+  if (d->dtype != LORA_F32 && d->dtype != LORA_BF16)
+    return fail(LORA_E_DTYPE, "block norm dtype must be fp32 or bf16, got %d", d->dtype);
+  if (d->hidden < 8 || d->hidden > kMaxHidden)
+    return fail(LORA_E_SHAPE, "hidden must be in [8, %d], got %d", kMaxHidden, d->hidden);
+  if (d->hidden % 8)
+    return fail(LORA_E_ALIGN, "hidden must be a multiple of 8, got %d", d->hidden);
+  if (!(d->eps >= 0.f && d->eps < __builtin_inff()))
+    return fail(LORA_E_ARG, "eps must be finite and >= 0, got %g", (double)d->eps);
+  if (d->gate < LORA_GATE_NONE || d->gate > LORA_GATE_ELEMENT)
+    return fail(LORA_E_ARG, "unknown gate %d", d->gate);
+  if (!(__builtin_fabsf(d->residual_scale) < __builtin_inff()) ||
+      !(__builtin_fabsf(d->block_scale) < __builtin_inff()))
+    return fail(LORA_E_ARG, "the scales of residual and block must be finite");
+  return LORA_OK;
+}
+
+int32_t check_aligned(const void* const* p, int n) {
+  for (int i = 0; i < n; ++i)
+    if (!aligned16(p[i]))
+      return fail(LORA_E_ALIGN, "every buffer of the block norm must be 16-byte aligned");
+  return LORA_OK;
+}
+
+}  // namespace
+
+}  // namespace lora
+
+using namespace lora;
+
+extern "C" int32_t lora_block_norm(const lora_block_norm_desc* desc, const void* y,
+                                   const void* residual, const void* gate,
+                                   const void* post_weight, const void* pre_weight, void* sum,
+                                   void* out, void* out8, float* scale, int32_t T,
+                                   void* stream) {
+  clear_error();
+  if (int32_t e = check_join(desc)) return e;
+  if (int32_t e = check_rows(T)) return e;
+  if (T == 0) return LORA_OK;
+  if (!y || !residual || !sum)
+    return fail(LORA_E_ARG, "y, residual and sum must not be NULL");
+  if ((gate != nullptr) != (desc->gate != LORA_GATE_NONE))
+    return fail(LORA_E_ARG, "the gate is NULL, or the descriptor has none");
+  if ((out8 != nullptr) != (scale != nullptr))
+    return fail(LORA_E_ARG, "out8 and scale go together: one of them is NULL");
+  if ((pre_weight != nullptr) != (out || out8))
+    return fail(LORA_E_ARG, "pre_weight and an output go together");
+  const void* ptrs[] = {y, residual, gate, post_weight, pre_weight, sum, out, out8, scale};
+  if (int32_t e = check_aligned(ptrs, 9)) return e;
+  const JoinArgs a{y,
+                   residual,
+                   gate,
+                   post_weight,
+                   pre_weight,
+                   sum,
+                   out,
+                   (uint8_t*)out8,
+                   scale,
+                   desc->gate == LORA_GATE_ELEMENT ? desc->hidden : 0,
+                   desc->hidden,
+                   desc->residual_scale,
+                   desc->block_scale,
+                   1.0 / desc->hidden,
+                   (double)desc->eps};
+  if (desc->dtype == LORA_BF16)
+    launch_join<LORA_BF16>(a, T, (hipStream_t)stream);
+  else
+    launch_join<LORA_F32>(a, T, (hipStream_t)stream);
+  return check_launch("block norm");
+}
+
+extern "C" int64_t lora_block_norm_backward_workspace_bytes(const lora_block_norm_desc* desc,
+                                                            int32_t T) {
+  clear_error();
+  if (int32_t e = check_join(desc)) return e;
+  if (int32_t e = check_rows(T)) return e;
+  return (int64_t)3 * (T < kSumGroups ? T : kSumGroups) * desc->hidden * 4;
+}
+
+extern "C" int32_t lora_block_norm_backward(
+    const lora_block_norm_desc* desc, const void* dout, const void* dsum, const void* y,
+    const void* sum, const void* gate, const void* post_weight, const void* pre_weight, void* dy,
+    void* dresidual, void* dgate, float* dpost_weight, float* dpre_weight, int32_t accumulate,
+    int32_t T, void* ws, int64_t ws_bytes, void* stream) {
+  clear_error();
+  if (int32_t e = check_join(desc)) return e;
+  if (int32_t e = check_rows(T)) return e;
+  if (accumulate != 0 && accumulate != 1)
+    return fail(LORA_E_ARG, "accumulate must be 0 or 1, got %d", accumulate);
+  if (dgate && desc->gate == LORA_GATE_NONE)
+    return fail(LORA_E_ARG, "dgate, and the descriptor has no gate");
+  const bool element = desc->gate == LORA_GATE_ELEMENT;
+  if (T) {
+    if (dpost_weight && !post_weight)
+      return fail(LORA_E_ARG, "dpost_weight without post_weight");
+    if (dpre_weight && !pre_weight) return fail(LORA_E_ARG, "dpre_weight without pre_weight");
+    if (!dy || !dresidual) return fail(LORA_E_ARG, "dy and dresidual must not be NULL");
+    if ((post_weight || desc->gate != LORA_GATE_NONE) && !y)
+      return fail(LORA_E_ARG, "y is NULL, and a norm or a gate takes it");
+    if ((gate != nullptr) != (desc->gate != LORA_GATE_NONE))
+      return fail(LORA_E_ARG, "the gate is NULL, or the descriptor has none");
+    if ((pre_weight != nullptr) != (dout != nullptr))
+      return fail(LORA_E_ARG, "pre_weight and dout go together: one of them is NULL");
+    if (pre_weight && !sum) return fail(LORA_E_ARG, "pre_weight without the kept sum");
+    if (!dout && !dsum) return fail(LORA_E_ARG, "dout and dsum are both NULL");
+  }
+  const void* ptrs[] = {dout, dsum,      y,     sum,          gate,        post_weight, pre_weight,
+                        dy,   dresidual, dgate, dpost_weight, dpre_weight, ws};
+  if (int32_t e = check_aligned(ptrs, 13)) return e;
+  SumArgs s{};
+  BackArgs a{};
+  int kinds = 0;
+  a.k_pre = a.k_post = a.k_gate = -1;
+  if (dpre_weight) s.to[kinds] = dpre_weight, a.k_pre = kinds++;
+  if (dpost_weight) s.to[kinds] = dpost_weight, a.k_post = kinds++;
+  if (dgate && !element) s.to[kinds] = (float*)dgate, a.k_gate = kinds++;
+  // without sums over the rows nothing is kept from row to row
+  const int groups = kinds ? (T < kSumGroups ? T : kSumGroups) : T;
+  if (kinds && T) {
+    const int64_t need = lora_block_norm_backward_workspace_bytes(desc, T);
+    if (!ws) return fail(LORA_E_ARG, "workspace is NULL");
+    if (ws_bytes < need)
+      return fail(LORA_E_WORKSPACE, "workspace holds %lld bytes, the call needs %lld",
+                  (long long)ws_bytes, (long long)need);
+  }
+  const hipStream_t st = (hipStream_t)stream;
+  if (T) {
+    a.dout = dout;
+    a.dsum = dsum;
+    a.y = y;
+    a.sum = sum;
+    a.gate = gate;
+    a.post = post_weight;
+    a.pre = pre_weight;
+    a.dy = dy;
+    a.dresidual = dresidual;
+    a.dgate = element ? dgate : nullptr;
+    a.part = (float*)ws;
+    a.gate_row = element ? desc->hidden : 0;
+    a.H = desc->hidden;
+    a.T = T;
+    a.alpha = desc->residual_scale;
+    a.beta = desc->block_scale;
+    a.over_h = 1.0 / desc->hidden;
+    a.eps = (double)desc->eps;
+    if (desc->dtype == LORA_BF16)
+      launch_backward<LORA_BF16>(a, groups, st);
+    else
+      launch_backward<LORA_F32>(a, groups, st);
+    if (int32_t e = check_launch("block norm backward")) return e;
+  }
+  if (!kinds || (!T && accumulate)) return LORA_OK;
+  s.part = (const float*)ws;
+  s.groups = T ? groups : 0;
+  s.H = desc->hidden;
+  s.accumulate = accumulate;
+  hipLaunchKernelGGL(column_sums, dim3((desc->hidden + 63) / 64, kinds), dim3(1024), 0, st, s);
+  return check_launch("sums over the rows");
+}

@@ -17,7 +17,7 @@
 // 330 MB in 61 us, 5.4 TB/s).
 #include <hip/hip_runtime.h>
 
-#include "lora_block.h"
+#include "lora_norm.h"
 
 namespace lora {
 
@@ -37,38 +37,6 @@ struct NormArgs {
   float* scale;
   int32_t H;
   double over_h, eps;
-};
-
-// 1 / x and 1 / sqrt(x) to within a few steps of 64 bits: the hardware's
-// estimates (some 2^-26) and one step of third order.  Zero and infinity keep
-// the estimate's infinity and zero.
-__device__ __forceinline__ double reciprocal(double x) {
-  const double y = __builtin_amdgcn_rcp(x), e = __builtin_fma(-x, y, 1.0);
-  const double z = __builtin_fma(y, __builtin_fma(e, e, e), y);
-  return e == e ? z : y;
-}
-__device__ __forceinline__ double reciprocal_root(double x) {
-  const double y = __builtin_amdgcn_rsq(x), e = __builtin_fma(-x * y, y, 1.0);
-  const double z = __builtin_fma(y, e * __builtin_fma(0.375, e, 0.5), y);
-  return e == e ? z : y;
-}
-
-// A piece of eight elements as it is stored (the weights are fetched with the
-// row, and take their room before its statistic is known).
-template <int DT>
-struct Raw {
-  bk_u32x4 v[DT == LORA_F32 ? 2 : 1];
-  __device__ __forceinline__ void load(const void* base, int64_t i) {
-    const bk_u32x4* p = reinterpret_cast<const bk_u32x4*>(
-        (const char*)base + i * (DT == LORA_F32 ? 4 : 2));
-    v[0] = p[0];
-    if constexpr (DT == LORA_F32) v[1] = p[1];
-  }
-  __device__ __forceinline__ float at(int i) const {
-    if constexpr (DT == LORA_F32) return __uint_as_float(v[i >> 2][i & 3]);
-    const uint32_t w = v[0][i >> 1];
-    return i & 1 ? bk_hi(w) : bk_lo(w);
-  }
 };
 
 // NP pieces of eight elements a thread, one row a workgroup.

@@ -45,9 +45,22 @@ typedef int32_t (*gated_backward_fn)(const lora_gated_desc*, const void*, const 
                                      const void*, void*, void*, void*, int32_t, void*, int64_t,
                                      void*);
 
+typedef int32_t (*block_norm_fn)(const lora_block_norm_desc*, const void*, const void*,
+                                 const void*, const void*, const void*, void*, void*, void*,
+                                 float*, int32_t, void*);
+typedef int32_t (*block_norm_backward_fn)(const lora_block_norm_desc*, const void*, const void*,
+                                          const void*, const void*, const void*, const void*,
+                                          const void*, void*, void*, void*, float*, float*,
+                                          int32_t, int32_t, void*, int64_t, void*);
+
 /* the typedefs match the header's declarations */
 _Static_assert(__builtin_types_compatible_p(__typeof__(&lora_add_rms_norm), norm_fn),
                "lora_add_rms_norm");
+_Static_assert(__builtin_types_compatible_p(__typeof__(&lora_block_norm), block_norm_fn),
+               "lora_block_norm");
+_Static_assert(__builtin_types_compatible_p(__typeof__(&lora_block_norm_backward),
+                                            block_norm_backward_fn),
+               "lora_block_norm_backward");
 _Static_assert(__builtin_types_compatible_p(__typeof__(&lora_linear), linear_fn), "lora_linear");
 _Static_assert(__builtin_types_compatible_p(__typeof__(&lora_gated_ffn), gated_fn),
                "lora_gated_ffn");
@@ -280,6 +293,68 @@ static PyObject* py_norm(PyObject* self, PyObject* const* args, Py_ssize_t nargs
   return PyLong_FromLong(st);
 }
 
+/* block_norm(fn, desc, y, residual, gate, post_weight, pre_weight, sum, out, out8,
+ *            scale, T, stream) */
+static PyObject* py_block_norm(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+  (void)self;
+  static const int kinds[13] = {P, P, D, D, D, D, D, D, D, D, D, I32, P};
+  static const char* const names[13] = {"fn",          "desc",       "y",   "residual", "gate",
+                                        "post_weight", "pre_weight", "sum", "out",      "out8",
+                                        "scale",       "T",          "stream"};
+  uint64_t a[13];
+  int64_t bytes[13];
+  if (convert_args(args, nargs, "block_norm", kinds, names, 13, a, bytes)) return NULL;
+  const lora_block_norm_desc* d = (const lora_block_norm_desc*)PTR(1);
+  const int32_t T = I32V(11);
+  if (d && T > 0) {
+    const wide H = d->hidden, all = H * T, e = size_of(d->dtype);
+    const wide gate = d->gate == LORA_GATE_ELEMENT ? all * e : H * e;
+    const wide need[13] = {0,     0,       all * e, all * e, gate,
+                           H * e, H * e,   all * e, all * e, all,
+                           (wide)T * 4, 0, 0};
+    if (large_enough("block_norm", names, 13, bytes, need, -1)) return NULL;
+  }
+  const block_norm_fn f = (block_norm_fn)(uintptr_t)a[0];
+  int32_t st;
+  Py_BEGIN_ALLOW_THREADS
+  st = f(d, PTR(2), PTR(3), PTR(4), PTR(5), PTR(6), PTR(7), PTR(8), PTR(9), (float*)PTR(10), T,
+         PTR(12));
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(st);
+}
+
+/* block_norm_backward(fn, desc, dout, dsum, y, sum, gate, post_weight, pre_weight,
+ *                     dy, dresidual, dgate, dpost_weight, dpre_weight, accumulate,
+ *                     T, ws, ws_bytes, stream) */
+static PyObject* py_block_norm_backward(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+  (void)self;
+  static const int kinds[19] = {P, P, D, D, D, D, D, D, D, D, D, D, D, D, I32, I32, D, I64, P};
+  static const char* const names[19] = {
+      "fn",          "desc",       "dout", "dsum",      "y",     "sum",          "gate",
+      "post_weight", "pre_weight", "dy",   "dresidual", "dgate", "dpost_weight", "dpre_weight",
+      "accumulate",  "T",          "ws",   "ws_bytes",  "stream"};
+  uint64_t a[19];
+  int64_t bytes[19];
+  if (convert_args(args, nargs, "block_norm_backward", kinds, names, 19, a, bytes)) return NULL;
+  const lora_block_norm_desc* d = (const lora_block_norm_desc*)PTR(1);
+  const int32_t T = I32V(15);
+  if (d && T >= 0) {
+    const wide H = d->hidden, e = size_of(d->dtype), all = H * T * e;
+    const int element = d->gate == LORA_GATE_ELEMENT;
+    const wide w = T ? H * e : 0;
+    const wide need[19] = {0,   0, all, all, all, all, element ? all : w, w, w, all,
+                           all, element ? all : H * 4, H * 4, H * 4, 0, 0, T ? I64V(17) : 0, 0, 0};
+    if (large_enough("block_norm_backward", names, 19, bytes, need, 16)) return NULL;
+  }
+  const block_norm_backward_fn f = (block_norm_backward_fn)(uintptr_t)a[0];
+  int32_t st;
+  Py_BEGIN_ALLOW_THREADS
+  st = f(d, PTR(2), PTR(3), PTR(4), PTR(5), PTR(6), PTR(7), PTR(8), PTR(9), PTR(10), PTR(11),
+         (float*)PTR(12), (float*)PTR(13), I32V(14), T, PTR(16), I64V(17), PTR(18));
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(st);
+}
+
 /* linear(fn, desc, x, w, x_scale, w_scale, bias, delta, residual, out, T, ws,
  *        ws_bytes, stream) */
 static PyObject* py_linear(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
@@ -378,6 +453,13 @@ static PyMethodDef methods[] = {
     {"add_rms_norm", (PyCFunction)(void (*)(void))py_norm, METH_FASTCALL,
      "add_rms_norm(fn, desc, x, residual, weight, sum, out, out8, scale, T, stream) -> status of "
      "lora_add_rms_norm"},
+    {"block_norm", (PyCFunction)(void (*)(void))py_block_norm, METH_FASTCALL,
+     "block_norm(fn, desc, y, residual, gate, post_weight, pre_weight, sum, out, out8, scale, T, "
+     "stream) -> status of lora_block_norm"},
+    {"block_norm_backward", (PyCFunction)(void (*)(void))py_block_norm_backward, METH_FASTCALL,
+     "block_norm_backward(fn, desc, dout, dsum, y, sum, gate, post_weight, pre_weight, dy, "
+     "dresidual, dgate, dpost_weight, dpre_weight, accumulate, T, ws, ws_bytes, stream) -> status "
+     "of lora_block_norm_backward"},
     {"linear", (PyCFunction)(void (*)(void))py_linear, METH_FASTCALL,
      "linear(fn, desc, x, w, x_scale, w_scale, bias, delta, residual, out, T, ws, ws_bytes, "
      "stream) -> status of lora_linear"},
