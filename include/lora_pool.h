@@ -672,6 +672,46 @@ int32_t lora_block_norm_backward(const lora_block_norm_desc* desc, const void* d
                                  float* dpost_weight, float* dpre_weight, int32_t accumulate,
                                  int32_t T, void* ws, int64_t ws_bytes, void* stream);
 
+/* Gradient norms over many tensors, and clipping: one norm over all of them, or
+ * one for each group (an adapter slot's gradients, say):
+ *   norms[g] = sqrt(sum of x^2 over the tensors of group g)
+ *   out = round(x min(1, max_norm / norms[g]))       for every tensor of group g
+ * Squares are summed in 64 bits, the factor is rounded to fp32.  A group whose
+ * norm is infinite or NaN in fp32 is not clipped (out = x).  max_norm >= 0;
+ * infinity gives the norms alone (and copies where out is another array).
+ *
+ * lora_grad_list_build (host only) cuts the tensors into chunks, once for a list
+ * of tensors that many calls take; the caller copies the image, lora_grad_list_bytes
+ * bytes, to the GPU (16-byte aligned) and keeps the tensors.  Tensors are contiguous
+ * device memory of any size, aligned to their elements; out NULL is in place.
+ * Errors: LORA_E_ARG where two of the list's arrays overlap (out == grad apart),
+ * LORA_E_ID for a group outside [0, groups), LORA_E_DTYPE, LORA_E_SHAPE,
+ * LORA_E_ALIGN, LORA_E_WORKSPACE. */
+typedef struct {
+  void* grad;
+  void* out;      /* NULL: in place */
+  int64_t count;  /* elements */
+  int32_t dtype;  /* LORA_F32 or LORA_BF16, of grad and out */
+  int32_t group;
+} lora_grad;
+
+typedef struct {
+  int32_t chunks;
+  int32_t groups;
+  int32_t most_chunks;  /* of one group */
+  int32_t empty;        /* groups without an element: their norm is 0 */
+  int32_t separate;     /* 1: some tensor has an out of its own */
+  int32_t reserved;     /* 0 */
+  int64_t bytes;        /* of the image */
+} lora_grad_list;
+
+int64_t lora_grad_list_bytes(const lora_grad* grads, int32_t n, int32_t groups);
+int32_t lora_grad_list_build(const lora_grad* grads, int32_t n, int32_t groups, void* image,
+                             int64_t image_bytes, lora_grad_list* list);
+int64_t lora_clip_grads_workspace_bytes(const lora_grad_list* list);
+int32_t lora_clip_grads(const lora_grad_list* list, const void* image, float max_norm,
+                        float* norms, void* ws, int64_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -76,6 +76,18 @@ class lora_gated_desc(ctypes.Structure):
                 ("act", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class lora_grad_list(ctypes.Structure):
+    _fields_ = [("chunks", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("most_chunks", ctypes.c_int32), ("empty", ctypes.c_int32),
+                ("separate", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("bytes", ctypes.c_int64)]
+
+
+# lora_grad, as an array of them
+GRAD_DTYPE = np.dtype([("grad", "<u8"), ("out", "<u8"), ("count", "<i8"), ("dtype", "<i4"),
+                       ("group", "<i4")])
+
+
 class lora_meta(ctypes.Structure):
     _fields_ = [("num_sgmv_rows", ctypes.c_int32), ("num_segs", ctypes.c_int32),
                 ("num_bgmv_rows", ctypes.c_int32), ("reserved", ctypes.c_int32),
@@ -112,6 +124,7 @@ _I64 = ctypes.c_int64
 _DP = ctypes.POINTER(lora_pool_desc)
 _NP = ctypes.POINTER(lora_norm_desc)
 _BP = ctypes.POINTER(lora_block_norm_desc)
+_CP = ctypes.POINTER(lora_grad_list)
 _LP = ctypes.POINTER(lora_linear_desc)
 _GP = ctypes.POINTER(lora_gated_desc)
 
@@ -154,6 +167,10 @@ _SIGNATURES = {
     "lora_block_norm": (_I32, [_BP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I32, _P]),
     "lora_block_norm_backward_workspace_bytes": (_I64, [_BP, _I32]),
     "lora_block_norm_backward": (_I32, [_BP] + [_P] * 12 + [_I32, _I32, _P, _I64, _P]),
+    "lora_grad_list_bytes": (_I64, [_P, _I32, _I32]),
+    "lora_grad_list_build": (_I32, [_P, _I32, _I32, _P, _I64, _CP]),
+    "lora_clip_grads_workspace_bytes": (_I64, [_CP]),
+    "lora_clip_grads": (_I32, [_CP, _P, ctypes.c_float, _P, _P, _I64, _P]),
     "lora_linear_workspace_bytes": (_I64, [_LP, _I32]),
     "lora_linear": (_I32, [_LP, _P, _P, _P, _P, _P, _P, _P, _P, _I32, _P, _I64, _P]),
     "lora_gated_ffn_workspace_bytes": (_I64, [_GP, _I32]),
@@ -649,3 +666,66 @@ def lora_gated_ffn_backward(desc, dout, pre, x, w, dpre, dx, dw, T, ws, ws_bytes
                                        ctypes.addressof(desc), dout, pre, x,
                                        w, dpre, dx, dw, int(T), ws,
                                        int(ws_bytes), _stream(stream)))
+
+
+# ------------------------------------------------------------ gradient norms
+
+def lora_grad_list_build(grads: np.ndarray, groups: int):
+    """(list, image) from an array of GRAD_DTYPE; the image (bytes) goes to the GPU."""
+    grads = np.ascontiguousarray(grads, dtype=GRAD_DTYPE)
+    n = int(grads.shape[0])
+    at = grads.ctypes.data if n else None
+    need = _check(lib().lora_grad_list_bytes(at, n, int(groups)))
+    image = np.zeros(need, np.uint8)
+    out = lora_grad_list()
+    _check(lib().lora_grad_list_build(at, n, int(groups), image.ctypes.data, need,
+                                      ctypes.byref(out)))
+    return out, image
+
+
+class GradList:
+    """The tensors of lora_clip_grads, cut into chunks once: contiguous fp32 or bf16
+    tensors of one GPU, the group of each (default: one group of all), and where the
+    clipped gradients go (outs, or an entry of it, None: in place).  It keeps the
+    tensors and the list's image on their GPU."""
+
+    def __init__(self, tensors, groups=None, outs=None, num_groups: Optional[int] = None):
+        import torch
+
+        tensors = list(tensors)
+        groups = [0] * len(tensors) if groups is None else [int(g) for g in groups]
+        outs = [None] * len(tensors) if outs is None else list(outs)
+        if len(groups) != len(tensors) or len(outs) != len(tensors):
+            raise LoraError(LORA_E_SHAPE, "groups and outs must have an entry for each tensor")
+        if not tensors:
+            raise LoraError(LORA_E_ARG, "the list of tensors is empty")
+        codes = {torch.float32: LORA_F32, torch.bfloat16: LORA_BF16}
+        grads = np.zeros(len(tensors), GRAD_DTYPE)
+        for i, (t, o) in enumerate(zip(tensors, outs)):
+            if t.dtype not in codes or (o is not None and o.dtype != t.dtype):
+                raise LoraError(LORA_E_DTYPE, f"tensor {i} must be fp32 or bf16, as its out")
+            for u in (t, o):
+                if u is not None and (not u.is_cuda or u.device != tensors[0].device):
+                    raise LoraError(LORA_E_ARG, f"tensor {i} is not on the first one's GPU")
+                if u is not None and not u.is_contiguous():
+                    raise LoraError(LORA_E_SHAPE, f"tensor {i} is not contiguous")
+            if o is not None and o.numel() != t.numel():
+                raise LoraError(LORA_E_SHAPE, f"tensor {i} and its out differ in size")
+            if not -1 << 31 <= groups[i] < 1 << 31:
+                raise LoraError(LORA_E_ID, f"tensor {i}: group {groups[i]}")
+            grads[i] = (t.data_ptr(), 0 if o is None else o.data_ptr(), t.numel(),
+                        codes[t.dtype], groups[i])
+        self.tensors, self.outs = tensors, outs
+        self.num_groups = max(groups) + 1 if num_groups is None else int(num_groups)
+        self.struct, image = lora_grad_list_build(grads, self.num_groups)
+        self.image = torch.from_numpy(image).to(tensors[0].device)
+
+
+def lora_clip_grads_workspace_bytes(grads) -> int:
+    return _check(lib().lora_clip_grads_workspace_bytes(ctypes.byref(grads.struct)))
+
+
+def lora_clip_grads(grads, max_norm: float, norms, ws, ws_bytes, stream=None) -> None:
+    """norms[g]: fp32 norm of group g's tensors; each tensor times min(1, max_norm / norm)."""
+    _check(pycall().clip_grads(entry_address("lora_clip_grads"), ctypes.addressof(grads.struct),
+                               grads.image, max_norm, norms, ws, ws_bytes, _stream(stream)))

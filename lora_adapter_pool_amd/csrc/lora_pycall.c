@@ -20,6 +20,7 @@
 #include <Python.h>
 #include <ATen/dlpack.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "lora_pool.h"
 
@@ -53,6 +54,9 @@ typedef int32_t (*block_norm_backward_fn)(const lora_block_norm_desc*, const voi
                                           const void*, void*, void*, void*, float*, float*,
                                           int32_t, int32_t, void*, int64_t, void*);
 
+typedef int32_t (*clip_grads_fn)(const lora_grad_list*, const void*, float, float*, void*, int64_t,
+                                 void*);
+
 /* the typedefs match the header's declarations */
 _Static_assert(__builtin_types_compatible_p(__typeof__(&lora_add_rms_norm), norm_fn),
                "lora_add_rms_norm");
@@ -61,6 +65,8 @@ _Static_assert(__builtin_types_compatible_p(__typeof__(&lora_block_norm), block_
 _Static_assert(__builtin_types_compatible_p(__typeof__(&lora_block_norm_backward),
                                             block_norm_backward_fn),
                "lora_block_norm_backward");
+_Static_assert(__builtin_types_compatible_p(__typeof__(&lora_clip_grads), clip_grads_fn),
+               "lora_clip_grads");
 _Static_assert(__builtin_types_compatible_p(__typeof__(&lora_linear), linear_fn), "lora_linear");
 _Static_assert(__builtin_types_compatible_p(__typeof__(&lora_gated_ffn), gated_fn),
                "lora_gated_ffn");
@@ -73,8 +79,8 @@ _Static_assert(__builtin_types_compatible_p(__typeof__(&lora_apply_ranked), appl
 _Static_assert(__builtin_types_compatible_p(__typeof__(&lora_apply_device), apply_device_fn),
                "lora_apply_device");
 
-/* kinds of argument; D: device memory, an int or a tensor */
-enum { P = 0, I32 = 1, I64 = 2, D = 3 };
+/* kinds of argument; D: device memory, an int or a tensor; F32: as a float's bits */
+enum { P = 0, I32 = 1, I64 = 2, D = 3, F32 = 4 };
 
 typedef __int128 wide;
 
@@ -180,6 +186,13 @@ static int convert_args(PyObject* const* args, Py_ssize_t nargs, const char* nam
       const unsigned long long v = PyLong_AsUnsignedLongLong(a);
       if (v == (unsigned long long)-1 && PyErr_Occurred()) return -1;
       out[i] = v;
+    } else if (kinds[i] == F32) {
+      const double v = PyFloat_AsDouble(a);
+      if (v == -1.0 && PyErr_Occurred()) return -1;
+      const float f = (float)v;
+      uint32_t bits;
+      memcpy(&bits, &f, 4);
+      out[i] = bits;
     } else {
       const long long v = PyLong_AsLongLong(a);
       if (v == -1 && PyErr_Occurred()) return -1;
@@ -355,6 +368,31 @@ static PyObject* py_block_norm_backward(PyObject* self, PyObject* const* args, P
   return PyLong_FromLong(st);
 }
 
+/* clip_grads(fn, list, image, max_norm, norms, ws, ws_bytes, stream) */
+static PyObject* py_clip_grads(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+  (void)self;
+  static const int kinds[8] = {P, P, D, F32, D, D, I64, P};
+  static const char* const names[8] = {"fn",    "list", "image",    "max_norm",
+                                       "norms", "ws",   "ws_bytes", "stream"};
+  uint64_t a[8];
+  int64_t bytes[8];
+  if (convert_args(args, nargs, "clip_grads", kinds, names, 8, a, bytes)) return NULL;
+  const lora_grad_list* l = (const lora_grad_list*)PTR(1);
+  if (l) {
+    const wide need[8] = {0, 0, l->bytes, 0, (wide)l->groups * 4, I64V(6), 0, 0};
+    if (large_enough("clip_grads", names, 8, bytes, need, 5)) return NULL;
+  }
+  const uint32_t bits = (uint32_t)a[3];
+  float max_norm;
+  memcpy(&max_norm, &bits, 4);
+  const clip_grads_fn f = (clip_grads_fn)(uintptr_t)a[0];
+  int32_t st;
+  Py_BEGIN_ALLOW_THREADS
+  st = f(l, PTR(2), max_norm, (float*)PTR(4), PTR(5), I64V(6), PTR(7));
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(st);
+}
+
 /* linear(fn, desc, x, w, x_scale, w_scale, bias, delta, residual, out, T, ws,
  *        ws_bytes, stream) */
 static PyObject* py_linear(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
@@ -460,6 +498,9 @@ static PyMethodDef methods[] = {
      "block_norm_backward(fn, desc, dout, dsum, y, sum, gate, post_weight, pre_weight, dy, "
      "dresidual, dgate, dpost_weight, dpre_weight, accumulate, T, ws, ws_bytes, stream) -> status "
      "of lora_block_norm_backward"},
+    {"clip_grads", (PyCFunction)(void (*)(void))py_clip_grads, METH_FASTCALL,
+     "clip_grads(fn, list, image, max_norm, norms, ws, ws_bytes, stream) -> status of "
+     "lora_clip_grads"},
     {"linear", (PyCFunction)(void (*)(void))py_linear, METH_FASTCALL,
      "linear(fn, desc, x, w, x_scale, w_scale, bias, delta, residual, out, T, ws, ws_bytes, "
      "stream) -> status of lora_linear"},
