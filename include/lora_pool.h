@@ -501,6 +501,58 @@ int32_t lora_apply_ranked(const lora_pool_desc* desc, const void* A_pool, const 
                           const int32_t* slot_ranks, void* ws, int64_t ws_bytes,
                           void* meta_host, int64_t meta_host_bytes, void* stream);
 
+/* --------------------------------------------------- gradients of the delta */
+/* The backward pass of the delta path.  With u = B_a^T dy and v = A_a x in rank
+ * space, for every row t of an adapter a = ids[t] >= 0 and every slice s:
+ *   dx[t] = dx_in[t] + sum_s A_pool[a][s]^T u[t][s]
+ *   dA[a][s][r][k]     = sum over a's rows of u[t][s][r] x[t][k]
+ *   dB[a][off_s + j][r] = sum over a's rows of dy[t][off_s + j] v[t][s][r]
+ * the gradients of A_pool and B_pool as they are stored (the scale is in B: peft's
+ * lora_B has s_a times dB's).  dx_in is the base projection's part, dy W.
+ *   x, dx_in, dx [T][K], dy [T][O] of the pool's dtype; dA [max_loras][S][R][K] and
+ *   dB [max_loras][O][R] fp32
+ * Products keep fp32: u and v enter the matrix instructions of a bf16 pool in
+ * pieces of 8 bits each, three for dA and dB (24 bits), two for dx (16 bits; dx
+ * is rounded to 8).  dA and dB of the batch's adapters are overwritten, or
+ * added to where accumulate is 1; other slots' are never touched.  dx may be
+ * dx_in itself (rows without an adapter are then left alone); without dx_in
+ * (NULL) dx is the delta's part alone, zero in rows without an adapter.  dx may be
+ * NULL (dx_in then too), and dA and dB may be NULL together.
+ *
+ * lora_delta_backward_plan (host only, deterministic) sorts the rows by adapter
+ * and cuts the work; the plan serves every call with this pool's geometry and
+ * these ids (the layers of a step).  image: host memory of
+ * lora_delta_backward_image_bytes(desc, T) bytes; the caller copies its first
+ * plan->image_bytes to the GPU (16-byte aligned).  Errors: LORA_E_ID for an id
+ * outside [-1, max_loras), LORA_E_WORKSPACE, LORA_E_ARG, LORA_E_SHAPE for T > 2^21.
+ * The kernels skip rows, slots and pieces of the device image that are out of
+ * range.  The workspace's size depends on the pool and T alone and does not
+ * shrink as T grows. */
+typedef struct {
+  int32_t rows;        /* with an adapter */
+  int32_t none;        /* without */
+  int32_t tiles;       /* of at most 64 rows of one adapter */
+  int32_t none_tiles;  /* of at most 64 rows without one, behind them */
+  int32_t parts;       /* pieces of adapters' rows */
+  int32_t multi;       /* adapters of more than one piece */
+  int32_t partials;    /* their pieces */
+  int32_t chunk;       /* columns of a part of the reductions to rank space */
+  int64_t image_bytes;
+  int64_t off_perm;    /* int32 offsets inside the image: perm[rows + none], */
+  int64_t off_tiles;   /* {slot or -1, rows, first row, 0}, */
+  int64_t off_parts;   /* {slot, rows, first row, partial or -1}, */
+  int64_t off_multi;   /* {slot, first partial, partials, 0} */
+} lora_delta_plan;
+
+int64_t lora_delta_backward_image_bytes(const lora_pool_desc* desc, int32_t T);
+int32_t lora_delta_backward_plan(const lora_pool_desc* desc, int32_t T, const int32_t* ids_host,
+                                 void* image, int64_t image_bytes, lora_delta_plan* plan);
+int64_t lora_delta_backward_workspace_bytes(const lora_pool_desc* desc, int32_t T);
+int32_t lora_delta_backward(const lora_pool_desc* desc, const void* A_pool, const void* B_pool,
+                            const void* x, const void* dy, const void* dx_in, void* dx, float* dA,
+                            float* dB, int32_t T, const lora_delta_plan* plan, const void* image,
+                            int32_t accumulate, void* ws, int64_t ws_bytes, void* stream);
+
 /* ------------------------------------------------ decoder-block operators */
 /* The base model's half of the layer that the adapters' delta joins: norm,
  * projection, gated feed-forward block and that block's gradients.  All

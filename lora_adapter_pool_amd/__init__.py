@@ -18,7 +18,8 @@ from ._lib import (  # noqa: F401
     lora_gated_ffn_backward, lora_gated_ffn_backward_workspace_bytes,
     make_block_norm_desc, lora_block_norm, lora_block_norm_backward,
     lora_block_norm_backward_workspace_bytes, GradList, lora_grad_list_build, lora_clip_grads,
-    lora_clip_grads_workspace_bytes,
+    lora_clip_grads_workspace_bytes, lora_delta_backward_plan, lora_delta_backward,
+    lora_delta_backward_image_bytes, lora_delta_backward_workspace_bytes,
 )
 from .mlp import LoraMlp  # noqa: F401
 from .pool import LoraPool  # noqa: F401

@@ -76,6 +76,15 @@ class lora_gated_desc(ctypes.Structure):
                 ("act", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class lora_delta_plan(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("none", ctypes.c_int32), ("tiles", ctypes.c_int32),
+                ("none_tiles", ctypes.c_int32), ("parts", ctypes.c_int32),
+                ("multi", ctypes.c_int32), ("partials", ctypes.c_int32),
+                ("chunk", ctypes.c_int32), ("image_bytes", ctypes.c_int64),
+                ("off_perm", ctypes.c_int64), ("off_tiles", ctypes.c_int64),
+                ("off_parts", ctypes.c_int64), ("off_multi", ctypes.c_int64)]
+
+
 class lora_grad_list(ctypes.Structure):
     _fields_ = [("chunks", ctypes.c_int32), ("groups", ctypes.c_int32),
                 ("most_chunks", ctypes.c_int32), ("empty", ctypes.c_int32),
@@ -124,6 +133,7 @@ _I64 = ctypes.c_int64
 _DP = ctypes.POINTER(lora_pool_desc)
 _NP = ctypes.POINTER(lora_norm_desc)
 _BP = ctypes.POINTER(lora_block_norm_desc)
+_XP = ctypes.POINTER(lora_delta_plan)
 _CP = ctypes.POINTER(lora_grad_list)
 _LP = ctypes.POINTER(lora_linear_desc)
 _GP = ctypes.POINTER(lora_gated_desc)
@@ -167,6 +177,10 @@ _SIGNATURES = {
     "lora_block_norm": (_I32, [_BP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I32, _P]),
     "lora_block_norm_backward_workspace_bytes": (_I64, [_BP, _I32]),
     "lora_block_norm_backward": (_I32, [_BP] + [_P] * 12 + [_I32, _I32, _P, _I64, _P]),
+    "lora_delta_backward_image_bytes": (_I64, [_DP, _I32]),
+    "lora_delta_backward_plan": (_I32, [_DP, _I32, _P, _P, _I64, _XP]),
+    "lora_delta_backward_workspace_bytes": (_I64, [_DP, _I32]),
+    "lora_delta_backward": (_I32, [_DP] + [_P] * 8 + [_I32, _XP, _P, _I32, _P, _I64, _P]),
     "lora_grad_list_bytes": (_I64, [_P, _I32, _I32]),
     "lora_grad_list_build": (_I32, [_P, _I32, _I32, _P, _I64, _CP]),
     "lora_clip_grads_workspace_bytes": (_I64, [_CP]),
@@ -666,6 +680,45 @@ def lora_gated_ffn_backward(desc, dout, pre, x, w, dpre, dx, dw, T, ws, ws_bytes
                                        ctypes.addressof(desc), dout, pre, x,
                                        w, dpre, dx, dw, int(T), ws,
                                        int(ws_bytes), _stream(stream)))
+
+
+# ----------------------------------------------------- gradients of the delta
+
+def lora_delta_backward_plan(desc, ids, image: Optional[np.ndarray] = None):
+    """(plan, image) of a batch's rows: ids int32 per row, -1 without an adapter.  The
+    image (int32; into `image`, an array of lora_delta_backward_image_bytes, or a new
+    one) goes to the GPU, and both serve every call with this geometry and these ids."""
+    ids = np.ascontiguousarray(np.asarray(ids, dtype=np.int32))
+    if ids.ndim != 1:
+        raise LoraError(LORA_E_SHAPE, "ids must have one dimension")
+    T = int(ids.shape[0])
+    if image is None:
+        image = np.empty(_check(lib().lora_delta_backward_image_bytes(ctypes.byref(desc), T)) // 4,
+                         np.int32)
+    elif image.dtype != np.int32 or not image.flags.c_contiguous:
+        raise LoraError(LORA_E_SHAPE, "image must be a contiguous int32 array")
+    plan = lora_delta_plan()
+    _check(lib().lora_delta_backward_plan(ctypes.byref(desc), T, ids.ctypes.data if T else None,
+                                          image.ctypes.data, image.nbytes, ctypes.byref(plan)))
+    return plan, image[:plan.image_bytes // 4]
+
+
+def lora_delta_backward_image_bytes(desc, T: int) -> int:
+    return _check(lib().lora_delta_backward_image_bytes(ctypes.byref(desc), int(T)))
+
+
+def lora_delta_backward_workspace_bytes(desc, T: int) -> int:
+    return _check(lib().lora_delta_backward_workspace_bytes(ctypes.byref(desc), int(T)))
+
+
+def lora_delta_backward(desc, A_pool, B_pool, x, dy, dx_in, dx, dA, dB, T, plan, image, accumulate,
+                        ws, ws_bytes, stream=None) -> None:
+    """dx = dx_in + the delta's part; dA, dB (fp32) of the batch's adapters, overwritten or
+    added to.  plan and image: lora_delta_backward_plan's, the image on the GPU."""
+    _check(pycall().delta_backward(entry_address("lora_delta_backward"), ctypes.addressof(desc),
+                                   A_pool, B_pool, x, dy, dx_in, dx, dA, dB, T,
+                                   ctypes.addressof(plan), image, int(accumulate), ws, ws_bytes,
+                                   _stream(stream)))
 
 
 # ------------------------------------------------------------ gradient norms

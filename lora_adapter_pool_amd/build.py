@@ -22,7 +22,7 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
 SOURCES = ["lora_host.cpp", "lora_kernels.hip", "lora_meta.hip", "lora_merge.hip", "lora_api.hip",
            "lora_norm.hip", "lora_block_norm.hip", "lora_clip.hip",
-           "lora_block.hip", "lora_gemm_bf16.hip", "lora_gemm_e4m3.hip",
+           "lora_delta_plan.cpp", "lora_delta.hip", "lora_block.hip", "lora_gemm_bf16.hip", "lora_gemm_e4m3.hip",
            "lora_gemm_f32.hip"]
 ARCH = os.environ.get("LORA_POOL_ARCH", "gfx950")
 

@@ -57,6 +57,11 @@ typedef int32_t (*block_norm_backward_fn)(const lora_block_norm_desc*, const voi
 typedef int32_t (*clip_grads_fn)(const lora_grad_list*, const void*, float, float*, void*, int64_t,
                                  void*);
 
+typedef int32_t (*delta_backward_fn)(const lora_pool_desc*, const void*, const void*, const void*,
+                                     const void*, const void*, void*, float*, float*, int32_t,
+                                     const lora_delta_plan*, const void*, int32_t, void*, int64_t,
+                                     void*);
+
 /* the typedefs match the header's declarations */
 _Static_assert(__builtin_types_compatible_p(__typeof__(&lora_add_rms_norm), norm_fn),
                "lora_add_rms_norm");
@@ -65,6 +70,8 @@ _Static_assert(__builtin_types_compatible_p(__typeof__(&lora_block_norm), block_
 _Static_assert(__builtin_types_compatible_p(__typeof__(&lora_block_norm_backward),
                                             block_norm_backward_fn),
                "lora_block_norm_backward");
+_Static_assert(__builtin_types_compatible_p(__typeof__(&lora_delta_backward), delta_backward_fn),
+               "lora_delta_backward");
 _Static_assert(__builtin_types_compatible_p(__typeof__(&lora_clip_grads), clip_grads_fn),
                "lora_clip_grads");
 _Static_assert(__builtin_types_compatible_p(__typeof__(&lora_linear), linear_fn), "lora_linear");
@@ -368,6 +375,40 @@ static PyObject* py_block_norm_backward(PyObject* self, PyObject* const* args, P
   return PyLong_FromLong(st);
 }
 
+/* delta_backward(fn, desc, A_pool, B_pool, x, dy, dx_in, dx, dA, dB, T, plan, image,
+ *                accumulate, ws, ws_bytes, stream) */
+static PyObject* py_delta_backward(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+  (void)self;
+  static const int kinds[17] = {P, P, D, D, D, D, D, D, D, D, I32, P, D, I32, D, I64, P};
+  static const char* const names[17] = {"fn",    "desc",       "A_pool", "B_pool",   "x",     "dy",
+                                        "dx_in", "dx",         "dA",     "dB",       "T",     "plan",
+                                        "image", "accumulate", "ws",     "ws_bytes", "stream"};
+  uint64_t a[17];
+  int64_t bytes[17];
+  if (convert_args(args, nargs, "delta_backward", kinds, names, 17, a, bytes)) return NULL;
+  const lora_pool_desc* d = (const lora_pool_desc*)PTR(1);
+  const lora_delta_plan* p = (const lora_delta_plan*)PTR(11);
+  const int32_t T = I32V(10);
+  if (d && p && T > 0 && d->num_slices >= 1 && d->num_slices <= LORA_MAX_SLICES) {
+    const wide K = d->in_features, e = size_of(d->dtype), rows = T;
+    wide O = 0;
+    for (int s = 0; s < d->num_slices; ++s) O += d->out_features[s];
+    const wide A = (wide)d->max_loras * d->num_slices * d->max_lora_rank * K;
+    const wide B = (wide)d->max_loras * O * d->max_lora_rank;
+    const wide need[17] = {0,     0,     A * e, B * e, rows * K * e, rows * O * e, rows * K * e,
+                           rows * K * e, A * 4, B * 4, 0,            0, p->image_bytes, 0,
+                           I64V(15), 0, 0};
+    if (large_enough("delta_backward", names, 17, bytes, need, 14)) return NULL;
+  }
+  const delta_backward_fn f = (delta_backward_fn)(uintptr_t)a[0];
+  int32_t st;
+  Py_BEGIN_ALLOW_THREADS
+  st = f(d, PTR(2), PTR(3), PTR(4), PTR(5), PTR(6), PTR(7), (float*)PTR(8), (float*)PTR(9), T, p,
+         PTR(12), I32V(13), PTR(14), I64V(15), PTR(16));
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(st);
+}
+
 /* clip_grads(fn, list, image, max_norm, norms, ws, ws_bytes, stream) */
 static PyObject* py_clip_grads(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
   (void)self;
@@ -498,6 +539,9 @@ static PyMethodDef methods[] = {
      "block_norm_backward(fn, desc, dout, dsum, y, sum, gate, post_weight, pre_weight, dy, "
      "dresidual, dgate, dpost_weight, dpre_weight, accumulate, T, ws, ws_bytes, stream) -> status "
      "of lora_block_norm_backward"},
+    {"delta_backward", (PyCFunction)(void (*)(void))py_delta_backward, METH_FASTCALL,
+     "delta_backward(fn, desc, A_pool, B_pool, x, dy, dx_in, dx, dA, dB, T, plan, image, "
+     "accumulate, ws, ws_bytes, stream) -> status of lora_delta_backward"},
     {"clip_grads", (PyCFunction)(void (*)(void))py_clip_grads, METH_FASTCALL,
      "clip_grads(fn, list, image, max_norm, norms, ws, ws_bytes, stream) -> status of "
      "lora_clip_grads"},
