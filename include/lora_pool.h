@@ -540,7 +540,7 @@ typedef struct {
   int64_t image_bytes;
   int64_t off_perm;    /* int32 offsets inside the image: perm[rows + none], */
   int64_t off_tiles;   /* {slot or -1, rows, first row, 0}, */
-  int64_t off_parts;   /* {slot, rows, first row, partial or -1}, */
+  int64_t off_parts;   /* {slot, rows, first tile, partial or -1}, */
   int64_t off_multi;   /* {slot, first partial, partials, 0} */
 } lora_delta_plan;
 

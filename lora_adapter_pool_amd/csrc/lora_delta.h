@@ -7,9 +7,9 @@
 namespace lora {
 
 constexpr int kDeltaTileRows = 64;      // rows of a shrink's or a dx's workgroup
-constexpr int kDeltaColumnBytes = 256;  // columns of a gradient's workgroup, in stored bytes
-constexpr int kDeltaColumns = 512;      // columns of a dx's workgroup
-constexpr int64_t kDeltaAim = 512;      // workgroups wanted, two a compute unit
+constexpr int kDeltaColumnBytes = 512;  // columns of a gradient's workgroup, in stored bytes
+constexpr int64_t kDeltaAim = 512;      // workgroups of the gradients, two a compute unit
+constexpr int64_t kDeltaShrinks = 256;  // workgroups of the ranks, one a compute unit
 constexpr int kDeltaMaxSplits = 8;
 
 // Rank tiles of 16 in a rank block, rank blocks, and the ranks they pad to.
@@ -25,11 +25,11 @@ inline int32_t delta_column_tile(const Geo& g) {
   return kDeltaColumnBytes / (int32_t)elem_bytes(g.dtype);
 }
 
-// Bytes of the parts of a workspace: the rows' rank-space values (u of every
-// slice, then v of every slice) as the products take them, partials of their
-// reductions, partials of the gradients.
+// A workspace's parts (byte offsets): the rows' rank-space values (u of every slice,
+// then v of every slice) ranks outside, u rows outside, partials of their reductions,
+// partials of the gradients.
 struct DeltaLayout {
-  int64_t ranks, partial, grads, total;  // byte offsets of the last two, and the end
+  int64_t turned, straight, partial, grads, total;
 };
 DeltaLayout delta_layout(const Geo& g, int32_t T);
 

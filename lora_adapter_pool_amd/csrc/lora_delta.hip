@@ -2,12 +2,12 @@
 // space, dx += A^T u, dA = u x^T and dB = dy v^T summed over each adapter's rows.
 //
 // Launches, all over the host plan's records:
-//   1 ranks   u and v of 64-row tiles (reductions over out and in features, cut
-//             into parts where tiles are few)
-//   2 join    adds the parts, where there are any
-//   3 spread  dx of 64-row tiles by 512 columns; dA and dB of a piece of an
-//             adapter's rows by 256 bytes of columns
-//   4 sums    adds the partials of adapters whose rows were cut
+//   1 ranks  u and v of 64-row tiles (reductions over out and in features, cut
+//            into parts where tiles are few)
+//   2 join   adds the parts, where there are any
+//   3 dx     of 64-row tiles by 256 bytes of columns
+//   4 grads  dA and dB of a piece of an adapter's rows by 512 bytes of columns
+//   5 sums   adds the partials of adapters whose rows were cut
 //
 // Every product is MFMA (16x16x32 bf16, 16x16x4 fp32).  The ranks are at most a
 // few hundred, so that every product is bound by memory: x and dy are read twice
@@ -27,10 +27,13 @@ using gemm::barrier;
 using gemm::bk_half4;
 using gemm::bk_u32x2;
 using gemm::kZeros;
+using gemm::load_lds;
 using gemm::read_columns;
 using gemm::wait_all_lds;
 
-constexpr int kPlanes = 3;  // bf16 pieces of an fp32 value
+constexpr int kMaxFeatures = 1 << 22;
+constexpr int kPlanes = 3;       // bf16 pieces of an fp32 value
+constexpr int kGradsStages = 4;  // of 32 rows
 
 struct DeltaArgs {
   const char* A;
@@ -45,26 +48,25 @@ struct DeltaArgs {
   const int32_t* tiles;
   const int32_t* parts;
   const int32_t* multi;
-  char* ranks;      // bf16: [planes][2 S][rows][padded]; fp32: [2 S][rows][padded]
-  float* partial;   // [splits][2 S][rows][padded]
+  char* turned;     // rank space, ranks outside
+  char* straight;   // u, rows outside
+  float* partial;   // [splits][2 S][slots][padded]
   float* grads;     // [partials][values of a slot]
   int32_t num_tiles, none_tiles, num_parts, num_multi;
   int32_t rows;     // with an adapter
+  int64_t slots;    // 64 a tile
   int32_t partials;
   int32_t all;      // rows of x, dy, dx
   int32_t max_loras, K, S, O, R;
   int32_t padded, blocks;
   int32_t chunk;
   int32_t accumulate;
-  int32_t dx_blocks, dx_groups;  // workgroups of dx, of them for one tile
+  int32_t jobs;       // workgroups of the ranks for one tile
+  int32_t dx_groups;  // of dx for one tile
   int32_t out[LORA_MAX_SLICES], off[LORA_MAX_SLICES];
 };
 
 constexpr int es(int dt) { return dt == LORA_BF16 ? 2 : 4; }
-
-__device__ __forceinline__ int64_t plane_values(const DeltaArgs& a) {
-  return (int64_t)2 * a.S * a.rows * a.padded;
-}
 
 // ---- operands in LDS: rows of RB bytes, 16-byte pieces in an order that keeps
 // the reads below free of bank conflicts
@@ -77,11 +79,11 @@ __device__ __forceinline__ int row_place(int p, int r) { return p ^ (r & 7); }
 template <int DT, int RB>
 __device__ __forceinline__ int column_place(int c, int k) {
   if constexpr (DT == LORA_F32) {
-    if constexpr (RB == 256) return c ^ (((k >> 3) & 3) << 6);
+    if constexpr (RB >= 256) return c ^ (((k >> 3) & 3) << 6);
     if constexpr (RB == 128) return c ^ (((k >> 3) & 1) << 6);
     return c;
   }
-  if constexpr (RB == 256) return c ^ (((k & 3) | ((k >> 3) & 1) << 2) << 5);
+  if constexpr (RB >= 256) return c ^ (((k & 3) | ((k >> 3) & 1) << 2) << 5);
   if constexpr (RB == 128) return c ^ ((((k >> 1) & 1) | ((k >> 3) & 1) << 1) << 5);
   if constexpr (RB == 64) return c ^ (((k >> 3) & 1) << 5);
   return c;
@@ -184,338 +186,463 @@ __device__ __forceinline__ void pieces_of(const float (&v)[4], bk_u32x2 (&p)[kPl
 
 typedef const __attribute__((address_space(4))) int32_t* scalar_words;
 
-// Four values of a row's ranks, `at` their place in [2 S][rows][padded].
-template <int DT>
-__device__ __forceinline__ void put_ranks(const DeltaArgs& a, int64_t at, const float (&v)[4]) {
+// Where a value of rank space is kept: `turned` [planes][2 S][padded][slots], ranks
+// outside (a gradient's operand, whose reduction is over the rows), and for u also
+// `straight` [planes][S][slots][padded] (dx's operand).  slots: 64 for every tile;
+// those past a tile's rows are zero.
+__device__ __forceinline__ int64_t turned_values(const DeltaArgs& a) {
+  return (int64_t)2 * a.S * a.padded * a.slots;
+}
+__device__ __forceinline__ int64_t straight_values(const DeltaArgs& a) {
+  return (int64_t)a.S * a.padded * a.slots;
+}
+
+// Stores N values (4, or 8 and more in eights) as they are kept, pieces `apart` values
+// from each other.
+template <int DT, int N>
+__device__ __forceinline__ void keep(char* base, int64_t at, int64_t apart, int planes,
+                                     const float (&v)[N]) {
   if constexpr (DT == LORA_F32) {
-    *reinterpret_cast<bk_f32x4*>(a.ranks + at * 4) = bk_f32x4{v[0], v[1], v[2], v[3]};
-  } else {
-    bk_u32x2 p[kPlanes];
-    pieces_of(v, p);
 #pragma unroll
-    for (int k = 0; k < kPlanes; ++k)
-      *reinterpret_cast<bk_u32x2*>(a.ranks + (k * plane_values(a) + at) * 2) = p[k];
+    for (int i = 0; i < N; i += 4)
+      *reinterpret_cast<bk_f32x4*>(base + (at + i) * 4) =
+          bk_f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float w[4] = {v[i], v[i + 1], v[i + 2], v[i + 3]};
+      bk_u32x2 p[kPlanes];
+      pieces_of(w, p);
+#pragma unroll
+      for (int k = 0; k < kPlanes; ++k)
+        if (k < planes) *reinterpret_cast<bk_u32x2*>(base + (k * apart + at + i) * 2) = p[k];
+    }
+  }
+}
+
+// A tile's values of one rank block, from LDS ([64][LD], the sums already in it).
+template <int DT, int NT>
+__device__ __forceinline__ void finish_ranks(const DeltaArgs& a, const float* sums, int q, int tile,
+                                             int rank0) {
+  constexpr int RB = 16 * NT, LD = RB + 4, N = RB / 4;  // N rows a thread
+  const int tid = threadIdx.x;
+  {
+    const int r = tid % RB, row = tid / RB * N;
+    float v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = sums[(row + i) * LD + r];
+    keep<DT, N>(a.turned, ((int64_t)q * a.padded + rank0 + r) * a.slots + tile * 64 + row,
+                turned_values(a), kPlanes, v);
+  }
+  if (q >= a.S || !a.dx) return;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int o = (i * 256 + tid) * 4, row = o / RB, r = o % RB;
+    const bk_f32x4 w = *reinterpret_cast<const bk_f32x4*>(sums + row * LD + r);
+    const float v[4] = {w[0], w[1], w[2], w[3]};
+    keep<DT, 4>(a.straight, ((int64_t)q * a.slots + tile * 64 + row) * a.padded + rank0 + r,
+                straight_values(a), 2, v);
   }
 }
 
 // ------------------------------------------------------------- 1: rank space
 //
 // One workgroup: 64 rows of one adapter, one rank block, one part of one
-// reduction.  A ring of four stages of 128 bytes of the reduction (x or dy rows,
-// and A rows or B's rows as columns), filled by direct loads; a wave multiplies 16
-// rows with all ranks of the block.
+// reduction, which its four waves share: wave w takes every fourth 128 bytes of it,
+// multiplies all rows with all ranks of the block, and the waves' sums meet in LDS at
+// the end.  So nothing waits for another wave on the way: x or dy comes straight to
+// registers, two steps ahead, and A or B through the wave's own part of LDS (B is
+// read as columns there).
+template <int DT, int NT>
+constexpr int ranks_lds() {
+  const int ring = 4 * 2 * 16 * NT * 128, sums = 4 * 64 * (16 * NT + 4) * 4;
+  return ring > sums ? ring : sums;
+}
+template <int N>
+struct Count {
+  static constexpr int value = N;
+};
 template <int DT, int NT, bool kOut>  // kOut: u, from dy and B; else v, from x and A
-__device__ __forceinline__ void ranks_tile(const DeltaArgs& a, char* lds, int slot, int rows,
-                                           int first, int s, int rank0, int part) {
-  constexpr int ES = es(DT), KS = 128 / ES;   // reduction indexes a stage
+__device__ __forceinline__ void ranks_tile(const DeltaArgs& a, char* lds, int tile, int slot,
+                                           int rows, int first, int s, int rank0, int part) {
+  constexpr int ES = es(DT), KS = 128 / ES;   // reduction indexes a step
+  constexpr int QS = KS / 32, XV = sizeof(Frag<DT>) / 16;
   constexpr int WB = 16 * NT * ES;            // bytes of a column row of B
-  constexpr int XB = 64 * 128, STAGE = XB + 16 * NT * 128, NST = 4;
-  constexpr int WL = (NT + 1) / 2;            // loads of a wave for the weights
-  constexpr int LOADS = 2 + WL;
-  static_assert(KS * WB == 16 * NT * 128, "");
+  constexpr int WL = 2 * NT, SLOT = WL * 1024;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const int len = kOut ? a.out[s] : a.K;
   const int lo = part * a.chunk, hi = lo + a.chunk < len ? lo + a.chunk : len;
-  const int nk = (hi - lo + KS - 1) / KS;
+  const int all = (hi - lo + KS - 1) / KS;          // steps of the workgroup
+  const int nk = (all - wave + 3) / 4;              // of this wave (it may be 0)
+  const int nr = (rows + 15) / 16;                  // row tiles that hold rows
+  char* const ring = lds + wave * 2 * SLOT;
 
-  // what this lane loads: two pieces of rows, WL pieces of the weights
-  const char* xp[2];
-  int xk[2];  // reduction index of the piece in a stage
+  // Rows past the last one read row 0 of the batch: their sums are not kept.
+  const char* xp[4];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int r = 8 * (2 * wave + j) + (lane >> 3), p = row_place(lane & 7, r);
-    const int t = r < rows ? a.perm[first + r] : -1;
-    xk[j] = p * (16 / ES);
-    xp[j] = t < 0 || t >= a.all ? nullptr
-            : kOut ? a.dy + ((int64_t)t * a.O + a.off[s] + lo + xk[j]) * ES
-                   : a.x + ((int64_t)t * a.K + lo + xk[j]) * ES;
+  for (int i = 0; i < 4; ++i) {
+    const int r = 16 * i + l16;
+    int t = r < rows ? a.perm[first + r] : 0;
+    if (t < 0 || t >= a.all) t = 0;
+    const int64_t k = lo + wave * KS + 8 * g;
+    xp[i] = kOut ? a.dy + ((int64_t)t * a.O + a.off[s] + k) * ES : a.x + ((int64_t)t * a.K + k) * ES;
   }
-  const char* wp[WL];
-  int wk[WL];
-  int64_t step;
-#pragma unroll
-  for (int j = 0; j < WL; ++j) {
-    const int i = NT == 1 ? wave & 1 : WL * wave + j;  // (NT = 1: two waves load the same)
+  // the weights' block of the step, and a lane's place in each 1 KB of it
+  const char* wbase =
+      kOut ? a.B + (((int64_t)slot * a.O + a.off[s] + lo + wave * KS) * a.R + rank0) * ES
+           : a.A + ((((int64_t)slot * a.S + s) * a.R + rank0) * a.K + lo + wave * KS) * ES;
+  const int64_t wstep = kOut ? (int64_t)4 * KS * a.R * ES : 512;
+  // reduction index and rank of a lane's piece of the j-th KB of a step
+  auto place = [&](int ln, int j, int& k, int& r) {
     if constexpr (kOut) {
-      const int o = i * 1024 + lane * 16, k = o / WB, c = column_place<DT, WB>(o % WB, k);
-      wk[j] = k;
-      wp[j] = rank0 + c / ES < a.R
-                  ? a.B + (((int64_t)slot * a.O + a.off[s] + lo + k) * a.R + rank0) * ES + c
-                  : nullptr;
-      step = (int64_t)KS * a.R * ES;
+      const int o = j * 1024 + ln * 16;
+      k = o / WB;
+      r = column_place<DT, WB>(o % WB, k) / ES;
     } else {
-      const int r = i * 8 + (lane >> 3), p = row_place(lane & 7, r);
-      wk[j] = p * (16 / ES);
-      wp[j] = rank0 + r < a.R
-                  ? a.A + ((((int64_t)slot * a.S + s) * a.R + rank0 + r) * a.K + lo + wk[j]) * ES
-                  : nullptr;
-      step = 128;
-    }
-  }
-  auto load = [&](int kt) {
-    char* to = lds + (kt % NST) * STAGE;
-    const int left = kt < nk ? hi - lo - kt * KS : 0;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      to_lds(xp[j] && xk[j] < left ? xp[j] + kt * 128 : zeros(), to + (2 * wave + j) * 1024);
-#pragma unroll
-    for (int j = 0; j < WL; ++j) {
-      const int i = NT == 1 ? wave & 1 : WL * wave + j;
-      to_lds(wp[j] && wk[j] < left ? wp[j] + kt * step : zeros(), to + XB + i * 1024);
+      r = j * 8 + (ln >> 3);
+      k = row_place(ln & 7, r) * (16 / ES);
     }
   };
-  bk_f32x4 acc[NT] = {};
+  auto offset = [&](int k, int r) {
+    return (uint32_t)(kOut ? k * a.R + r : r * a.K + k) * (uint32_t)ES;
+  };
+  uint32_t off[kOut ? WL : 1];
 #pragma unroll
-  for (int i = 0; i < NST - 1; ++i) load(i);
-  for (int kt = 0; kt < nk; ++kt) {
-    wait_loads<(NST - 2) * LOADS>();
-    barrier();
-    load(kt + NST - 1);  // (past the end: zeros, so that the count of loads holds)
-    const char* at = lds + (kt % NST) * STAGE;
+  for (int j = 0; j < (kOut ? WL : 1); ++j) {
+    int k, r;
+    place(lane, j, k, r);
+    off[j] = offset(k, r);
+  }
+  struct Rows {
+    Frag<DT> f[4][QS];
+  };
+  auto load_w = [&](int i) {
+    char* to = ring + (i & 1) * SLOT;
+    const char* from = wbase + i * wstep;
+    const int left = hi - lo - (wave + 4 * i) * KS, ranks = a.R - rank0;
+    if (left >= KS && ranks >= 16 * NT) {
 #pragma unroll
-    for (int q = 0; q < KS / 32; ++q) {
-      const Frag<DT> x = read_rows<DT>(at, 16 * wave + l16, g, q);
+      for (int j = 0; j < WL; ++j)
+        load_lds(from, kOut ? off[kOut ? j : 0] : off[0] + (uint32_t)(j * 8 * ES) * (uint32_t)a.K,
+                 to + j * 1024);
+    } else {
+      int ln = lane;
+      asm volatile("" : "+v"(ln));  // (so that the places are not kept in registers)
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const Frag<DT> w = kOut
-            ? read_cols<DT, WB>(at + XB, 32 * q, 16 * i, 4, l16, g)
-            : read_rows<DT>(at + XB, 16 * i + l16, g, q);
-        acc[i] = product<DT>(w, x, acc[i]);
+      for (int j = 0; j < WL; ++j) {
+        int k, r;
+        place(ln, j, k, r);
+        to_lds(k < left && r < ranks ? from + offset(k, r) : zeros(), to + j * 1024);
       }
     }
+  };
+  auto load_x = [&](int i, Rows& x) {
+    const int left = hi - lo - (wave + 4 * i) * KS;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      if (t >= nr) break;
+#pragma unroll
+      for (int q = 0; q < QS; ++q)
+#pragma unroll
+        for (int h = 0; h < XV; ++h) {
+          const bk_u32x4* p =
+              reinterpret_cast<const bk_u32x4*>(xp[t] + (int64_t)i * 512 + q * 32 * ES) + h;
+          // (a reduction's last step may end inside: zeros, as for the weights)
+          if (left >= KS)
+            x.f[t][q].v[h] = *p;
+          else
+            x.f[t][q].v[h] = 32 * q + 8 * g + h * 4 < left ? *p : bk_u32x4{0, 0, 0, 0};
+        }
+    }
+  };
+  bk_f32x4 acc[4][NT] = {};
+  // What follows step i's loads: those of step i + 1, and none behind the last.
+  auto arrived = [&](bool last) {
+    if (last)
+      wait_loads<0>();
+    else if (nr == 1)
+      wait_loads<WL + QS * XV>();
+    else if (nr == 2)
+      wait_loads<WL + 2 * QS * XV>();
+    else if (nr == 3)
+      wait_loads<WL + 3 * QS * XV>();
+    else
+      wait_loads<WL + 4 * QS * XV>();
+    asm volatile("" ::: "memory");
+  };
+  auto multiply = [&](int i, const Rows& x) {
+    const char* at = ring + (i & 1) * SLOT;
+#pragma unroll
+    for (int q = 0; q < QS; ++q) {
+      Frag<DT> w[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        w[j] = kOut ? read_cols<DT, WB>(at, 32 * q, 16 * j, 4, l16, g)
+                    : read_rows<DT>(at, 16 * j + l16, g, q);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        if (t >= nr) break;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[t][j] = product<DT>(w[j], x.f[t][q], acc[t][j]);
+      }
+    }
+  };
+  auto load = [&](int i, Rows& x) {
+    // the slot's reads are done before its place is filled again
+    __builtin_amdgcn_s_waitcnt(wait_all_lds(63));
+    asm volatile("" ::: "memory");
+    load_w(i);
+    asm volatile("" ::: "memory");
+    load_x(i, x);
+    asm volatile("" ::: "memory");
+  };
+  Rows x[2];
+  if (nk > 0) load(0, x[0]);
+  if (nk > 1) load(1, x[1]);
+  for (int i = 0; i < nk; i += 2) {
+    arrived(i + 1 >= nk);
+    multiply(i, x[0]);
+    if (i + 2 < nk) load(i + 2, x[0]);
+    if (i + 1 < nk) {
+      arrived(i + 2 >= nk);
+      multiply(i + 1, x[1]);
+      if (i + 3 < nk) load(i + 3, x[1]);
+    }
   }
-  wait_loads<0>();
-  // a lane holds ranks 4 g .. 4 g + 3 of every tile, of row l16
-  const int row = 16 * wave + l16;
-  if (row >= rows) return;
+  // a lane holds ranks 4 g .. 4 g + 3 of every rank tile, of row l16 of every row tile
+  constexpr int RB = 16 * NT, LD = RB + 4;
+  float* const sums = reinterpret_cast<float*>(lds);
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const bool in = 16 * t + l16 < rows;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      *reinterpret_cast<bk_f32x4*>(sums + (wave * 64 + 16 * t + l16) * LD + 16 * j + 4 * g) =
+          in ? acc[t][j] : bk_f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  __syncthreads();
   const int q = kOut ? s : a.S + s;
-  const int64_t at = ((int64_t)q * a.rows + first + row) * a.padded + rank0 + 4 * g;
   const bool whole = a.chunk >= len;
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    const float v[4] = {acc[i][0], acc[i][1], acc[i][2], acc[i][3]};
+    const int o = (i * 256 + (int)threadIdx.x) * 4, row = o / RB, r = o % RB;
+    bk_f32x4* p = reinterpret_cast<bk_f32x4*>(sums + row * LD + r);
+    bk_f32x4 v = *p;
+#pragma unroll
+    for (int w = 1; w < 4; ++w) v += *reinterpret_cast<bk_f32x4*>(sums + (w * 64 + row) * LD + r);
     if (whole)
-      put_ranks<DT>(a, at + 16 * i, v);
+      *p = v;
     else
-      *reinterpret_cast<bk_f32x4*>(a.partial + part * plane_values(a) + at + 16 * i) = acc[i];
+      *reinterpret_cast<bk_f32x4*>(
+          a.partial + (((int64_t)part * 2 * a.S + q) * a.slots + tile * 64 + row) * a.padded +
+          rank0 + r) = v;
   }
+  if (!whole) return;
+  __syncthreads();
+  finish_ranks<DT, NT>(a, sums, q, tile, rank0);
 }
 
 __device__ __forceinline__ int parts_of(int len, int chunk) { return (len + chunk - 1) / chunk; }
 
-// A record's rows, if they and its slot are in range.
-__device__ __forceinline__ bool take(const DeltaArgs& a, const int32_t* rec, int limit, int& slot,
-                                     int& rows, int& first) {
+// A tile's rows, if they and its slot are in range.
+__device__ __forceinline__ bool take_tile(const DeltaArgs& a, int tile, int& slot, int& rows,
+                                          int& first) {
+  const int32_t* rec = a.tiles + 4 * tile;
   slot = rec[0];
   rows = rec[1];
   first = rec[2];
-  return slot >= 0 && slot < a.max_loras && rows > 0 && rows <= limit && first >= 0 &&
+  return slot >= 0 && slot < a.max_loras && rows > 0 && rows <= kDeltaTileRows && first >= 0 &&
          first <= a.rows - rows;
 }
 
 template <int DT, int NT>
-__global__ __launch_bounds__(256) void ranks_kernel(DeltaArgs a) {
-  __shared__ __attribute__((aligned(16))) char lds[4 * (64 + 16 * NT) * 128];
-  // jobs of a tile together, neighbouring tiles on one XCD: they share x, dy and
-  // the weights in its L2
-  const int item = xcd_item(blockIdx.x, gridDim.x);
-  const int jobs = gridDim.x / a.num_tiles, tile = item / jobs;
-  int job = item - tile * jobs, slot, rows, first;
-  if (!take(a, a.tiles + 4 * tile, kDeltaTileRows, slot, rows, first)) return;
+__global__ __launch_bounds__(256, 2) void ranks_kernel(DeltaArgs a) {
+  __shared__ __attribute__((aligned(16))) char lds[ranks_lds<DT, NT>()];
+  // Many tiles: an XCD takes neighbouring ones, which share x, dy and the weights in
+  // its L2, and all its tiles' first job before the second, so that a compute unit
+  // gets jobs of every length.
+  int tile, job, slot, rows, first;
+  if (a.num_tiles >= 64) {
+    const int x = blockIdx.x & 7, at = blockIdx.x >> 3;
+    const int q = a.num_tiles >> 3, r = a.num_tiles & 7, n = q + (x < r);
+    job = at / n;
+    tile = x * q + (x < r ? x : r) + at - job * n;
+    if (job >= a.jobs) return;
+  } else {
+    job = blockIdx.x / a.num_tiles;
+    tile = blockIdx.x - job * a.num_tiles;
+  }
+  if (!take_tile(a, tile, slot, rows, first)) return;
   const int rank0 = job % a.blocks * 16 * NT;
   job /= a.blocks;
-  for (int s = 0; s < a.S; ++s) {
+  int s = 0;
+  for (; s < a.S; ++s) {
     const int n = parts_of(a.out[s], a.chunk);
-    if (job < n)
-      return ranks_tile<DT, NT, true>(a, lds, slot, rows, first, s, rank0, job);
+    if (job < n) break;
     job -= n;
   }
+  if (s < a.S)
+    return ranks_tile<DT, NT, true>(a, lds, tile, slot, rows, first, s, rank0, job);
   const int n = parts_of(a.K, a.chunk);
-  ranks_tile<DT, NT, false>(a, lds, slot, rows, first, job / n, rank0, job % n);
+  ranks_tile<DT, NT, false>(a, lds, tile, slot, rows, first, job / n, rank0, job % n);
 }
 
 // ------------------------------------------------------- 2: parts of the sums
-template <int DT>
+template <int DT, int NT>
 __global__ __launch_bounds__(256) void join_kernel(DeltaArgs a) {
-  const int q = blockIdx.y;
+  constexpr int RB = 16 * NT, LD = RB + 4;
+  __shared__ __attribute__((aligned(16))) float sums[64 * LD];
+  const int tile = blockIdx.x, q = blockIdx.y, rank0 = blockIdx.z * RB;
   const int n = parts_of(q < a.S ? a.out[q] : a.K, a.chunk);
   if (n == 1) return;
-  const int64_t values = (int64_t)a.rows * a.padded;
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (i >= values) return;
-  const int64_t at = q * values + i;
-  bk_f32x4 s = *reinterpret_cast<const bk_f32x4*>(a.partial + at);
-  for (int p = 1; p < n; ++p)
-    s += *reinterpret_cast<const bk_f32x4*>(a.partial + p * plane_values(a) + at);
-  const float v[4] = {s[0], s[1], s[2], s[3]};
-  put_ranks<DT>(a, at, v);
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int o = (i * 256 + (int)threadIdx.x) * 4, row = o / RB, r = o % RB;
+    const float* from = a.partial + (((int64_t)q * a.slots + tile * 64 + row) * a.padded + rank0 + r);
+    bk_f32x4 v = *reinterpret_cast<const bk_f32x4*>(from);
+    for (int p = 1; p < n; ++p) v += *reinterpret_cast<const bk_f32x4*>(from + p * turned_values(a));
+    *reinterpret_cast<bk_f32x4*>(sums + row * LD + r) = v;
+  }
+  __syncthreads();
+  finish_ranks<DT, NT>(a, sums, q, tile, rank0);
 }
 
-// ------------------------------------------------------------- 3a: the input's
+// ------------------------------------------------------------- 3: the input's
 //
-// 64 rows of one adapter (or none: a copy), 512 columns in steps of 64.  A step
-// holds up to 128 ranks of A for its columns; a wave multiplies its 16 rows' u,
-// which stay in registers where one step holds all ranks, with all 64 columns.
-// The columns are dealt to the output's index so that a lane's are neighbours.
+// 64 rows of one adapter (or none: a copy) by 256 bytes of columns: the ranks' rows of
+// A for these columns in LDS, 128 ranks at a time, a wave's 16 rows of u and of dx_in
+// straight to registers.  The columns are dealt to the output's index so that a
+// lane's are neighbours in memory.
 template <int DT>
-__device__ __forceinline__ void dx_tile(const DeltaArgs& a, char* lds, int block) {
-  constexpr int ES = es(DT), RB = 64 * ES, P = DT == LORA_BF16 ? 2 : 1;
-  constexpr int RANKS = 128, STAGE = RANKS * RB, PL = STAGE / 4096;  // loads of a wave
+__global__ __launch_bounds__(256) void dx_kernel(DeltaArgs a) {
+  constexpr int ES = es(DT), RB = 256, CB = RB / ES, RANKS = 128;
+  constexpr int P = DT == LORA_BF16 ? 2 : 1, XV = sizeof(Frag<DT>) / 16;
+  constexpr int CT = CB / 16, V = 16 / ES;  // column tiles; columns of a 16-byte piece
+  constexpr int TV = V / 4, NV = CT / TV;   // tiles a piece spans; a lane's pieces
+  __shared__ __attribute__((aligned(16))) char lds[RANKS * RB];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
-  const int tile = block / a.dx_groups;
-  const int c_lo = (block - tile * a.dx_groups) * kDeltaColumns;
-  const int c_hi = c_lo + kDeltaColumns < a.K ? c_lo + kDeltaColumns : a.K;
+  // (where the groups are a multiple of 8, one XCD takes a column group of all tiles)
+  const int tile = blockIdx.x / a.dx_groups, c0 = (blockIdx.x - tile * a.dx_groups) * CB;
   int slot, rows, first;
-  const int32_t* rec = a.tiles + 4 * tile;
   const bool none = tile >= a.num_tiles;
   if (none) {
+    const int32_t* rec = a.tiles + 4 * tile;
     rows = rec[1];
     first = rec[2];
-    if (rows < 1 || rows > kDeltaTileRows || first < a.rows || first > a.all - rows) return;
-  } else if (!take(a, rec, kDeltaTileRows, slot, rows, first)) {
+    if (a.dx_in == a.dx || rows < 1 || rows > kDeltaTileRows || first < a.rows ||
+        first > a.all - rows)
+      return;
+  } else if (!take_tile(a, tile, slot, rows, first)) {
     return;
   }
   const int row = 16 * wave + l16;
   int t = row < rows ? a.perm[first + row] : -1;
   if (t >= a.all) t = -1;
-  if (none) {
-    if (t < 0 || a.dx_in == a.dx) return;
-    for (int c = c_lo + g * (16 / ES); c < c_hi; c += 64 / ES) {
-      const int64_t at = ((int64_t)t * a.K + c) * ES;
-      bk_u32x4 v = {0, 0, 0, 0};
-      if (a.dx_in) v = *reinterpret_cast<const bk_u32x4*>(a.dx_in + at);
-      *reinterpret_cast<bk_u32x4*>(a.dx + at) = v;
-    }
-    return;
-  }
-
-  const int all_ranks = a.S * a.padded;               // of the reduction
-  const int groups = (all_ranks + RANKS - 1) / RANKS; // steps of a column step
-  const int steps = (c_hi - c_lo + 63) / 64 * groups;
-  // rank index i of the reduction is rank i % padded of slice i / padded
-  auto load = [&](int st) {
-    if (st >= steps) return;
-    const int cs = st / groups, r0 = (st - cs * groups) * RANKS;
-    char* to = lds + (st & 1) * STAGE;
+  // a lane's pieces: columns c0 + i 4 V + g V ..
+  bk_u32x4 base[NV];
 #pragma unroll
-    for (int j = 0; j < PL; ++j) {
-      const int o = (wave * PL + j) * 1024 + lane * 16, k = o / RB;
-      const int c = c_lo + cs * 64 + column_place<DT, RB>(o % RB, k) / ES;
-      const int i = r0 + k, s = i / a.padded, r = i - s * a.padded;
-      const bool in = i < all_ranks && r < a.R && c < a.K;
+  for (int i = 0; i < NV; ++i) {
+    const int c = c0 + i * 4 * V + g * V;
+    base[i] = bk_u32x4{0, 0, 0, 0};
+    if (a.dx_in && t >= 0 && c < a.K)
+      base[i] = *reinterpret_cast<const bk_u32x4*>(a.dx_in + ((int64_t)t * a.K + c) * ES);
+  }
+  bk_f32x4 acc[CT] = {};
+  const int ranks = none ? 0 : a.S * a.padded;  // of the reduction
+  for (int r0 = 0; r0 < ranks; r0 += RANKS) {
+    const int n = ranks - r0 < RANKS ? ranks - r0 : RANKS;
+    // rank index i of the reduction is rank i % padded of slice i / padded
+    for (int j = wave; j * 4 < ((n + 31) & ~31); j += 4) {
+      const int k = j * 4 + g, i = r0 + k, s = i / a.padded, r = i - s * a.padded;
+      const int c = c0 + column_place<DT, RB>(l16 * 16, k) / ES;
+      const bool in = k < n && r < a.R && c < a.K;
       to_lds(in ? a.A + ((((int64_t)slot * a.S + s) * a.R + r) * a.K + c) * ES : zeros(),
-             to + (wave * PL + j) * 1024);
+             lds + j * 1024);
     }
-  };
-  Frag<DT> u[P][RANKS / 32];
-  auto fetch = [&](int r0) {
+    Frag<DT> u[P][RANKS / 32];
 #pragma unroll
     for (int q = 0; q < RANKS / 32; ++q) {
       const int i = r0 + 32 * q + 8 * g, s = i / a.padded, r = i - s * a.padded;
-      const int64_t at = ((int64_t)s * a.rows + first + (row < rows ? row : 0)) * a.padded + r;
+      const int64_t at = ((int64_t)s * a.slots + tile * 64 + row) * a.padded + r;
 #pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const char* from = a.ranks + (p * plane_values(a) + at) * ES;
+      for (int p = 0; p < P; ++p)
 #pragma unroll
-        for (int h = 0; h < (int)(sizeof(Frag<DT>) / 16); ++h)
-          u[p][q].v[h] = i < all_ranks ? reinterpret_cast<const bk_u32x4*>(from)[h]
-                                       : bk_u32x4{0, 0, 0, 0};
-      }
+        for (int h = 0; h < XV; ++h)
+          u[p][q].v[h] =
+              i < r0 + n ? reinterpret_cast<const bk_u32x4*>(
+                               a.straight + (p * straight_values(a) + at) * ES)[h]
+                         : bk_u32x4{0, 0, 0, 0};
     }
-  };
-  bk_f32x4 acc[4] = {};
-  load(0);
-  fetch(0);
-  for (int st = 0; st < steps; ++st) {
-    const int cs = st / groups, rg = st - cs * groups;
-    if (groups > 1 && st) fetch(rg * RANKS);
     wait_loads<0>();
     barrier();
-    load(st + 1);
-    const char* at = lds + (st & 1) * STAGE;
-    const int left = all_ranks - rg * RANKS;
 #pragma unroll
     for (int q = 0; q < RANKS / 32; ++q) {
-      if (32 * q >= left) break;
+      if (32 * q >= n) break;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const Frag<DT> w = read_cols<DT, RB>(at, 32 * q, 4 * i, 16, l16, g);
+      for (int i = 0; i < CT; ++i) {
+        const Frag<DT> w =
+            read_cols<DT, RB>(lds, 32 * q, i / TV * 4 * V + i % TV * 4, V, l16, g);
 #pragma unroll
-        for (int p = 0; p < P; ++p) acc[i] = product<DT>(w, u[p][q], acc[i]);
+        for (int p = P - 1; p >= 0; --p) acc[i] = product<DT>(w, u[p][q], acc[i]);
       }
     }
-    if (rg + 1 < groups) continue;
-    // a lane holds columns 16 g .. 16 g + 15 of its row
-    const int c = c_lo + cs * 64 + 16 * g;
-    if (t >= 0) {
+    wait_loads<0>();
+    barrier();
+  }
+  if (t < 0) return;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (c + 8 * h >= c_hi) continue;
-        float z[8];
+  for (int i = 0; i < NV; ++i) {
+    const int c = c0 + i * 4 * V + g * V;
+    if (c >= a.K) continue;
+    bk_u32x4 v;
+    if constexpr (DT == LORA_BF16) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = acc[2 * h + (i >> 2)][i & 3];
-        const int64_t to = (int64_t)t * a.K + c + 8 * h;
-        if (a.dx_in) add8(z, a.dx_in, to, 8, DT);
-        store8(a.dx, to, 8, DT, z);
+      for (int j = 0; j < 4; ++j) {
+        const bk_f32x4& z = acc[2 * i + j / 2];
+        v[j] = bk_pack(z[2 * (j & 1)] + bk_lo(base[i][j]), z[2 * (j & 1) + 1] + bk_hi(base[i][j]));
       }
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = bk_f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < 4; ++j)
+        v[j] = __float_as_uint(acc[i][j] + __uint_as_float(base[i][j]));
+    }
+    *reinterpret_cast<bk_u32x4*>(a.dx + ((int64_t)t * a.K + c) * ES) = v;
   }
 }
 
-// ------------------------------------------------------ 3b: the adapters' own
+// ------------------------------------------------------ 4: the adapters' own
 //
-// One workgroup: a piece of an adapter's rows, 256 bytes of columns of x or dy,
-// one rank block.  A ring of four stages of 32 rows; both operands are
-// reduction-major (a row of memory is a reduction index).
-template <int DT, int NT>
-constexpr int grads_stage() {
-  return 32 * 256 + (DT == LORA_BF16 ? kPlanes : 1) * 32 * 16 * NT * es(DT);
-}
+// One workgroup: a piece of an adapter's rows, 512 bytes of columns of x or dy,
+// one rank block.  x or dy goes through a ring of stages of 32 rows in LDS, from which
+// both reads are of columns (a row of memory is a reduction index); a wave's 16
+// ranks of u or v come straight to registers, a step ahead.
 template <int DT, int NT, bool kOut>  // kOut: dB, from dy and v; else dA, from x and u
 __device__ __forceinline__ void grads_tile(const DeltaArgs& a, char* lds, int slot, int rows,
-                                           int first, int partial, int s, int rank0, int c0) {
-  constexpr int ES = es(DT), P = DT == LORA_BF16 ? kPlanes : 1;
-  constexpr int UB = 16 * NT * ES, UP = 32 * UB;         // a row of ranks, a plane's stage
-  constexpr int XB = 32 * 256, STAGE = XB + P * UP, NST = 4;
-  constexpr int RUNS = P * UP / 1024, UL = (RUNS + 3) / 4;  // 1 KB runs of ranks, a wave's
-  constexpr int LOADS = 2 + UL;
-  // waves: over the ranks where there are two tiles of them, and over the columns
-  constexpr int WR = NT >= 2 ? 2 : 1, WC = 4 / WR;
-  constexpr int CT = 256 / ES / 16 / WC, RT = NT / WR;   // a wave's tiles
+                                           int first, int tile, int partial, int s, int rank0,
+                                           int c0) {
+  constexpr int ES = es(DT), P = DT == LORA_BF16 ? kPlanes : 1, XV = sizeof(Frag<DT>) / 16;
+  constexpr int RB = kDeltaColumnBytes, STAGE = 32 * RB, NST = kGradsStages, LOADS = 4;
+  constexpr int CT = RB / ES / 16 / (4 / NT);  // a wave's column tiles
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const int len = kOut ? a.out[s] : a.K;
-  const int col = wave / WR * CT * 16, rank = wave % WR * RT * 16;
+  const int col = wave / NT * CT * 16, rank = rank0 + wave % NT * 16;
   const int nk = (rows + 31) / 32;
 
   const char* base = kOut ? a.dy : a.x;
   const int64_t stride = (int64_t)(kOut ? a.O : a.K) * ES;
-  int xr[2], xc[2];  // row of a stage, and column of the row in memory or -1
+  int xc[4];  // column in memory of a lane's piece, or -1: rows 8 wave + 2 j and the next
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int o = (2 * wave + j) * 1024 + lane * 16;
-    xr[j] = o / 256;
-    const int c = column_place<DT, 256>(o % 256, xr[j]) / ES;
+  for (int j = 0; j < 4; ++j) {
+    const int k = 8 * wave + 2 * j + (lane >> 5);
+    const int c = column_place<DT, RB>(lane % 32 * 16, k) / ES;
     xc[j] = c0 + c < len ? (kOut ? a.off[s] : 0) + c0 + c : -1;
-  }
-  const int q = kOut ? a.S + s : s;
-  const char* up[UL];
-  int ur[UL];
-#pragma unroll
-  for (int j = 0; j < UL; ++j) {
-    const int i = UL * wave + j < RUNS ? UL * wave + j : RUNS - 1;  // (the last one again)
-    const int o = i * 1024 + lane * 16, p = o / UP, k = o % UP / UB;
-    const int c = column_place<DT, UB>(o % UB, k);
-    ur[j] = k;
-    up[j] = a.ranks + (p * plane_values(a) + ((int64_t)q * a.rows + first + k) * a.padded + rank0) *
-                          ES + c;
   }
   // Tokens of the wave's eight rows of a stage, by scalar loads: these are not
   // counted with the direct loads, which stay in flight.  (Past the piece's last row
@@ -532,24 +659,36 @@ __device__ __forceinline__ void grads_tile(const DeltaArgs& a, char* lds, int sl
     return k;
   };
   auto load = [&](int kt, const Tokens& tok) {
-    char* to = lds + (kt % NST) * STAGE;
+    char* to = lds + (kt % NST) * STAGE + wave * 4096;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int t = g == 0   ? tok.t[4 * j]
-                    : g == 1 ? tok.t[4 * j + 1]
-                    : g == 2 ? tok.t[4 * j + 2]
-                             : tok.t[4 * j + 3];
-      const bool in = kt * 32 + xr[j] < rows && t >= 0 && t < a.all && xc[j] >= 0;
-      to_lds(in ? base + t * stride + (int64_t)xc[j] * ES : zeros(), to + (2 * wave + j) * 1024);
-    }
-#pragma unroll
-    for (int j = 0; j < UL; ++j) {
-      const int i = UL * wave + j < RUNS ? UL * wave + j : RUNS - 1;
-      to_lds(kt * 32 + ur[j] < rows ? up[j] + (int64_t)kt * 32 * a.padded * ES : zeros(),
-             to + XB + i * 1024);
+    for (int j = 0; j < 4; ++j) {
+      const int t = lane < 32 ? tok.t[2 * j] : tok.t[2 * j + 1];
+      const bool in = kt * 32 + 8 * wave + 2 * j + (lane >> 5) < rows && t >= 0 && t < a.all &&
+                      xc[j] >= 0;
+      to_lds(in ? base + t * stride + (int64_t)xc[j] * ES : zeros(), to + j * 1024);
     }
   };
-  bk_f32x4 acc[CT][RT] = {};
+  // (rank, row 8 g) of the piece's first step; a piece begins with a tile
+  const char* const up =
+      a.turned + (((int64_t)(kOut ? a.S + s : s) * a.padded + rank + l16) * a.slots + tile * 64 +
+                  8 * g) * ES;
+  const int64_t apart = turned_values(a) * ES;
+  struct Ranks {
+    Frag<DT> f[P];
+  };
+  auto load_u = [&](int kt, Ranks& u) {
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int h = 0; h < XV; ++h) {
+        const char* from = up + p * apart + (int64_t)kt * 32 * ES + 16 * h;
+        u.f[p].v[h] = *reinterpret_cast<const bk_u32x4*>(kt < nk ? from : zeros());
+      }
+  };
+  bk_f32x4 acc[CT] = {};
+  Ranks u[2];
+  load_u(0, u[0]);
+  asm volatile("" ::: "memory");
   Tokens tok = fetch(0);
 #pragma unroll
   for (int i = 0; i < NST - 1; ++i) {
@@ -557,32 +696,25 @@ __device__ __forceinline__ void grads_tile(const DeltaArgs& a, char* lds, int sl
     load(i, tok);
     tok = next;
   }
-  for (int kt = 0; kt < nk; ++kt) {
+  auto step = [&](int kt, const Ranks& now, Ranks& ahead) {
     wait_loads<(NST - 2) * LOADS>();
     barrier();
+    load_u(kt + 1, ahead);
     const Tokens next = fetch(kt + NST);
     load(kt + NST - 1, tok);
     tok = next;
     const char* at = lds + (kt % NST) * STAGE;
-    Frag<DT> xf[CT], uf[P][RT];
 #pragma unroll
-    for (int i = 0; i < CT; ++i)
-      xf[i] = kOut ? read_cols<DT, 256>(at, 0, col + 16 * i, 4, l16, g)
-                   : read_cols<DT, 256>(at, 0, col + 4 * i, 4 * CT, l16, g);
+    for (int i = 0; i < CT; ++i) {
+      const Frag<DT> x = read_cols<DT, RB>(at, 0, col + 16 * i, 4, l16, g);
 #pragma unroll
-    for (int p = 0; p < P; ++p)
-#pragma unroll
-      for (int i = 0; i < RT; ++i)
-        uf[p][i] = kOut ? read_cols<DT, UB>(at + XB + p * UP, 0, rank + 4 * i, 4 * RT, l16, g)
-                        : read_cols<DT, UB>(at + XB + p * UP, 0, rank + 16 * i, 4, l16, g);
-#pragma unroll
-    for (int p = P - 1; p >= 0; --p)  // the smallest first
-#pragma unroll
-      for (int i = 0; i < CT; ++i)
-#pragma unroll
-        for (int j = 0; j < RT; ++j)
-          acc[i][j] = kOut ? product<DT>(uf[p][j], xf[i], acc[i][j])
-                           : product<DT>(xf[i], uf[p][j], acc[i][j]);
+      for (int p = P - 1; p >= 0; --p)  // the smallest first
+        acc[i] = kOut ? product<DT>(now.f[p], x, acc[i]) : product<DT>(x, now.f[p], acc[i]);
+    }
+  };
+  for (int kt = 0; kt < nk; kt += 2) {  // (one step too many is zeros)
+    step(kt, u[0], u[1]);
+    step(kt + 1, u[1], u[0]);
   }
   wait_loads<0>();
 
@@ -593,67 +725,57 @@ __device__ __forceinline__ void grads_tile(const DeltaArgs& a, char* lds, int sl
     *p = add ? *p + v : v;
   };
   if constexpr (!kOut) {
-    // a lane holds columns 4 CT g + 4 i .. + 3 of rank l16 of every rank tile
+    // a lane holds columns 4 g .. 4 g + 3 of every column tile, of rank l16
     float* to = partial < 0 ? a.dA + (int64_t)slot * a.S * a.R * a.K : a.grads + partial * values;
+    const int r = rank + l16;
+    if (r >= a.R) return;
+    to += ((int64_t)s * a.R + r) * a.K;
 #pragma unroll
-    for (int j = 0; j < RT; ++j) {
-      const int r = rank0 + rank + 16 * j + l16;
-      if (r >= a.R) continue;
-#pragma unroll
-      for (int i = 0; i < CT; ++i) {
-        const int c = c0 + col + 4 * CT * g + 4 * i;
-        if (c < a.K) put(to + ((int64_t)s * a.R + r) * a.K + c, acc[i][j]);
-      }
+    for (int i = 0; i < CT; ++i) {
+      const int c = c0 + col + 16 * i + 4 * g;
+      if (c < a.K) put(to + c, acc[i]);
     }
   } else {
-    // ranks 4 RT g + 4 j .. + 3 of column l16 of every column tile
+    // ranks 4 g .. 4 g + 3 of column l16 of every column tile
     float* to = partial < 0 ? a.dB + (int64_t)slot * a.O * a.R
                             : a.grads + partial * values + (int64_t)a.S * a.R * a.K;
+    const int r = rank + 4 * g;
+    if (r >= a.R) return;
 #pragma unroll
     for (int i = 0; i < CT; ++i) {
       const int c = c0 + col + 16 * i + l16;
-      if (c >= len) continue;
-#pragma unroll
-      for (int j = 0; j < RT; ++j) {
-        const int r = rank0 + rank + 4 * RT * g + 4 * j;
-        if (r < a.R) put(to + (int64_t)(a.off[s] + c) * a.R + r, acc[i][j]);
-      }
+      if (c < len) put(to + (int64_t)(a.off[s] + c) * a.R + r, acc[i]);
     }
   }
 }
 
 template <int DT, int NT>
-constexpr int spread_lds() {
-  const int dx = 2 * 128 * 64 * es(DT), grads = 4 * grads_stage<DT, NT>();
-  return dx > grads ? dx : grads;
-}
-template <int DT, int NT>
-__global__ __launch_bounds__(256) void spread_kernel(DeltaArgs a) {
-  __shared__ __attribute__((aligned(16))) char lds[spread_lds<DT, NT>()];
-  constexpr int CB = 256 / es(DT);
-  const int nb = gridDim.x - a.dx_blocks;  // the gradients' workgroups, the long ones, first
-  if ((int)blockIdx.x >= nb) {
-    dx_tile<DT>(a, lds, xcd_item(blockIdx.x - nb, a.dx_blocks));
+__global__ __launch_bounds__(256, 2) void grads_kernel(DeltaArgs a) {
+  __shared__ __attribute__((aligned(16))) char lds[kGradsStages * 32 * kDeltaColumnBytes];
+  constexpr int CB = kDeltaColumnBytes / es(DT);
+  const int jobs = gridDim.x / a.num_parts, part = blockIdx.x / jobs;
+  int job = blockIdx.x - part * jobs, slot, n, first;
+  const int32_t* rec = a.parts + 4 * part;  // (the longest first)
+  const int rows = rec[1], tile = rec[2], partial = rec[3];
+  if (tile < 0 || tile >= a.num_tiles || !take_tile(a, tile, slot, n, first) || slot != rec[0] ||
+      rows < 1 || first > a.rows - rows || (rows + 63) / 64 > a.num_tiles - tile ||
+      partial < -1 || partial >= a.partials)
     return;
-  }
-  const int item = xcd_item(blockIdx.x, nb);
-  const int jobs = nb / a.num_parts, part = item / jobs;
-  int job = item - part * jobs, slot, rows, first;
-  const int32_t* rec = a.parts + 4 * part;
-  if (!take(a, rec, a.rows, slot, rows, first) || rec[3] < -1 || rec[3] >= a.partials) return;
   const int rank0 = job % a.blocks * 16 * NT;
   job /= a.blocks;
-  for (int s = 0; s < a.S; ++s) {
-    const int n = parts_of(a.out[s], CB);
-    if (job < n)
-      return grads_tile<DT, NT, true>(a, lds, slot, rows, first, rec[3], s, rank0, job * CB);
+  int s = 0;
+  for (; s < a.S; ++s) {
+    n = parts_of(a.out[s], CB);
+    if (job < n) break;
     job -= n;
   }
-  const int n = parts_of(a.K, CB);
-  grads_tile<DT, NT, false>(a, lds, slot, rows, first, rec[3], job / n, rank0, job % n * CB);
+  if (s < a.S)
+    return grads_tile<DT, NT, true>(a, lds, slot, rows, first, tile, partial, s, rank0, job * CB);
+  n = parts_of(a.K, CB);
+  grads_tile<DT, NT, false>(a, lds, slot, rows, first, tile, partial, job / n, rank0, job % n * CB);
 }
 
-// ----------------------------------------------------- 4: cut adapters' sums
+// ----------------------------------------------------- 5: cut adapters' sums
 __global__ __launch_bounds__(256) void sums_kernel(DeltaArgs a) {
   const int32_t* rec = a.multi + 4 * blockIdx.y;
   const int slot = rec[0], from = rec[1], n = rec[2];
@@ -670,29 +792,34 @@ __global__ __launch_bounds__(256) void sums_kernel(DeltaArgs a) {
 }
 
 template <int DT, int NT>
-int32_t run(const DeltaArgs& a, hipStream_t st) {
+int32_t run(DeltaArgs& a, hipStream_t st) {
   auto count = [&](int32_t width) {
     int64_t n = (int64_t)a.S * ((a.K + width - 1) / width);
     for (int s = 0; s < a.S; ++s) n += (a.out[s] + width - 1) / width;
     return n * a.blocks;
   };
   if (a.rows) {
-    const int64_t blocks = a.num_tiles * count(a.chunk);
+    const int64_t jobs = count(a.chunk);
+    const int64_t blocks = (a.num_tiles >= 64 ? (a.num_tiles + 7) & ~7 : a.num_tiles) * jobs;
     if (blocks > INT32_MAX) return fail(LORA_E_SHAPE, "too many workgroups");
+    a.jobs = (int32_t)jobs;
     hipLaunchKernelGGL((ranks_kernel<DT, NT>), dim3((uint32_t)blocks), dim3(256), 0, st, a);
     bool cut = a.K > a.chunk;
     for (int s = 0; s < a.S; ++s) cut |= a.out[s] > a.chunk;
-    if (cut) {
-      const int64_t values = (int64_t)a.rows * a.padded;
-      hipLaunchKernelGGL(join_kernel<DT>, dim3((uint32_t)((values + 1023) / 1024), 2 * a.S),
-                         dim3(256), 0, st, a);
-    }
+    if (cut)
+      hipLaunchKernelGGL((join_kernel<DT, NT>), dim3(a.num_tiles, 2 * a.S, a.blocks), dim3(256), 0,
+                         st, a);
   }
-  const int64_t grads = a.dA ? a.num_parts * count(256 / es(DT)) : 0;
-  if (grads + a.dx_blocks > INT32_MAX) return fail(LORA_E_SHAPE, "too many workgroups");
-  if (grads + a.dx_blocks)
-    hipLaunchKernelGGL((spread_kernel<DT, NT>), dim3((uint32_t)(grads + a.dx_blocks)), dim3(256),
-                       0, st, a);
+  if (a.dx) {
+    const int64_t blocks = (int64_t)(a.num_tiles + a.none_tiles) * a.dx_groups;
+    if (blocks > INT32_MAX) return fail(LORA_E_SHAPE, "too many workgroups");
+    hipLaunchKernelGGL(dx_kernel<DT>, dim3((uint32_t)blocks), dim3(256), 0, st, a);
+  }
+  if (a.dA && a.rows) {
+    const int64_t blocks = a.num_parts * count(kDeltaColumnBytes / es(DT));
+    if (blocks > INT32_MAX) return fail(LORA_E_SHAPE, "too many workgroups");
+    hipLaunchKernelGGL((grads_kernel<DT, NT>), dim3((uint32_t)blocks), dim3(256), 0, st, a);
+  }
   if (a.dA && a.num_multi) {
     const int64_t values = (int64_t)a.R * ((int64_t)a.S * a.K + a.O);
     hipLaunchKernelGGL(sums_kernel, dim3((uint32_t)((values + 1023) / 1024), a.num_multi),
@@ -720,6 +847,9 @@ extern "C" int32_t lora_delta_backward(const lora_pool_desc* desc, const void* A
   if (accumulate != 0 && accumulate != 1)
     return fail(LORA_E_ARG, "accumulate must be 0 or 1, got %d", accumulate);
   if (T == 0) return LORA_OK;
+  // (offsets inside 64 ranks' rows of A have 32 bits)
+  if (g.K > kMaxFeatures || g.R > kMaxFeatures)
+    return fail(LORA_E_SHAPE, "in_features and max_lora_rank must be at most %d", kMaxFeatures);
   if (int32_t e = delta_check_plan(g, T, plan)) return e;
   if (!A_pool || !B_pool || !x || !dy || !image)
     return fail(LORA_E_ARG, "A_pool, B_pool, x, dy and image must not be NULL");
@@ -751,7 +881,8 @@ extern "C" int32_t lora_delta_backward(const lora_pool_desc* desc, const void* A
   a.tiles = im + plan->off_tiles;
   a.parts = im + plan->off_parts;
   a.multi = im + plan->off_multi;
-  a.ranks = (char*)ws + l.ranks;
+  a.turned = (char*)ws + l.turned;
+  a.straight = (char*)ws + l.straight;
   a.partial = (float*)((char*)ws + l.partial);
   a.grads = (float*)((char*)ws + l.grads);
   a.num_tiles = plan->tiles;
@@ -759,6 +890,7 @@ extern "C" int32_t lora_delta_backward(const lora_pool_desc* desc, const void* A
   a.num_parts = plan->parts;
   a.num_multi = plan->multi;
   a.rows = plan->rows;
+  a.slots = (int64_t)plan->tiles * kDeltaTileRows;
   a.partials = plan->partials;
   a.all = T;
   a.max_loras = g.max_loras;
@@ -771,10 +903,8 @@ extern "C" int32_t lora_delta_backward(const lora_pool_desc* desc, const void* A
   a.chunk = plan->chunk;
   a.accumulate = accumulate;
   for (int s = 0; s < g.S; ++s) a.out[s] = g.out[s], a.off[s] = g.off[s];
-  a.dx_groups = (g.K + kDeltaColumns - 1) / kDeltaColumns;
-  const int64_t tiles = (int64_t)plan->tiles + plan->none_tiles;
-  if (dx && tiles * a.dx_groups > INT32_MAX / 2) return fail(LORA_E_SHAPE, "too many workgroups");
-  a.dx_blocks = dx ? (int32_t)(tiles * a.dx_groups) : 0;
+  const int32_t cb = 256 / (int32_t)elem_bytes(g.dtype);
+  a.dx_groups = (g.K + cb - 1) / cb;
   const hipStream_t st = (hipStream_t)stream;
   if (g.dtype == LORA_BF16)
     return r.tiles == 1   ? run<LORA_BF16, 1>(a, st)

@@ -1,6 +1,6 @@
 // Host plan of the gradients of the adapters' delta: rows sorted by adapter, row
 // tiles, and the pieces of each adapter's rows whose gradients one workgroup sums.
-#include <cstdlib>
+#include <algorithm>
 #include <cstring>
 
 #include "lora_delta.h"
@@ -39,13 +39,13 @@ int64_t shrinks(const Geo& g, int64_t chunk) {
 }
 
 // Columns of a part of the shrink's reductions: the fewest parts that give every
-// compute unit its two workgroups.
+// compute unit a workgroup.
 int64_t shrink_chunk(const Geo& g, int64_t tiles) {
   int64_t len = g.K;
   for (int s = 0; s < g.S; ++s) len = g.out[s] > len ? g.out[s] : len;
   int64_t chunk = align_up(len, 64);
   for (int parts = 2; parts <= kDeltaMaxSplits; ++parts) {
-    if (tiles * delta_ranks(g.R).blocks * shrinks(g, chunk) >= kDeltaAim) break;
+    if (tiles * delta_ranks(g.R).blocks * shrinks(g, chunk) >= kDeltaShrinks) break;
     const int64_t c = align_up((len + parts - 1) / parts, 64);
     if (c < 256) break;
     chunk = c;
@@ -74,14 +74,20 @@ Words capacity(const Geo& g, int32_t T) {
 
 DeltaLayout delta_layout(const Geo& g, int32_t T) {
   const DeltaRanks r = delta_ranks(g.R);
-  const int64_t sides = 2 * g.S, values = sides * (int64_t)T * r.padded;
+  const int64_t sides = 2 * g.S, tile = kDeltaTileRows, e = elem_bytes(g.dtype);
+  // Every adapter adds at most one tile that is not full, and no tile is empty.
+  const int64_t runs = T < g.max_loras ? T : g.max_loras;
+  const int64_t tiles = T < T / tile + runs ? T : T / tile + runs;
   // Reductions are cut only while the unsplit workgroups are fewer than wanted.
-  const int64_t few = kDeltaAim * kDeltaTileRows / (sides * r.blocks) + 1;
+  const int64_t few = kDeltaShrinks / (sides * r.blocks) + 1;
+  const int64_t planes = g.dtype == LORA_BF16 ? 3 : 1, two = g.dtype == LORA_BF16 ? 2 : 1;
   DeltaLayout l;
-  l.ranks = 0;
-  l.partial = align_up(values * (g.dtype == LORA_BF16 ? 6 : 4), 256);
-  l.grads = l.partial +
-            align_up((int64_t)kDeltaMaxSplits * sides * (T < few ? T : few) * r.padded * 4, 256);
+  l.turned = 0;
+  l.straight = l.turned + align_up(planes * sides * tiles * tile * r.padded * e, 256);
+  l.partial = l.straight + align_up(two * g.S * tiles * tile * r.padded * e, 256);
+  l.grads = l.partial + align_up((int64_t)kDeltaMaxSplits * sides * (tiles < few ? tiles : few) *
+                                     tile * r.padded * 4,
+                                 256);
   l.total = l.grads + align_up(most_partials(g, T) * delta_grad_values(g) * 4, 256);
   return l;
 }
@@ -185,16 +191,21 @@ extern "C" int32_t lora_delta_backward_plan(const lora_pool_desc* desc, int32_t 
   p.off_tiles = w.tiles;
   p.off_parts = put - at;
   const int64_t most = piece_rows(g, rows);
-  for (int32_t a = 0; a < g.max_loras; ++a) {
-    const int32_t from = a ? next[a - 1] : 0, n = next[a] - from;
+  for (int32_t a = 0, tile = 0; a < g.max_loras; ++a) {
+    const int32_t n = next[a] - (a ? next[a - 1] : 0);
     if (!n) continue;
-    // equal pieces, whole steps of 64 rows
-    const int64_t k = (n + most - 1) / most, each = align_up((n + k - 1) / k, 64);
+    // equal pieces, whole steps of 64 rows; a cut costs about what 256 rows do
+    const int64_t k = n > most + 256 ? (n + most - 1) / most : 1;
+    const int64_t each = align_up((n + k - 1) / k, 64);
     for (int64_t r = 0; r < n; r += each, ++p.parts)
-      record(a, (int32_t)(n - r < each ? n - r : each), (int32_t)(from + r),
+      record(a, (int32_t)(n - r < each ? n - r : each), tile + (int32_t)(r / kDeltaTileRows),
              k > 1 ? p.partials++ : -1);
+    tile += (n + kDeltaTileRows - 1) / kDeltaTileRows;
   }
   p.off_multi = put - at;
+  struct Record {
+    int32_t w[4];
+  };
   for (int32_t i = 0, q = 0; i < p.parts; ++i) {
     const int32_t* part = at + p.off_parts + 4 * i;
     if (part[3] < 0) continue;
@@ -205,6 +216,11 @@ extern "C" int32_t lora_delta_backward_plan(const lora_pool_desc* desc, int32_t 
     ++put[-2];
     ++q;
   }
+  // the longest pieces first (ties in order)
+  Record* const parts = reinterpret_cast<Record*>(at + p.off_parts);
+  std::sort(parts, parts + p.parts, [](const Record& a, const Record& b) {
+    return a.w[1] != b.w[1] ? a.w[1] > b.w[1] : a.w[2] < b.w[2];
+  });
   p.chunk = (int32_t)shrink_chunk(g, p.tiles);
   p.image_bytes = (put - at) * 4;
   *plan = p;

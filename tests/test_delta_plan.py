@@ -30,13 +30,15 @@ def check(desc, ids):
     assert seen == list(range(T))
     parts = image[p.off_parts:p.off_parts + 4 * p.parts].reshape(-1, 4)
     seen, partials = [], []
-    for slot, rows, first, to in parts:
+    for slot, rows, tile, to in parts:
+        first = tiles[tile][2]
         assert rows >= 1 and (ids[perm[first:first + rows]] == slot).all()
         whole = rows == (ids == slot).sum()
         assert (to == -1) == whole
         partials += [] if whole else [(to, slot)]
         seen += range(first, first + rows)
-    assert seen == list(range(p.rows))
+    assert sorted(seen) == list(range(p.rows)) and (np.diff(parts[:, 1]) <= 0).all()
+    partials.sort()
     assert [q for q, _ in partials] == list(range(p.partials))
     multi = image[p.off_multi:p.off_multi + 4 * p.multi].reshape(-1, 4)
     flat = [(q, slot) for slot, at, n, _ in multi for q in range(at, at + n)]
@@ -63,7 +65,7 @@ def test_pieces_and_parts():
     small = L.make_desc("bf16", 4, 16, 256, [256])
     assert check(small, np.zeros(9000)).partials > 1
     assert check(small, np.zeros(100)).partials == 0
-    wide = L.make_desc("bf16", 4, 64, 16384, [65536])
+    wide = L.make_desc("bf16", 4, 64, 16384, [131072])
     assert check(wide, np.zeros(9000)).partials == 0
     p = check(L.make_desc("bf16", 4, 16, 4096, [4096]), np.zeros(64))
     assert 256 <= p.chunk < 4096
