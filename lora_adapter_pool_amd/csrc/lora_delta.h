@@ -9,7 +9,7 @@ namespace lora {
 constexpr int kDeltaTileRows = 64;      // rows of a shrink's or a dx's workgroup
 constexpr int kDeltaColumnBytes = 512;  // columns of a gradient's workgroup, in stored bytes
 constexpr int64_t kDeltaAim = 512;      // workgroups of the gradients, two a compute unit
-constexpr int64_t kDeltaShrinks = 256;  // workgroups of the ranks, one a compute unit
+constexpr int64_t kDeltaShrinks = 1024;  // workgroups of the ranks, four a compute unit
 constexpr int kDeltaMaxSplits = 8;
 
 // Rank tiles of 16 in a rank block, rank blocks, and the ranks they pad to.

@@ -33,7 +33,7 @@ using gemm::wait_all_lds;
 
 constexpr int kMaxFeatures = 1 << 22;
 constexpr int kPlanes = 3;       // bf16 pieces of an fp32 value
-constexpr int kGradsStages = 4;  // of 32 rows
+constexpr int kGradsStages = 3;  // of 32 rows
 
 struct DeltaArgs {
   const char* A;
@@ -197,50 +197,44 @@ __device__ __forceinline__ int64_t straight_values(const DeltaArgs& a) {
   return (int64_t)a.S * a.padded * a.slots;
 }
 
-// Stores N values (4, or 8 and more in eights) as they are kept, pieces `apart` values
-// from each other.
-template <int DT, int N>
+// Stores four values as they are kept, pieces `apart` values from each other.
+template <int DT>
 __device__ __forceinline__ void keep(char* base, int64_t at, int64_t apart, int planes,
-                                     const float (&v)[N]) {
+                                     const float (&v)[4]) {
   if constexpr (DT == LORA_F32) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4)
-      *reinterpret_cast<bk_f32x4*>(base + (at + i) * 4) =
-          bk_f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+    *reinterpret_cast<bk_f32x4*>(base + at * 4) = bk_f32x4{v[0], v[1], v[2], v[3]};
   } else {
+    bk_u32x2 p[kPlanes];
+    pieces_of(v, p);
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const float w[4] = {v[i], v[i + 1], v[i + 2], v[i + 3]};
-      bk_u32x2 p[kPlanes];
-      pieces_of(w, p);
-#pragma unroll
-      for (int k = 0; k < kPlanes; ++k)
-        if (k < planes) *reinterpret_cast<bk_u32x2*>(base + (k * apart + at + i) * 2) = p[k];
-    }
+    for (int k = 0; k < kPlanes; ++k)
+      if (k < planes) *reinterpret_cast<bk_u32x2*>(base + (k * apart + at) * 2) = p[k];
   }
 }
 
-// A tile's values of one rank block, from LDS ([64][LD], the sums already in it).
-template <int DT, int NT>
+// A tile's values of RB ranks, from LDS (64 rows of LD, the sums already in it).  16 lanes
+// take the 64 rows of a rank: whole cache lines of `turned`.
+template <int DT, int RB>
 __device__ __forceinline__ void finish_ranks(const DeltaArgs& a, const float* sums, int q, int tile,
                                              int rank0) {
-  constexpr int RB = 16 * NT, LD = RB + 4, N = RB / 4;  // N rows a thread
-  const int tid = threadIdx.x;
-  {
-    const int r = tid % RB, row = tid / RB * N;
-    float v[N];
+  constexpr int LD = RB + 4;
+  const int tid = threadIdx.x, row = tid % 16 * 4;
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = sums[(row + i) * LD + r];
-    keep<DT, N>(a.turned, ((int64_t)q * a.padded + rank0 + r) * a.slots + tile * 64 + row,
+  for (int i = 0; i < RB / 16; ++i) {
+    const int r = 16 * i + tid / 16;
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = sums[(row + j) * LD + r];
+    keep<DT>(a.turned, ((int64_t)q * a.padded + rank0 + r) * a.slots + tile * 64 + row,
                 turned_values(a), kPlanes, v);
   }
   if (q >= a.S || !a.dx) return;
 #pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int o = (i * 256 + tid) * 4, row = o / RB, r = o % RB;
-    const bk_f32x4 w = *reinterpret_cast<const bk_f32x4*>(sums + row * LD + r);
+  for (int i = 0; i < RB / 16; ++i) {
+    const int o = (i * 256 + tid) * 4;
+    const bk_f32x4 w = *reinterpret_cast<const bk_f32x4*>(sums + o / RB * LD + o % RB);
     const float v[4] = {w[0], w[1], w[2], w[3]};
-    keep<DT, 4>(a.straight, ((int64_t)q * a.slots + tile * 64 + row) * a.padded + rank0 + r,
+    keep<DT>(a.straight, ((int64_t)q * a.slots + tile * 64 + o / RB) * a.padded + rank0 + o % RB,
                 straight_values(a), 2, v);
   }
 }
@@ -258,11 +252,8 @@ constexpr int ranks_lds() {
   const int ring = 4 * 2 * 16 * NT * 128, sums = 4 * 64 * (16 * NT + 4) * 4;
   return ring > sums ? ring : sums;
 }
-template <int N>
-struct Count {
-  static constexpr int value = N;
-};
-template <int DT, int NT, bool kOut>  // kOut: u, from dy and B; else v, from x and A
+// kOut: u, from dy and B; else v, from x and A.  NR: row tiles that are multiplied.
+template <int DT, int NT, bool kOut, int NR>
 __device__ __forceinline__ void ranks_tile(const DeltaArgs& a, char* lds, int tile, int slot,
                                            int rows, int first, int s, int rank0, int part) {
   constexpr int ES = es(DT), KS = 128 / ES;   // reduction indexes a step
@@ -274,15 +265,14 @@ __device__ __forceinline__ void ranks_tile(const DeltaArgs& a, char* lds, int ti
   const int l16 = lane & 15, g = lane >> 4;
   const int len = kOut ? a.out[s] : a.K;
   const int lo = part * a.chunk, hi = lo + a.chunk < len ? lo + a.chunk : len;
-  const int all = (hi - lo + KS - 1) / KS;          // steps of the workgroup
-  const int nk = (all - wave + 3) / 4;              // of this wave (it may be 0)
-  const int nr = (rows + 15) / 16;                  // row tiles that hold rows
+  const int whole_steps = (hi - lo) / KS;           // of the workgroup
+  const int nk = (whole_steps - wave + 3) / 4;      // of this wave (it may be 0)
   char* const ring = lds + wave * 2 * SLOT;
 
   // Rows past the last one read row 0 of the batch: their sums are not kept.
-  const char* xp[4];
+  const char* xp[NR];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < NR; ++i) {
     const int r = 16 * i + l16;
     int t = r < rows ? a.perm[first + r] : 0;
     if (t < 0 || t >= a.all) t = 0;
@@ -316,12 +306,14 @@ __device__ __forceinline__ void ranks_tile(const DeltaArgs& a, char* lds, int ti
     off[j] = offset(k, r);
   }
   struct Rows {
-    Frag<DT> f[4][QS];
+    Frag<DT> f[NR][QS];
   };
-  auto load_w = [&](int i) {
-    char* to = ring + (i & 1) * SLOT;
+  bk_f32x4 acc[NR][NT] = {};
+  // Step i of this wave into ring slot i & 1; left: reduction indexes it holds.
+  auto load_w = [&](int i, int slot, int left) {
+    char* to = ring + slot * SLOT;
     const char* from = wbase + i * wstep;
-    const int left = hi - lo - (wave + 4 * i) * KS, ranks = a.R - rank0;
+    const int ranks = a.R - rank0;
     if (left >= KS && ranks >= 16 * NT) {
 #pragma unroll
       for (int j = 0; j < WL; ++j)
@@ -338,42 +330,8 @@ __device__ __forceinline__ void ranks_tile(const DeltaArgs& a, char* lds, int ti
       }
     }
   };
-  auto load_x = [&](int i, Rows& x) {
-    const int left = hi - lo - (wave + 4 * i) * KS;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      if (t >= nr) break;
-#pragma unroll
-      for (int q = 0; q < QS; ++q)
-#pragma unroll
-        for (int h = 0; h < XV; ++h) {
-          const bk_u32x4* p =
-              reinterpret_cast<const bk_u32x4*>(xp[t] + (int64_t)i * 512 + q * 32 * ES) + h;
-          // (a reduction's last step may end inside: zeros, as for the weights)
-          if (left >= KS)
-            x.f[t][q].v[h] = *p;
-          else
-            x.f[t][q].v[h] = 32 * q + 8 * g + h * 4 < left ? *p : bk_u32x4{0, 0, 0, 0};
-        }
-    }
-  };
-  bk_f32x4 acc[4][NT] = {};
-  // What follows step i's loads: those of step i + 1, and none behind the last.
-  auto arrived = [&](bool last) {
-    if (last)
-      wait_loads<0>();
-    else if (nr == 1)
-      wait_loads<WL + QS * XV>();
-    else if (nr == 2)
-      wait_loads<WL + 2 * QS * XV>();
-    else if (nr == 3)
-      wait_loads<WL + 3 * QS * XV>();
-    else
-      wait_loads<WL + 4 * QS * XV>();
-    asm volatile("" ::: "memory");
-  };
-  auto multiply = [&](int i, const Rows& x) {
-    const char* at = ring + (i & 1) * SLOT;
+  auto multiply = [&](int slot, const Rows& x) {
+    const char* at = ring + slot * SLOT;
 #pragma unroll
     for (int q = 0; q < QS; ++q) {
       Frag<DT> w[NT];
@@ -382,34 +340,67 @@ __device__ __forceinline__ void ranks_tile(const DeltaArgs& a, char* lds, int ti
         w[j] = kOut ? read_cols<DT, WB>(at, 32 * q, 16 * j, 4, l16, g)
                     : read_rows<DT>(at, 16 * j + l16, g, q);
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        if (t >= nr) break;
+      for (int t = 0; t < NR; ++t)
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[t][j] = product<DT>(w[j], x.f[t][q], acc[t][j]);
-      }
     }
   };
-  auto load = [&](int i, Rows& x) {
+  // Whole steps, two ahead.  Every step makes the same number of loads (past the last
+  // one the last again) with no branch around any, so that a count of them waits for
+  // the step's own.
+  auto load = [&](int i, int slot, Rows& x) {
+    const int k = i < nk ? i : nk - 1;
     // the slot's reads are done before its place is filled again
     __builtin_amdgcn_s_waitcnt(wait_all_lds(63));
     asm volatile("" ::: "memory");
-    load_w(i);
+    load_w(k, slot, KS);
     asm volatile("" ::: "memory");
-    load_x(i, x);
+#pragma unroll
+    for (int t = 0; t < NR; ++t)
+#pragma unroll
+      for (int q = 0; q < QS; ++q)
+#pragma unroll
+        for (int h = 0; h < XV; ++h)
+          x.f[t][q].v[h] =
+              reinterpret_cast<const bk_u32x4*>(xp[t] + (int64_t)k * 512 + q * 32 * ES)[h];
     asm volatile("" ::: "memory");
   };
-  Rows x[2];
-  if (nk > 0) load(0, x[0]);
-  if (nk > 1) load(1, x[1]);
-  for (int i = 0; i < nk; i += 2) {
-    arrived(i + 1 >= nk);
-    multiply(i, x[0]);
-    if (i + 2 < nk) load(i + 2, x[0]);
-    if (i + 1 < nk) {
-      arrived(i + 2 >= nk);
-      multiply(i + 1, x[1]);
-      if (i + 3 < nk) load(i + 3, x[1]);
+  constexpr int LOADS = WL + NR * QS * XV;
+  if (nk > 0) {
+    Rows x[2];
+    load(0, 0, x[0]);
+    load(1, 1, x[1]);
+    auto step = [&](int i, int slot, Rows& now) {
+      wait_loads<LOADS>();
+      asm volatile("" ::: "memory");
+      multiply(slot, now);
+      load(i + 2, slot, now);
+      return i + 1 < nk;
+    };
+    for (int i = 0;; i += 2) {
+      if (!step(i, 0, x[0])) break;
+      if (!step(i + 1, 1, x[1])) break;
     }
+    wait_loads<0>();
+  }
+  // The reduction's end, where it is no whole step: zeros past it.
+  const int left = hi - lo - whole_steps * KS;
+  if (left > 0 && wave == (whole_steps & 3)) {
+    Rows x;
+    load_w(nk, 0, left);
+#pragma unroll
+    for (int t = 0; t < NR; ++t)
+#pragma unroll
+      for (int q = 0; q < QS; ++q)
+#pragma unroll
+        for (int h = 0; h < XV; ++h) {
+          const char* p = xp[t] + (int64_t)nk * 512 + q * 32 * ES + 16 * h;
+          x.f[t][q].v[h] =
+              *reinterpret_cast<const bk_u32x4*>(32 * q + 8 * g + 4 * h < left ? p : zeros());
+        }
+    wait_loads<0>();
+    asm volatile("" ::: "memory");
+    multiply(0, x);
   }
   // a lane holds ranks 4 g .. 4 g + 3 of every rank tile, of row l16 of every row tile
   constexpr int RB = 16 * NT, LD = RB + 4;
@@ -421,7 +412,7 @@ __device__ __forceinline__ void ranks_tile(const DeltaArgs& a, char* lds, int ti
 #pragma unroll
     for (int j = 0; j < NT; ++j)
       *reinterpret_cast<bk_f32x4*>(sums + (wave * 64 + 16 * t + l16) * LD + 16 * j + 4 * g) =
-          in ? acc[t][j] : bk_f32x4{0.f, 0.f, 0.f, 0.f};
+          in && t < NR ? acc[t < NR ? t : 0][j] : bk_f32x4{0.f, 0.f, 0.f, 0.f};
   }
   __syncthreads();
   const int q = kOut ? s : a.S + s;
@@ -442,7 +433,7 @@ __device__ __forceinline__ void ranks_tile(const DeltaArgs& a, char* lds, int ti
   }
   if (!whole) return;
   __syncthreads();
-  finish_ranks<DT, NT>(a, sums, q, tile, rank0);
+  finish_ranks<DT, 16 * NT>(a, sums, q, tile, rank0);
 }
 
 __device__ __forceinline__ int parts_of(int len, int chunk) { return (len + chunk - 1) / chunk; }
@@ -484,30 +475,41 @@ __global__ __launch_bounds__(256, 2) void ranks_kernel(DeltaArgs a) {
     if (job < n) break;
     job -= n;
   }
-  if (s < a.S)
-    return ranks_tile<DT, NT, true>(a, lds, tile, slot, rows, first, s, rank0, job);
-  const int n = parts_of(a.K, a.chunk);
-  ranks_tile<DT, NT, false>(a, lds, tile, slot, rows, first, job / n, rank0, job % n);
+  const bool out = s < a.S;
+  if (!out) {
+    const int n = parts_of(a.K, a.chunk);
+    s = job / n;
+    job %= n;
+  }
+  if (rows <= 16) {
+    if (out)
+      ranks_tile<DT, NT, true, 1>(a, lds, tile, slot, rows, first, s, rank0, job);
+    else
+      ranks_tile<DT, NT, false, 1>(a, lds, tile, slot, rows, first, s, rank0, job);
+  } else {
+    if (out)
+      ranks_tile<DT, NT, true, 4>(a, lds, tile, slot, rows, first, s, rank0, job);
+    else
+      ranks_tile<DT, NT, false, 4>(a, lds, tile, slot, rows, first, s, rank0, job);
+  }
 }
 
 // ------------------------------------------------------- 2: parts of the sums
-template <int DT, int NT>
+template <int DT>
 __global__ __launch_bounds__(256) void join_kernel(DeltaArgs a) {
-  constexpr int RB = 16 * NT, LD = RB + 4;
+  constexpr int LD = 16 + 4;
   __shared__ __attribute__((aligned(16))) float sums[64 * LD];
-  const int tile = blockIdx.x, q = blockIdx.y, rank0 = blockIdx.z * RB;
+  const int tile = blockIdx.x, q = blockIdx.y, rank0 = blockIdx.z * 16;
   const int n = parts_of(q < a.S ? a.out[q] : a.K, a.chunk);
   if (n == 1) return;
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int o = (i * 256 + (int)threadIdx.x) * 4, row = o / RB, r = o % RB;
-    const float* from = a.partial + (((int64_t)q * a.slots + tile * 64 + row) * a.padded + rank0 + r);
-    bk_f32x4 v = *reinterpret_cast<const bk_f32x4*>(from);
-    for (int p = 1; p < n; ++p) v += *reinterpret_cast<const bk_f32x4*>(from + p * turned_values(a));
-    *reinterpret_cast<bk_f32x4*>(sums + row * LD + r) = v;
-  }
+  const int row = threadIdx.x / 4, r = threadIdx.x % 4 * 4;
+  const float* from = a.partial + (((int64_t)q * a.slots + tile * 64 + row) * a.padded + rank0 + r);
+  bk_f32x4 v = *reinterpret_cast<const bk_f32x4*>(from);
+#pragma unroll 4
+  for (int p = 1; p < n; ++p) v += *reinterpret_cast<const bk_f32x4*>(from + p * turned_values(a));
+  *reinterpret_cast<bk_f32x4*>(sums + row * LD + r) = v;
   __syncthreads();
-  finish_ranks<DT, NT>(a, sums, q, tile, rank0);
+  finish_ranks<DT, 16>(a, sums, q, tile, rank0);
 }
 
 // ------------------------------------------------------------- 3: the input's
@@ -517,7 +519,7 @@ __global__ __launch_bounds__(256) void join_kernel(DeltaArgs a) {
 // straight to registers.  The columns are dealt to the output's index so that a
 // lane's are neighbours in memory.
 template <int DT>
-__global__ __launch_bounds__(256) void dx_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(256, 4) void dx_kernel(DeltaArgs a) {
   constexpr int ES = es(DT), RB = 256, CB = RB / ES, RANKS = 128;
   constexpr int P = DT == LORA_BF16 ? 2 : 1, XV = sizeof(Frag<DT>) / 16;
   constexpr int CT = CB / 16, V = 16 / ES;  // column tiles; columns of a 16-byte piece
@@ -542,18 +544,21 @@ __global__ __launch_bounds__(256) void dx_kernel(DeltaArgs a) {
   }
   const int row = 16 * wave + l16;
   int t = row < rows ? a.perm[first + row] : -1;
-  if (t >= a.all) t = -1;
-  // a lane's pieces: columns c0 + i 4 V + g V ..
+  // a lane's pieces of dx_in: columns c0 + i 4 V + g V ..
   bk_u32x4 base[NV];
+  auto fetch = [&]() {
+    if (t >= a.all) t = -1;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = c0 + i * 4 * V + g * V;
-    base[i] = bk_u32x4{0, 0, 0, 0};
-    if (a.dx_in && t >= 0 && c < a.K)
-      base[i] = *reinterpret_cast<const bk_u32x4*>(a.dx_in + ((int64_t)t * a.K + c) * ES);
-  }
+    for (int i = 0; i < NV; ++i) {
+      const int c = c0 + i * 4 * V + g * V;
+      base[i] = bk_u32x4{0, 0, 0, 0};
+      if (a.dx_in && t >= 0 && c < a.K)
+        base[i] = *reinterpret_cast<const bk_u32x4*>(a.dx_in + ((int64_t)t * a.K + c) * ES);
+    }
+  };
   bk_f32x4 acc[CT] = {};
   const int ranks = none ? 0 : a.S * a.padded;  // of the reduction
+  if (none) fetch();
   for (int r0 = 0; r0 < ranks; r0 += RANKS) {
     const int n = ranks - r0 < RANKS ? ranks - r0 : RANKS;
     // rank index i of the reduction is rank i % padded of slice i / padded
@@ -578,6 +583,7 @@ __global__ __launch_bounds__(256) void dx_kernel(DeltaArgs a) {
                                a.straight + (p * straight_values(a) + at) * ES)[h]
                          : bk_u32x4{0, 0, 0, 0};
     }
+    if (r0 == 0) fetch();
     wait_loads<0>();
     barrier();
 #pragma unroll
@@ -626,7 +632,8 @@ __device__ __forceinline__ void grads_tile(const DeltaArgs& a, char* lds, int sl
                                            int first, int tile, int partial, int s, int rank0,
                                            int c0) {
   constexpr int ES = es(DT), P = DT == LORA_BF16 ? kPlanes : 1, XV = sizeof(Frag<DT>) / 16;
-  constexpr int RB = kDeltaColumnBytes, STAGE = 32 * RB, NST = kGradsStages, LOADS = 4;
+  constexpr int RB = kDeltaColumnBytes, STAGE = 32 * RB, NST = kGradsStages;
+  constexpr int RL = 1024 / RB, LOADS = 8 / RL;  // rows of a load, a wave's loads of a stage
   constexpr int CT = RB / ES / 16 / (4 / NT);  // a wave's column tiles
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -637,11 +644,12 @@ __device__ __forceinline__ void grads_tile(const DeltaArgs& a, char* lds, int sl
 
   const char* base = kOut ? a.dy : a.x;
   const int64_t stride = (int64_t)(kOut ? a.O : a.K) * ES;
-  int xc[4];  // column in memory of a lane's piece, or -1: rows 8 wave + 2 j and the next
+  const int lr = lane / (RB / 16);  // a lane's row of a load
+  int xc[LOADS];  // column in memory of a lane's piece, or -1
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int k = 8 * wave + 2 * j + (lane >> 5);
-    const int c = column_place<DT, RB>(lane % 32 * 16, k) / ES;
+  for (int j = 0; j < LOADS; ++j) {
+    const int k = 8 * wave + RL * j + lr;
+    const int c = column_place<DT, RB>(lane % (RB / 16) * 16, k) / ES;
     xc[j] = c0 + c < len ? (kOut ? a.off[s] : 0) + c0 + c : -1;
   }
   // Tokens of the wave's eight rows of a stage, by scalar loads: these are not
@@ -659,12 +667,13 @@ __device__ __forceinline__ void grads_tile(const DeltaArgs& a, char* lds, int sl
     return k;
   };
   auto load = [&](int kt, const Tokens& tok) {
-    char* to = lds + (kt % NST) * STAGE + wave * 4096;
+    char* to = lds + (kt % NST) * STAGE + wave * 8 * RB;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int t = lane < 32 ? tok.t[2 * j] : tok.t[2 * j + 1];
-      const bool in = kt * 32 + 8 * wave + 2 * j + (lane >> 5) < rows && t >= 0 && t < a.all &&
-                      xc[j] >= 0;
+    for (int j = 0; j < LOADS; ++j) {
+      int t = tok.t[RL * j];
+#pragma unroll
+      for (int r = 1; r < RL; ++r) t = lr == r ? tok.t[RL * j + r] : t;
+      const bool in = kt * 32 + 8 * wave + RL * j + lr < rows && t >= 0 && t < a.all && xc[j] >= 0;
       to_lds(in ? base + t * stride + (int64_t)xc[j] * ES : zeros(), to + j * 1024);
     }
   };
@@ -686,8 +695,10 @@ __device__ __forceinline__ void grads_tile(const DeltaArgs& a, char* lds, int sl
       }
   };
   bk_f32x4 acc[CT] = {};
-  Ranks u[2];
-  load_u(0, u[0]);
+  constexpr int AHEAD = 3;  // steps that u or v is fetched ahead
+  Ranks u[AHEAD + 1];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) load_u(i, u[i]);
   asm volatile("" ::: "memory");
   Tokens tok = fetch(0);
 #pragma unroll
@@ -699,7 +710,7 @@ __device__ __forceinline__ void grads_tile(const DeltaArgs& a, char* lds, int sl
   auto step = [&](int kt, const Ranks& now, Ranks& ahead) {
     wait_loads<(NST - 2) * LOADS>();
     barrier();
-    load_u(kt + 1, ahead);
+    load_u(kt + AHEAD, ahead);
     const Tokens next = fetch(kt + NST);
     load(kt + NST - 1, tok);
     tok = next;
@@ -712,9 +723,16 @@ __device__ __forceinline__ void grads_tile(const DeltaArgs& a, char* lds, int sl
         acc[i] = kOut ? product<DT>(now.f[p], x, acc[i]) : product<DT>(x, now.f[p], acc[i]);
     }
   };
-  for (int kt = 0; kt < nk; kt += 2) {  // (one step too many is zeros)
-    step(kt, u[0], u[1]);
-    step(kt + 1, u[1], u[0]);
+  wait_loads<(NST - 1) * LOADS>();
+  for (int kt = 0;;) {
+    step(kt, u[0], u[3]);
+    if (++kt >= nk) break;
+    step(kt, u[1], u[0]);
+    if (++kt >= nk) break;
+    step(kt, u[2], u[1]);
+    if (++kt >= nk) break;
+    step(kt, u[3], u[2]);
+    if (++kt >= nk) break;
   }
   wait_loads<0>();
 
@@ -807,7 +825,7 @@ int32_t run(DeltaArgs& a, hipStream_t st) {
     bool cut = a.K > a.chunk;
     for (int s = 0; s < a.S; ++s) cut |= a.out[s] > a.chunk;
     if (cut)
-      hipLaunchKernelGGL((join_kernel<DT, NT>), dim3(a.num_tiles, 2 * a.S, a.blocks), dim3(256), 0,
+      hipLaunchKernelGGL(join_kernel<DT>, dim3(a.num_tiles, 2 * a.S, a.padded / 16), dim3(256), 0,
                          st, a);
   }
   if (a.dx) {

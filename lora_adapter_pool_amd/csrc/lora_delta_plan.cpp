@@ -39,7 +39,7 @@ int64_t shrinks(const Geo& g, int64_t chunk) {
 }
 
 // Columns of a part of the shrink's reductions: the fewest parts that give every
-// compute unit a workgroup.
+// compute unit four workgroups.
 int64_t shrink_chunk(const Geo& g, int64_t tiles) {
   int64_t len = g.K;
   for (int s = 0; s < g.S; ++s) len = g.out[s] > len ? g.out[s] : len;
