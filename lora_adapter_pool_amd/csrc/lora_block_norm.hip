@@ -55,7 +55,13 @@ struct JoinArgs {
 // numbers below 2^-128, or near the largest, or not with all its bits.
 struct Factor {
   float part, rest;
-  __device__ __forceinline__ float of(float x) const { return x * part * rest; }
+  __device__ __forceinline__ void times(float (&x)[8]) const {
+    if (part != 1.f)  // (the same for the whole row)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] *= part;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] *= rest;
+  }
 };
 __device__ __forceinline__ Factor factor_of(double root) {
   if (root > 0x1p120) return {0x1p64f, (float)(root * 0x1p-64)};
@@ -63,25 +69,50 @@ __device__ __forceinline__ Factor factor_of(double root) {
   return {1.f, (float)root};
 }
 
-// Sums over the workgroup, the same in every thread.  `room` is not read again
-// before another barrier has passed.
+// A value of another lane of the same 16, by a lane move (no trip through LDS); all
+// lanes of the wave have to be active.
+template <int kMove>
+__device__ __forceinline__ double moved(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_mov_dpp((int)(uint32_t)b, kMove, 15, 15, true);
+  const uint32_t hi = __builtin_amdgcn_mov_dpp((int)(uint32_t)(b >> 32), kMove, 15, 15, true);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
+
+// Sums over 16 lanes, the same in each (a tree whose branches commute).
+template <int N>
+__device__ __forceinline__ void sum_over_16(double (&v)[N]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] += moved<kXor1>(v[k]);
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] += moved<kXor2>(v[k]);
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] += moved<kHalfMirror>(v[k]);
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] += moved<kMirror>(v[k]);
+}
+// Sums over the workgroup, the same in every thread.  `room` (a place for each of up to
+// 16 waves) is not read again before another barrier has passed.
 template <int N>
 __device__ __forceinline__ void sum_over(double (&v)[N], double (*room)[N]) {
   const int tid = threadIdx.x, waves = blockDim.x >> 6;
+  sum_over_16(v);
 #pragma unroll
-  for (int k = 0; k < N; ++k)
+  for (int d = 16; d < 64; d *= 2)
 #pragma unroll
-    for (int d = 32; d; d >>= 1) v[k] += __shfl_xor(v[k], d);
+    for (int k = 0; k < N; ++k) v[k] += __shfl_xor(v[k], d);
   if (waves == 1) return;
   if ((tid & 63) == 0)
 #pragma unroll
     for (int k = 0; k < N; ++k) room[tid >> 6][k] = v[k];
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < N; ++k) v[k] = 0.0;
-  for (int i = 0; i < waves; ++i)
-#pragma unroll
-    for (int k = 0; k < N; ++k) v[k] += room[i][k];
+  for (int k = 0; k < N; ++k) {
+    const double w = room[tid & 15][k];  // (past the last wave: not written, and not taken)
+    v[k] = (tid & 15) < waves ? w : 0.0;
+  }
+  sum_over_16(v);
 }
 
 __device__ __forceinline__ double square_plus(float x, double s) {
@@ -90,7 +121,7 @@ __device__ __forceinline__ double square_plus(float x, double s) {
 
 template <int DT, int NP>
 __global__ __launch_bounds__(kForwardThreads) void join_kernel(JoinArgs a) {
-  __shared__ double first[kForwardThreads / 64][1], second[kForwardThreads / 64][1];
+  __shared__ double first[16][1], second[16][1];
   __shared__ uint32_t tops[kForwardThreads / 64];
   const int tid = threadIdx.x, nt = blockDim.x, waves = nt >> 6;
   const int64_t base = (int64_t)blockIdx.x * a.H, gate = blockIdx.x * a.gate_row;
@@ -115,9 +146,11 @@ __global__ __launch_bounds__(kForwardThreads) void join_kernel(JoinArgs a) {
     sum_over(ss, first);
     const Factor f = factor_of(reciprocal_root(__builtin_fma(ss[0], a.over_h, a.eps)));
 #pragma unroll
-    for (int j = 0; j < NP; ++j)
+    for (int j = 0; j < NP; ++j) {
+      f.times(t[j]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t[j][i] = f.of(t[j][i]) * post[j].at(i);
+      for (int i = 0; i < 8; ++i) t[j][i] *= post[j].at(i);
+    }
   }
   ss[0] = 0.0;
 #pragma unroll
@@ -150,9 +183,10 @@ __global__ __launch_bounds__(kForwardThreads) void join_kernel(JoinArgs a) {
   for (int j = 0; j < NP; ++j) {
     const int c = (tid + j * nt) * 8;
     if (c < a.H) {
+      f.times(t[j]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        t[j][i] = f.of(t[j][i]) * pre[j].at(i);
+        t[j][i] *= pre[j].at(i);
         const uint32_t b = __float_as_uint(t[j][i]) & 0x7fffffffu;
         top = b > top ? b : top;
       }
@@ -224,56 +258,147 @@ struct BackArgs {
   double over_h, eps;
 };
 
-template <int DT, int NP>
-__global__ __launch_bounds__(kBackwardThreads) void join_backward_kernel(BackArgs a) {
-  // by the row's parity: a row's reductions may meet the next row's writes
-  __shared__ double first[2][kBackwardThreads / 64][3], second[2][kBackwardThreads / 64][1];
-  // Four pieces a thread leave no registers to hold a row over the reductions: it
+// Sum of eight products in fp32, in three levels: off by at most four half steps of the
+// sum of their magnitudes.
+__device__ __forceinline__ float dot8(const float (&a)[8], const float (&b)[8]) {
+  float p[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[i] = __builtin_fmaf(a[2 * i], b[2 * i], a[2 * i + 1] * b[2 * i + 1]);
+  return (p[0] + p[1]) + (p[2] + p[3]);
+}
+// Whether fp32 holds a sum of squares with all its bits, terms of 2^-24 of it too.
+__device__ __forceinline__ bool in_range(double s) { return s > 0x1p-80 && s < 0x1p120; }
+
+// Eight elements to a uniform address and an offset in bytes.
+template <int DT>
+__device__ __forceinline__ void put8(void* base, uint32_t at, const float (&v)[8]) {
+  bk_u32x4* p = reinterpret_cast<bk_u32x4*>((char*)base + at);
+  if constexpr (DT == LORA_BF16) {
+    *p = bk_u32x4{bk_pack(v[0], v[1]), bk_pack(v[2], v[3]), bk_pack(v[4], v[5]),
+                  bk_pack(v[6], v[7])};
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      p[h] = bk_u32x4{__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]),
+                      __float_as_uint(v[4 * h + 2]), __float_as_uint(v[4 * h + 3])};
+  }
+}
+template <int DT>
+__device__ __forceinline__ float element(const void* p, int64_t i) {
+  if constexpr (DT == LORA_F32) return ((const float*)p)[i];
+  return __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16);
+}
+
+// A thread's pieces of a row, as they are stored.
+template <int DT, int N>
+struct BackRow {
+  Raw<DT> y[N], t[N], dout[N], dsum[N], gate[N];
+};
+
+// The parts that a call has are the kernel's (kPre: a norm before the next block,
+// kPost: one after this, kGate), not questions at every element (8960 x 4096 bf16: 132
+// us with them).
+template <int DT, int NP, bool kPre, bool kPost, bool kGate>
+__global__ __launch_bounds__(kBackwardThreads, DT == LORA_BF16 && NP == 1 ? 4 : 2)
+void join_backward_kernel(BackArgs a) {
+  // One piece a thread: the next row's is fetched while this one is worked on.  Four pieces leave no registers to hold a row over the reductions: it
   // is read again, from the caches.
+  constexpr bool kAhead = NP == 1;
+  constexpr uint32_t ES = DT == LORA_F32 ? 4 : 2;
   constexpr int kHeld = NP < 4 ? NP : 1;
+  // by the row's parity: a row's reductions may meet the next row's writes
+  __shared__ double first[2][16][3], second[2][16][1];
   const int tid = threadIdx.x, nt = blockDim.x;
   float w_pre[NP][8] = {}, w_post[NP][8] = {}, w_gate[NP][8] = {};  // sums over the rows
+  Raw<DT> pre[kHeld], post[kHeld];
+  BackRow<DT, kHeld> now, next;
+  // (a row's address is uniform: one offset of 32 bits serves all arrays)
+  auto at_row = [&](const void* p, int64_t row) {
+    return (const void*)((const char*)p + row * ES);
+  };
+  // what the first reduction does not take
+  auto load_rest = [&](int row, int j, uint32_t c, BackRow<DT, kHeld>& r) {
+    if (a.dsum) r.dsum[j % kHeld].load_at(at_row(a.dsum, (int64_t)row * a.H), c * ES);
+    if (kGate) r.gate[j % kHeld].load_at(at_row(a.gate, row * a.gate_row), c * ES);
+  };
+  auto load_row = [&](int row, int j, uint32_t c, BackRow<DT, kHeld>& r) {
+    const int64_t base = (int64_t)row * a.H;
+    const int k = j % kHeld;
+    if (kPost || kGate) r.y[k].load_at(at_row(a.y, base), c * ES);
+    if (kPre) {
+      r.t[k].load_at(at_row(a.sum, base), c * ES);
+      r.dout[k].load_at(at_row(a.dout, base), c * ES);
+    }
+    if constexpr (!kAhead) load_rest(row, j, c, r);
+  };
+  auto load_weights = [&](int j, uint32_t c) {
+    if (kPre) pre[j % kHeld].load_at(a.pre, c * ES);
+    if (kPost) post[j % kHeld].load_at(a.post, c * ES);
+  };
+  if (kAhead && tid * 8 < a.H) load_row(blockIdx.x, 0, tid * 8, next);
   int parity = 0;
   for (int row = blockIdx.x; row < a.T; row += gridDim.x, parity ^= 1) {
-    const int64_t base = (int64_t)row * a.H, gate = row * a.gate_row;
-    Raw<DT> y[kHeld], t[kHeld], dout[kHeld], pre[kHeld];
-    auto load_y = [&](int j, int c) {
-      if (a.post || a.gate) y[j % kHeld].load(a.y, base + c);
-    };
-    auto load = [&](int j, int c) {
-      if (!a.pre) return;
-      t[j % kHeld].load(a.sum, base + c);
-      dout[j % kHeld].load(a.dout, base + c);
-      pre[j % kHeld].load(a.pre, c);
-    };
-    auto stat = [&](int j, double (&s)[3]) {
-      if (a.pre)
+    const int64_t base = (int64_t)row * a.H;
+    // (sums of the arrays' addresses and the thread's place are not kept over the rows)
+    uint32_t mine = (uint32_t)tid * 8;
+    if constexpr (kAhead) {
+      asm volatile("" : "+v"(mine));
+      now = next;
+      const int after = row + (int)gridDim.x;
+      if (mine < (uint32_t)a.H) {
+        load_rest(row, 0, mine, now);
+        if (after < a.T) load_row(after, 0, mine, next);
+      }
+    }
+    double s[3] = {0.0, 0.0, 0.0};  // of t^2, dout w_pre t and y^2
+    auto stat = [&](int j) {
+      const int k = j % kHeld;
+      float x[8], v[8];
+      if (kPre) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float x = t[j % kHeld].at(i);
-          s[0] = square_plus(x, s[0]);
-          s[1] = __builtin_fma((double)(dout[j % kHeld].at(i) * pre[j % kHeld].at(i)), (double)x,
-                               s[1]);
+          x[i] = now.t[k].at(i);
+          v[i] = now.dout[k].at(i) * pre[k].at(i);
         }
-      if (a.post)
+        s[0] += (double)dot8(x, x);
+        s[1] += (double)dot8(v, x);
+      }
+      if (kPost) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[2] = square_plus(y[j % kHeld].at(i), s[2]);
+        for (int i = 0; i < 8; ++i) x[i] = now.y[k].at(i);
+        s[2] += (double)dot8(x, x);
+      }
     };
-    double s[3] = {0.0, 0.0, 0.0};  // of t^2, dout w_pre t and y^2
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
-      const int c = (tid + j * nt) * 8;
-      if (c < a.H) {
-        load_y(j, c);
-        load(j, c);
-        if constexpr (kHeld < NP) stat(j, s);
+      const uint32_t c = mine + (uint32_t)(j * nt) * 8;
+      if (c < (uint32_t)a.H) {
+        if constexpr (!kAhead) load_row(row, j, c, now);
+        load_weights(j, c);
+        if constexpr (kHeld < NP) stat(j);
       }
     }
     if constexpr (kHeld == NP)
 #pragma unroll
       for (int j = 0; j < NP; ++j)
-        if ((tid + j * nt) * 8 < a.H) stat(j, s);
-    if (a.pre || a.post) sum_over(s, first[parity]);
+        if (mine + (uint32_t)(j * nt) * 8 < (uint32_t)a.H) stat(j);
+    if (kPre || kPost) sum_over(s, first[parity]);
+    if ((kPre && !in_range(s[0])) || (kPost && !in_range(s[2]))) {
+      // Squares past fp32's range: the row again, in 64 bits, an element at a time.
+      __syncthreads();
+      s[0] = s[1] = s[2] = 0.0;
+#pragma unroll 1
+      for (int i = tid; i < a.H; i += nt) {
+        if (kPre) {
+          const double x = element<DT>(a.sum, base + i);
+          s[0] = __builtin_fma(x, x, s[0]);
+          s[1] = __builtin_fma(
+              (double)(element<DT>(a.dout, base + i) * element<DT>(a.pre, i)), x, s[1]);
+        }
+        if (kPost) s[2] = square_plus(element<DT>(a.y, base + i), s[2]);
+      }
+      sum_over(s, first[parity]);
+    }
     const double rt = reciprocal_root(__builtin_fma(s[0], a.over_h, a.eps));
     const double ry = reciprocal_root(__builtin_fma(s[2], a.over_h, a.eps));
     const Factor ft = factor_of(rt), fy = factor_of(ry);
@@ -282,71 +407,89 @@ __global__ __launch_bounds__(kBackwardThreads) void join_backward_kernel(BackArg
     double s2[1] = {0.0};
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
-      const int c = (tid + j * nt) * 8;
-      if (c < a.H) {
-        Raw<DT> dsum, g, post;
-        if (a.dsum) dsum.load(a.dsum, base + c);
-        if (a.gate) g.load(a.gate, gate + c);
-        if (a.post) post.load(a.post, c);
+      const uint32_t c = mine + (uint32_t)(j * nt) * 8, k = j % kHeld;
+      if (c < (uint32_t)a.H) {
         if constexpr (kHeld < NP) {
           __builtin_amdgcn_sched_barrier(0);  // (a piece's loads and no more at a time)
-          load_y(j, c);
-          load(j, c);
+          load_row(row, j, c, now);
+          load_weights(j, c);
         }
-        float dres[8], dg[8];
+        float d[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, z[8];
+        if (kPre) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) z[i] = now.t[k].at(i);
+          ft.times(z);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float o = now.dout[k].at(i);
+            w_pre[j][i] = __builtin_fmaf(o, z[i], w_pre[j][i]);
+            d[i] = __builtin_fmaf(-z[i], ct, o * pre[k].at(i));
+          }
+          ft.times(d);
+        }
+        if (a.dsum)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) d[i] += now.dsum[k].at(i);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] = a.alpha * d[i];
+        put8<DT>((void*)at_row(a.dresidual, base), c * ES, z);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          float d = 0.f;
-          if (a.pre) {
-            const float hat = ft.of(t[j % kHeld].at(i)), o = dout[j % kHeld].at(i);
-            w_pre[j][i] += o * hat;
-            d = ft.of(o * pre[j % kHeld].at(i) - hat * ct);
-          }
-          if (a.dsum) d += dsum.at(i);
-          dres[i] = a.alpha * d;
-          d *= a.beta;
-          const float hat = a.post ? fy.of(y[j % kHeld].at(i)) : a.gate ? y[j % kHeld].at(i) : 0.f;
-          if (a.gate) {
-            dg[i] = d * (a.post ? hat * post.at(i) : hat);
-            w_gate[j][i] += dg[i];
-            d *= g.at(i);
-          }
-          if (a.post) {
-            w_post[j][i] += d * hat;
-            d *= post.at(i);
-            s2[0] = __builtin_fma((double)d, (double)y[j % kHeld].at(i), s2[0]);
-          }
-          dp[j][i] = d;
+          d[i] *= a.beta;
+          z[i] = kPost || kGate ? now.y[k].at(i) : 0.f;
         }
-        store8(a.dresidual, base + c, 8, DT, dres);
-        if (a.dgate) store8(a.dgate, base + c, 8, DT, dg);
-        if (!a.post) store8(a.dy, base + c, 8, DT, dp[j]);
+        if (kPost) fy.times(z);
+        if (kGate) {
+          float dg[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            dg[i] = d[i] * (kPost ? z[i] * post[k].at(i) : z[i]);
+            w_gate[j][i] += dg[i];
+            d[i] *= now.gate[k].at(i);
+          }
+          if (a.dgate) put8<DT>((void*)at_row(a.dgate, base), c * ES, dg);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (kPost) {
+            w_post[j][i] = __builtin_fmaf(d[i], z[i], w_post[j][i]);
+            d[i] *= post[k].at(i);
+          }
+          dp[j][i] = d[i];
+        }
+        // (with y normalised: the product with y itself may be past fp32's range)
+        if (kPost) s2[0] += (double)dot8(dp[j], z);
+        if (!kPost) put8<DT>((void*)at_row(a.dy, base), c * ES, dp[j]);
       }
     }
-    if (a.post) {
+    if (kPost) {
       sum_over(s2, second[parity]);
-      const float cy = (float)(s2[0] * ry * a.over_h);
+      const float cy = (float)(s2[0] * a.over_h);
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
-        const int c = (tid + j * nt) * 8;
-        if (c < a.H) {
+        const uint32_t c = mine + (uint32_t)(j * nt) * 8, k = j % kHeld;
+        if (c < (uint32_t)a.H) {
           float d[8];
-          if constexpr (kHeld < NP) load_y(j, c);
+          if constexpr (kHeld < NP) now.y[k].load_at(at_row(a.y, base), c * ES);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) d[i] = fy.of(dp[j][i] - fy.of(y[j % kHeld].at(i)) * cy);
-          store8(a.dy, base + c, 8, DT, d);
+          for (int i = 0; i < 8; ++i) d[i] = now.y[k].at(i);
+          fy.times(d);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) d[i] = __builtin_fmaf(-d[i], cy, dp[j][i]);
+          fy.times(d);
+          put8<DT>((void*)at_row(a.dy, base), c * ES, d);
         }
       }
     }
   }
 #pragma unroll
   for (int j = 0; j < NP; ++j) {
-    const int c = (tid + j * nt) * 8;
-    if (c < a.H) {
+    const uint32_t c = (uint32_t)(tid + j * nt) * 8;
+    if (c < (uint32_t)a.H) {
       const int64_t n = gridDim.x, at = (int64_t)blockIdx.x * a.H + c;
-      if (a.k_pre >= 0) store8(a.part, a.k_pre * n * a.H + at, 8, LORA_F32, w_pre[j]);
-      if (a.k_post >= 0) store8(a.part, a.k_post * n * a.H + at, 8, LORA_F32, w_post[j]);
-      if (a.k_gate >= 0) store8(a.part, a.k_gate * n * a.H + at, 8, LORA_F32, w_gate[j]);
+      if (kPre && a.k_pre >= 0) store8(a.part, a.k_pre * n * a.H + at, 8, LORA_F32, w_pre[j]);
+      if (kPost && a.k_post >= 0) store8(a.part, a.k_post * n * a.H + at, 8, LORA_F32, w_post[j]);
+      if (kGate && a.k_gate >= 0) store8(a.part, a.k_gate * n * a.H + at, 8, LORA_F32, w_gate[j]);
     }
   }
 }
@@ -365,6 +508,7 @@ __global__ __launch_bounds__(1024) void column_sums(SumArgs a) {
   const float* from = a.part + (int64_t)blockIdx.y * a.groups * a.H + c;
   float s = 0.f;
   if (c < a.H)
+#pragma unroll 8
     for (int r = wave; r < a.groups; r += 16) s += from[(int64_t)r * a.H];
   room[wave][lane] = s;
   __syncthreads();
@@ -376,15 +520,33 @@ __global__ __launch_bounds__(1024) void column_sums(SumArgs a) {
   to[c] = a.accumulate ? to[c] + s : s;
 }
 
+template <int DT, int NP, bool kPre, bool kPost>
+void launch_parts(const BackArgs& a, int groups, int nt, hipStream_t st) {
+  if (a.gate)
+    hipLaunchKernelGGL((join_backward_kernel<DT, NP, kPre, kPost, true>), dim3(groups), dim3(nt), 0,
+                       st, a);
+  else
+    hipLaunchKernelGGL((join_backward_kernel<DT, NP, kPre, kPost, false>), dim3(groups), dim3(nt),
+                       0, st, a);
+}
+template <int DT, int NP>
+void launch_pieces(const BackArgs& a, int groups, int nt, hipStream_t st) {
+  if (a.pre)
+    a.post ? launch_parts<DT, NP, true, true>(a, groups, nt, st)
+           : launch_parts<DT, NP, true, false>(a, groups, nt, st);
+  else
+    a.post ? launch_parts<DT, NP, false, true>(a, groups, nt, st)
+           : launch_parts<DT, NP, false, false>(a, groups, nt, st);
+}
 template <int DT>
 void launch_backward(const BackArgs& a, int groups, hipStream_t st) {
   const int nt = threads_of(a.H, kBackwardThreads), np = (a.H / 8 + nt - 1) / nt;
   if (np == 1)
-    hipLaunchKernelGGL((join_backward_kernel<DT, 1>), dim3(groups), dim3(nt), 0, st, a);
+    launch_pieces<DT, 1>(a, groups, nt, st);
   else if (np == 2)
-    hipLaunchKernelGGL((join_backward_kernel<DT, 2>), dim3(groups), dim3(nt), 0, st, a);
+    launch_pieces<DT, 2>(a, groups, nt, st);
   else
-    hipLaunchKernelGGL((join_backward_kernel<DT, 4>), dim3(groups), dim3(nt), 0, st, a);
+    launch_pieces<DT, 4>(a, groups, nt, st);
 }
 
 int32_t check_join(const lora_block_norm_desc* d) {

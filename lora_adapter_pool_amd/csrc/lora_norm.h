@@ -32,6 +32,12 @@ struct Raw {
     v[0] = p[0];
     if constexpr (DT == LORA_F32) v[1] = p[1];
   }
+  // from a uniform address and an offset in bytes
+  __device__ __forceinline__ void load_at(const void* base, uint32_t at) {
+    const bk_u32x4* p = reinterpret_cast<const bk_u32x4*>((const char*)base + at);
+    v[0] = p[0];
+    if constexpr (DT == LORA_F32) v[1] = p[1];
+  }
   __device__ __forceinline__ float at(int i) const {
     if constexpr (DT == LORA_F32) return __uint_as_float(v[i >> 2][i & 3]);
     const uint32_t w = v[0][i >> 1];
