@@ -536,7 +536,9 @@ typedef struct {
   int32_t parts;       /* pieces of adapters' rows */
   int32_t multi;       /* adapters of more than one piece */
   int32_t partials;    /* their pieces */
+  int32_t longest;     /* rows of the longest piece */
   int32_t chunk;       /* columns of a part of the reductions to rank space */
+  int32_t max_loras;   /* the pool's */
   int64_t image_bytes;
   int64_t off_perm;    /* int32 offsets inside the image: perm[rows + none], */
   int64_t off_tiles;   /* {slot or -1, rows, first row, 0}, */
@@ -713,7 +715,8 @@ int32_t lora_block_norm(const lora_block_norm_desc* desc, const void* y, const v
  * dpre_weight may be NULL.  The fp32 sums over the rows are overwritten, or added
  * to what is there where accumulate is 1 (for T = 0: zero, or left).  With
  * residual_scale = block_scale = 1, no gate and no post_weight these are the
- * gradients of lora_add_rms_norm (of out; dy = dresidual).  In place: dy may be y,
+ * gradients of lora_add_rms_norm (of out; dy = dresidual).  dy or dresidual may be
+ * NULL where it is not wanted.  In place: dy may be y,
  * dout or dsum, dresidual may be dout or dsum (each another one), and dgate an
  * element gate; other overlaps are not allowed. */
 int64_t lora_block_norm_backward_workspace_bytes(const lora_block_norm_desc* desc, int32_t T);

@@ -22,4 +22,4 @@ from ._lib import (  # noqa: F401
     lora_delta_backward_image_bytes, lora_delta_backward_workspace_bytes,
 )
 from .mlp import LoraMlp  # noqa: F401
-from .pool import LoraPool  # noqa: F401
+from .pool import DeltaPlan, LoraPool  # noqa: F401

@@ -80,7 +80,8 @@ class lora_delta_plan(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int32), ("none", ctypes.c_int32), ("tiles", ctypes.c_int32),
                 ("none_tiles", ctypes.c_int32), ("parts", ctypes.c_int32),
                 ("multi", ctypes.c_int32), ("partials", ctypes.c_int32),
-                ("chunk", ctypes.c_int32), ("image_bytes", ctypes.c_int64),
+                ("longest", ctypes.c_int32), ("chunk", ctypes.c_int32),
+                ("max_loras", ctypes.c_int32), ("image_bytes", ctypes.c_int64),
                 ("off_perm", ctypes.c_int64), ("off_tiles", ctypes.c_int64),
                 ("off_parts", ctypes.c_int64), ("off_multi", ctypes.c_int64)]
 

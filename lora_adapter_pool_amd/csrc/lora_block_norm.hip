@@ -432,7 +432,7 @@ void join_backward_kernel(BackArgs a) {
           for (int i = 0; i < 8; ++i) d[i] += now.dsum[k].at(i);
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[i] = a.alpha * d[i];
-        put8<DT>((void*)at_row(a.dresidual, base), c * ES, z);
+        if (a.dresidual) put8<DT>((void*)at_row(a.dresidual, base), c * ES, z);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           d[i] *= a.beta;
@@ -459,10 +459,10 @@ void join_backward_kernel(BackArgs a) {
         }
         // (with y normalised: the product with y itself may be past fp32's range)
         if (kPost) s2[0] += (double)dot8(dp[j], z);
-        if (!kPost) put8<DT>((void*)at_row(a.dy, base), c * ES, dp[j]);
+        if (!kPost && a.dy) put8<DT>((void*)at_row(a.dy, base), c * ES, dp[j]);
       }
     }
-    if (kPost) {
+    if (kPost && a.dy) {
       sum_over(s2, second[parity]);
       const float cy = (float)(s2[0] * a.over_h);
 #pragma unroll
@@ -646,7 +646,8 @@ extern "C" int32_t lora_block_norm_backward(
     if (dpost_weight && !post_weight)
       return fail(LORA_E_ARG, "dpost_weight without post_weight");
     if (dpre_weight && !pre_weight) return fail(LORA_E_ARG, "dpre_weight without pre_weight");
-    if (!dy || !dresidual) return fail(LORA_E_ARG, "dy and dresidual must not be NULL");
+    if (!dy && !dresidual && !dgate && !dpost_weight && !dpre_weight)
+      return fail(LORA_E_ARG, "every output is NULL");
     if ((post_weight || desc->gate != LORA_GATE_NONE) && !y)
       return fail(LORA_E_ARG, "y is NULL, and a norm or a gate takes it");
     if ((gate != nullptr) != (desc->gate != LORA_GATE_NONE))

@@ -33,7 +33,6 @@ using gemm::wait_all_lds;
 
 constexpr int kMaxFeatures = 1 << 22;
 constexpr int kPlanes = 3;       // bf16 pieces of an fp32 value
-constexpr int kGradsStages = 3;  // of 32 rows
 
 struct DeltaArgs {
   const char* A;
@@ -56,6 +55,7 @@ struct DeltaArgs {
   int32_t rows;     // with an adapter
   int64_t slots;    // 64 a tile
   int32_t partials;
+  int32_t longest;  // piece, in rows
   int32_t all;      // rows of x, dy, dx
   int32_t max_loras, K, S, O, R;
   int32_t padded, blocks;
@@ -626,13 +626,13 @@ __global__ __launch_bounds__(256, 4) void dx_kernel(DeltaArgs a) {
 // One workgroup: a piece of an adapter's rows, 512 bytes of columns of x or dy,
 // one rank block.  x or dy goes through a ring of stages of 32 rows in LDS, from which
 // both reads are of columns (a row of memory is a reduction index); a wave's 16
-// ranks of u or v come straight to registers, a step ahead.
-template <int DT, int NT, bool kOut>  // kOut: dB, from dy and v; else dA, from x and u
+// ranks of u or v come straight to registers, with the stages.
+template <int DT, int NT, int NST, bool kOut>  // kOut: dB, from dy and v; else dA, from x and u
 __device__ __forceinline__ void grads_tile(const DeltaArgs& a, char* lds, int slot, int rows,
                                            int first, int tile, int partial, int s, int rank0,
                                            int c0) {
   constexpr int ES = es(DT), P = DT == LORA_BF16 ? kPlanes : 1, XV = sizeof(Frag<DT>) / 16;
-  constexpr int RB = kDeltaColumnBytes, STAGE = 32 * RB, NST = kGradsStages;
+  constexpr int RB = kDeltaColumnBytes, STAGE = 32 * RB;
   constexpr int RL = 1024 / RB, LOADS = 8 / RL;  // rows of a load, a wave's loads of a stage
   constexpr int CT = RB / ES / 16 / (4 / NT);  // a wave's column tiles
   const int lane = threadIdx.x & 63;
@@ -666,8 +666,8 @@ __device__ __forceinline__ void grads_tile(const DeltaArgs& a, char* lds, int sl
     for (int j = 0; j < 8; ++j) k.t[j] = p[j];
     return k;
   };
-  auto load = [&](int kt, const Tokens& tok) {
-    char* to = lds + (kt % NST) * STAGE + wave * 8 * RB;
+  auto load = [&](int kt, int slot, const Tokens& tok) {
+    char* to = lds + slot * STAGE + wave * 8 * RB;
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) {
       int t = tok.t[RL * j];
@@ -695,44 +695,42 @@ __device__ __forceinline__ void grads_tile(const DeltaArgs& a, char* lds, int sl
       }
   };
   bk_f32x4 acc[CT] = {};
-  constexpr int AHEAD = 3;  // steps that u or v is fetched ahead
-  Ranks u[AHEAD + 1];
+  Ranks u[NST];
 #pragma unroll
-  for (int i = 0; i < AHEAD; ++i) load_u(i, u[i]);
+  for (int i = 0; i < NST - 1; ++i) load_u(i, u[i]);
   asm volatile("" ::: "memory");
   Tokens tok = fetch(0);
 #pragma unroll
   for (int i = 0; i < NST - 1; ++i) {
     const Tokens next = fetch(i + 1);
-    load(i, tok);
+    load(i, i, tok);
     tok = next;
   }
-  auto step = [&](int kt, const Ranks& now, Ranks& ahead) {
+  // step kt, whose stage is in `slot` (a constant: the loop below is over the ring)
+  auto step = [&](int kt, int slot) {
+    const int last = (slot + NST - 1) % NST;
     wait_loads<(NST - 2) * LOADS>();
     barrier();
-    load_u(kt + AHEAD, ahead);
+    load_u(kt + NST - 1, u[last]);
     const Tokens next = fetch(kt + NST);
-    load(kt + NST - 1, tok);
+    load(kt + NST - 1, last, tok);
     tok = next;
-    const char* at = lds + (kt % NST) * STAGE;
+    const char* at = lds + slot * STAGE;
 #pragma unroll
     for (int i = 0; i < CT; ++i) {
       const Frag<DT> x = read_cols<DT, RB>(at, 0, col + 16 * i, 4, l16, g);
 #pragma unroll
       for (int p = P - 1; p >= 0; --p)  // the smallest first
-        acc[i] = kOut ? product<DT>(now.f[p], x, acc[i]) : product<DT>(x, now.f[p], acc[i]);
+        acc[i] = kOut ? product<DT>(u[slot].f[p], x, acc[i]) : product<DT>(x, u[slot].f[p], acc[i]);
     }
+    return kt + 1 < nk;
   };
   wait_loads<(NST - 1) * LOADS>();
-  for (int kt = 0;;) {
-    step(kt, u[0], u[3]);
-    if (++kt >= nk) break;
-    step(kt, u[1], u[0]);
-    if (++kt >= nk) break;
-    step(kt, u[2], u[1]);
-    if (++kt >= nk) break;
-    step(kt, u[3], u[2]);
-    if (++kt >= nk) break;
+  for (int kt = 0;; kt += NST) {
+    if (!step(kt, 0)) break;
+    if (!step(kt + 1, 1)) break;
+    if constexpr (NST > 2)
+      if (!step(kt + 2, 2)) break;
   }
   wait_loads<0>();
 
@@ -767,16 +765,18 @@ __device__ __forceinline__ void grads_tile(const DeltaArgs& a, char* lds, int sl
   }
 }
 
-template <int DT, int NT>
+// NST: stages of the ring.  Three, 48 KB, let three workgroups share a compute unit;
+// pieces of at most two steps take no third.
+template <int DT, int NT, int NST>
 __global__ __launch_bounds__(256, 2) void grads_kernel(DeltaArgs a) {
-  __shared__ __attribute__((aligned(16))) char lds[kGradsStages * 32 * kDeltaColumnBytes];
+  __shared__ __attribute__((aligned(16))) char lds[NST * 32 * kDeltaColumnBytes];
   constexpr int CB = kDeltaColumnBytes / es(DT);
   const int jobs = gridDim.x / a.num_parts, part = blockIdx.x / jobs;
   int job = blockIdx.x - part * jobs, slot, n, first;
   const int32_t* rec = a.parts + 4 * part;  // (the longest first)
   const int rows = rec[1], tile = rec[2], partial = rec[3];
   if (tile < 0 || tile >= a.num_tiles || !take_tile(a, tile, slot, n, first) || slot != rec[0] ||
-      rows < 1 || first > a.rows - rows || (rows + 63) / 64 > a.num_tiles - tile ||
+      rows < 1 || rows > a.longest || first > a.rows - rows || (rows + 63) / 64 > a.num_tiles - tile ||
       partial < -1 || partial >= a.partials)
     return;
   const int rank0 = job % a.blocks * 16 * NT;
@@ -788,9 +788,9 @@ __global__ __launch_bounds__(256, 2) void grads_kernel(DeltaArgs a) {
     job -= n;
   }
   if (s < a.S)
-    return grads_tile<DT, NT, true>(a, lds, slot, rows, first, tile, partial, s, rank0, job * CB);
+    return grads_tile<DT, NT, NST, true>(a, lds, slot, rows, first, tile, partial, s, rank0, job * CB);
   n = parts_of(a.K, CB);
-  grads_tile<DT, NT, false>(a, lds, slot, rows, first, tile, partial, job / n, rank0, job % n * CB);
+  grads_tile<DT, NT, NST, false>(a, lds, slot, rows, first, tile, partial, job / n, rank0, job % n * CB);
 }
 
 // ----------------------------------------------------- 5: cut adapters' sums
@@ -836,7 +836,10 @@ int32_t run(DeltaArgs& a, hipStream_t st) {
   if (a.dA && a.rows) {
     const int64_t blocks = a.num_parts * count(kDeltaColumnBytes / es(DT));
     if (blocks > INT32_MAX) return fail(LORA_E_SHAPE, "too many workgroups");
-    hipLaunchKernelGGL((grads_kernel<DT, NT>), dim3((uint32_t)blocks), dim3(256), 0, st, a);
+    if (a.longest <= 64)
+      hipLaunchKernelGGL((grads_kernel<DT, NT, 2>), dim3((uint32_t)blocks), dim3(256), 0, st, a);
+    else
+      hipLaunchKernelGGL((grads_kernel<DT, NT, 3>), dim3((uint32_t)blocks), dim3(256), 0, st, a);
   }
   if (a.dA && a.num_multi) {
     const int64_t values = (int64_t)a.R * ((int64_t)a.S * a.K + a.O);
@@ -910,6 +913,7 @@ extern "C" int32_t lora_delta_backward(const lora_pool_desc* desc, const void* A
   a.rows = plan->rows;
   a.slots = (int64_t)plan->tiles * kDeltaTileRows;
   a.partials = plan->partials;
+  a.longest = plan->longest;
   a.all = T;
   a.max_loras = g.max_loras;
   a.K = g.K;

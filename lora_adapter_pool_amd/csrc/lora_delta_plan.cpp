@@ -105,7 +105,8 @@ int32_t delta_check_plan(const Geo& g, int32_t T, const lora_delta_plan* p) {
       p->off_multi == p->off_parts + 4 * (int64_t)p->parts &&
       p->image_bytes == 4 * (p->off_multi + 4 * (int64_t)p->multi) &&
       p->image_bytes <= 4 * w.total && (p->tiles > 0) == (p->rows > 0) &&
-      (p->none_tiles > 0) == (p->none > 0) && (p->parts > 0) == (p->rows > 0);
+      (p->none_tiles > 0) == (p->none > 0) && (p->parts > 0) == (p->rows > 0) &&
+      p->longest >= 0 && p->longest <= p->rows && p->max_loras == g.max_loras;
   if (!fits || p->chunk != shrink_chunk(g, p->tiles))
     return fail(LORA_E_ARG, "the plan is not lora_delta_backward_plan's for this pool and T");
   return LORA_OK;
@@ -221,6 +222,8 @@ extern "C" int32_t lora_delta_backward_plan(const lora_pool_desc* desc, int32_t 
   std::sort(parts, parts + p.parts, [](const Record& a, const Record& b) {
     return a.w[1] != b.w[1] ? a.w[1] > b.w[1] : a.w[2] < b.w[2];
   });
+  p.max_loras = g.max_loras;
+  p.longest = p.parts ? parts[0].w[1] : 0;
   p.chunk = (int32_t)shrink_chunk(g, p.tiles);
   p.image_bytes = (put - at) * 4;
   *plan = p;

@@ -4,6 +4,8 @@
     n = rms_norm(s) * norm_weight             (and, for 8-bit weights, n in e4m3)
     h = act(n Wg^T + dg) * (n Wu^T + du)      dg, du: the adapters' gate/up delta
     y = h Wd^T + dd + s                       dd: the adapters' down delta
+or, in models with a norm after the block, a gate or scales of the two branches,
+    y = residual_scale s + block_scale gate rms_norm(h Wd^T + dd) post_norm_weight
 
 Every row names its adapter slot in each pool, or none (-1).  The adapters'
 deltas are LoraPool.apply onto zeros; they join the base products before the
@@ -20,6 +22,8 @@ from __future__ import annotations
 
 from typing import Optional
 
+import numpy as np
+
 from . import _lib as L
 from .pool import LoraPool
 
@@ -28,11 +32,14 @@ class LoraMlp:
     """norm_weight [H], w_gate_up [2 I][H] (gate rows, then up rows), w_down
     [H][I], all of the activations' dtype (fp32 or bf16); or w_gate_up in e4m3
     with one fp32 scale a row in gate_up_scale, for bf16 activations.  gate_up
-    and down: pools of the activations' dtype with slices [I, I] and [H]."""
+    and down: pools of the activations' dtype with slices [I, I] and [H].
+    post_norm_weight, gate [H] (of the activations' dtype), residual_scale,
+    block_scale: of the second form of y; post_norm_weight and gate may be None."""
 
     def __init__(self, norm_weight, w_gate_up, w_down, eps: float = 1e-5, act: str = "silu",
                  gate_up_scale=None, gate_up: Optional[LoraPool] = None,
-                 down: Optional[LoraPool] = None):
+                 down: Optional[LoraPool] = None, post_norm_weight=None, gate=None,
+                 residual_scale: float = 1.0, block_scale: float = 1.0):
         import torch
 
         self.torch = torch
@@ -59,7 +66,12 @@ class LoraMlp:
                 raise L.LoraError(L.LORA_E_SHAPE, "a pool does not fit the block")
             if pool is not None and pool.A.device != w_down.device:
                 raise L.LoraError(L.LORA_E_ARG, "a pool is not on the weights' device")
-        for t in (norm_weight, w_gate_up, w_down, gate_up_scale):
+        for t in (post_norm_weight, gate):
+            if t is not None and t.dtype != w_down.dtype:
+                raise L.LoraError(L.LORA_E_DTYPE, "post_norm_weight and gate have w_down's dtype")
+            if t is not None and tuple(t.shape) != (self.H,):
+                raise L.LoraError(L.LORA_E_SHAPE, "post_norm_weight and gate must be [H]")
+        for t in (norm_weight, w_gate_up, w_down, gate_up_scale, post_norm_weight, gate):
             if t is not None and not t.is_contiguous():
                 raise L.LoraError(L.LORA_E_SHAPE, "weights must be contiguous")
             if t is not None and t.device != w_down.device:
@@ -71,9 +83,19 @@ class LoraMlp:
                                             self.H, self.I, act)
         self.grad_desc = L.make_gated_desc(self.dtype, self.dtype, self.H, self.I, act)
         self.down_desc = L.make_linear_desc(self.dtype, self.dtype, self.I, self.H)
+        self.post_norm_weight, self.gate = post_norm_weight, gate
+        self.norm_grad_desc = L.make_block_norm_desc(self.dtype, self.H, eps)
+        self.join_desc = None
+        if post_norm_weight is not None or gate is not None or residual_scale != 1.0 or \
+                block_scale != 1.0:
+            self.join_desc = L.make_block_norm_desc(
+                self.dtype, self.H, eps, "none" if gate is None else "channel", residual_scale,
+                block_scale)
+        self.dh_desc = L.make_linear_desc(self.dtype, self.dtype, self.H, self.I)
         self._ws = None
         self._outgrown = []
         self._saved = None
+        self._saved_rest = None
 
     def _workspace(self, need: int):
         have = 0 if self._ws is None else self._ws.numel()
@@ -106,7 +128,7 @@ class LoraMlp:
     def forward(self, x, residual, ids=None, prefill=None, keep: bool = False):
         """y [T][H] on the current stream of the weights' GPU.  ids, prefill: as
         LoraPool.apply takes them (None: no adapters).  keep: hold what
-        gate_up_backward needs."""
+        gate_up_backward and backward need."""
         self._check_rows(x, self.H, "x")
         self._check_rows(residual, self.H, "residual")
         if residual.shape != x.shape:
@@ -132,8 +154,19 @@ class LoraMlp:
         L.lora_gated_ffn(self.gated_desc, n8 if self.eight else n, self.w_gate_up, scale,
                          self.gate_up_scale, d, pre, h, T, ws, ws.numel())
         d = self._delta(self.down, h, ids, prefill, H)
-        L.lora_linear(self.down_desc, h, self.w_down, None, None, None, d, s, y, T, ws, ws.numel())
+        block = None
+        if self.join_desc is None:
+            L.lora_linear(self.down_desc, h, self.w_down, None, None, None, d, s, y, T, ws,
+                          ws.numel())
+        else:
+            block = new(T, H)
+            L.lora_linear(self.down_desc, h, self.w_down, None, None, None, d, None, block, T, ws,
+                          ws.numel())
+            L.lora_block_norm(self.join_desc, block, s, self.gate, self.post_norm_weight, None, y,
+                              None, None, None, T)
         self._saved = (n, pre) if keep else None
+        kept = None if ids is None else np.array(ids, dtype=np.int32)
+        self._saved_rest = (s, h, block, kept) if keep else None
         return y
 
     def _delta(self, pool, x, ids, prefill, width):
@@ -168,3 +201,84 @@ class LoraMlp:
         L.lora_gated_ffn_backward(self.grad_desc, dh, pre, n if need_dw else None, self.w_gate_up,
                                   dpre, dn, dw, T, ws, ws.numel())
         return dpre, dn, dw
+
+    def backward(self, dy, w_down_t, need_dw: bool = False, grads=None, accumulate: bool = False):
+        """Gradients of the kept forward pass from dy [T][H], the gradient of y, as a dict:
+        "x" (also residual's), "norm_weight" (fp32, as the next two), "post_norm_weight", "gate",
+        "gate_up" and "down" ((dA, dB) of the pools, as LoraPool.backward gives them) and
+        "w_gate_up" (need_dw).  w_down_t: w_down transposed, [I][H]; the base is frozen in this
+        pass, so that a program makes it once.  grads: buffers for the fp32 sums by these names,
+        which accumulate adds to; new ones are made for the others.  Weights must not be in
+        e4m3.  Takes the kept pass with it."""
+        if self._saved is None:
+            raise L.LoraError(L.LORA_E_ARG, "no forward pass was kept (keep=True)")
+        if self.eight:
+            raise L.LoraError(L.LORA_E_DTYPE, "the gradients take weights in fp32 or bf16")
+        self._check_rows(dy, self.H, "dy")
+        if dy.shape[0] != self._saved[0].shape[0]:
+            raise L.LoraError(L.LORA_E_SHAPE, "dy must have the kept pass's rows")
+        if tuple(w_down_t.shape) != (self.I, self.H) or not w_down_t.is_contiguous():
+            raise L.LoraError(L.LORA_E_SHAPE, "w_down_t must be a contiguous [I, H]")
+        if w_down_t.dtype != self.w_down.dtype or w_down_t.device != self.w_down.device:
+            raise L.LoraError(L.LORA_E_DTYPE, "w_down_t must have w_down's dtype and device")
+        grads = dict(grads or {})
+        names = {"norm_weight", "post_norm_weight", "gate", "gate_up", "down"}
+        if set(grads) - names:
+            raise L.LoraError(L.LORA_E_ARG, f"unknown gradients {sorted(set(grads) - names)}")
+        for k in ("norm_weight", "post_norm_weight", "gate"):
+            t = grads.get(k)
+            if t is not None and (t.dtype != self.torch.float32 or tuple(t.shape) != (self.H,) or
+                                  not t.is_contiguous() or t.device != self.w_down.device):
+                raise L.LoraError(L.LORA_E_SHAPE, f"the gradient of {k} must be fp32 [H]")
+        return self._on_device(self._backward, dy, w_down_t, need_dw, grads, accumulate)
+
+    def _backward(self, dy, w_down_t, need_dw, grads, accumulate):
+        torch = self.torch
+        (n, pre), (s, h, block, ids) = self._saved, self._saved_rest
+        T, out = int(dy.shape[0]), {}
+        row = lambda k: (grads[k] if k in grads else  # noqa: E731
+                         torch.zeros(self.H, device=dy.device))
+        ws = self._workspace(max(
+            L.lora_linear_workspace_bytes(self.dh_desc, T),
+            L.lora_gated_ffn_backward_workspace_bytes(self.grad_desc, T, True, need_dw),
+            L.lora_block_norm_backward_workspace_bytes(self.norm_grad_desc, T)))
+
+        def adapters(name, pool, x, d, dx):
+            """dx += the adapters' part; their gradients."""
+            if pool is None or ids is None:
+                return
+            dA, dB = grads.get(name, (None, None))
+            plan = pool.backward_plan(ids)
+            out[name] = pool.backward(x, d, plan, dx, dx, dA, dB, accumulate=accumulate)[1:]
+
+        ds, db = dy, dy     # gradients of s and of the block's output
+        if self.join_desc is not None:
+            ds, db = torch.empty_like(dy), torch.empty_like(dy)
+            if self.post_norm_weight is not None:
+                out["post_norm_weight"] = row("post_norm_weight")
+            if self.gate is not None:
+                out["gate"] = row("gate")
+            L.lora_block_norm_backward(
+                self.join_desc, None, dy, block, None, self.gate, self.post_norm_weight, None, db,
+                ds, out.get("gate"), out.get("post_norm_weight"), None, accumulate, T, ws,
+                ws.numel())
+        dh = torch.empty_like(h)
+        L.lora_linear(self.dh_desc, db, w_down_t, None, None, None, None, None, dh, T, ws,
+                      ws.numel())
+        adapters("down", self.down, h, db, dh)
+        dpre, dn = torch.empty_like(pre), torch.empty_like(n)
+        dw = torch.empty_like(self.w_gate_up) if need_dw else None
+        L.lora_gated_ffn_backward(self.grad_desc, dh, pre, n if need_dw else None, self.w_gate_up,
+                                  dpre, dn, dw, T, ws, ws.numel())
+        if need_dw:
+            out["w_gate_up"] = dw
+        adapters("gate_up", self.gate_up, n, dpre, dn)
+        out["norm_weight"] = row("norm_weight")
+        dx = torch.empty_like(dy)
+        # (sum = x + residual: one gradient for both)
+        L.lora_block_norm_backward(self.norm_grad_desc, dn, ds, None, s, None, None,
+                                   self.norm_weight, None, dx, None, None, out["norm_weight"],
+                                   accumulate, T, ws, ws.numel())
+        out["x"] = dx
+        self._saved = self._saved_rest = None
+        return out

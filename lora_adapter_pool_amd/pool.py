@@ -17,6 +17,19 @@ import numpy as np
 from . import _lib as L
 
 
+class DeltaPlan:
+    """The plan of a batch's rows for LoraPool.backward: the host's records and their image
+    on the pool's GPU.  It serves every pool of this geometry, and every call with these ids
+    (the layers of a step); keep it as long as graphs that its calls were captured in."""
+
+    def __init__(self, desc, ids, device):
+        import torch
+
+        self.struct, image = L.lora_delta_backward_plan(desc, ids)
+        self.T = self.struct.rows + self.struct.none
+        self.image = torch.from_numpy(image).to(device)
+
+
 class LoraPool:
     def __init__(self, dtype: str, max_loras: int, max_lora_rank: int, in_features: int,
                  out_features: Sequence[int], device: str = "cuda", staging_slots: int = 3):
@@ -39,6 +52,8 @@ class LoraPool:
         # rank last loaded into each (slot, slice); 0 = nothing loaded (zeros)
         self.loaded_ranks = np.zeros((self.max_loras, len(self.out_features)), np.int32)
         self._ws = None
+        self._bws = None
+        self._outgrown: List = []
         self._staging: List[list] = [[None, None] for _ in range(max(1, staging_slots))]
         self._next = 0
 
@@ -72,6 +87,70 @@ class LoraPool:
         st = self.torch.cuda.current_stream() if stream is None else stream
         L.lora_merge_weights(self.desc, self.A, self.B, slot, slice_, W, out, stream=st)
         return out
+
+    def backward_plan(self, ids) -> DeltaPlan:
+        """The plan that backward takes; ids int32 per row (-1 = none), on the host."""
+        return DeltaPlan(self.desc, ids, self.A.device)
+
+    def backward(self, x, dy, plan: DeltaPlan, dx_in=None, dx=None, dA=None, dB=None,
+                 need_dx: bool = True, need_grads: bool = True, accumulate: bool = False):
+        """Gradients of apply: (dx, dA, dB) from dy [T, O], the gradient of y, on the current
+        stream of the pool's GPU.
+        dx [T, K] = dx_in (the base projection's part; None: zeros) + the delta's; it may be
+        dx_in itself.  dA, dB: fp32 gradients of A_view() and B_view(), overwritten or added to
+        (accumulate) for the batch's slots, others left; new ones are zeros.  peft's lora_B has
+        the adapter's scale times dB's gradient."""
+        torch = self.torch
+        if not self.A.is_cuda:
+            raise L.LoraError(L.LORA_E_ARG, "the pool is not on a GPU")
+        if not need_dx and not need_grads:
+            raise L.LoraError(L.LORA_E_ARG, "neither dx nor the adapters' gradients are wanted")
+        T, S = plan.T, len(self.out_features)
+        want = {"x": (x, (T, self.K), self.tdtype), "dy": (dy, (T, self.O), self.tdtype),
+                "dx_in": (dx_in, (T, self.K), self.tdtype), "dx": (dx, (T, self.K), self.tdtype),
+                "dA": (dA, (self.max_loras, S, self.R, self.K), torch.float32),
+                "dB": (dB, (self.max_loras, self.O, self.R), torch.float32)}
+        for name, (t, shape, dtype) in want.items():
+            if t is None:
+                continue
+            if t.dtype != dtype or t.device != self.A.device:
+                raise L.LoraError(L.LORA_E_DTYPE, f"{name} must be {dtype} on the pool's GPU")
+            if tuple(t.shape) != shape or not t.is_contiguous():
+                raise L.LoraError(L.LORA_E_SHAPE, f"{name} must be a contiguous {list(shape)}")
+        if not need_dx and (dx is not None or dx_in is not None):
+            raise L.LoraError(L.LORA_E_ARG, "dx is given and not wanted")
+        if not need_grads and (dA is not None or dB is not None):
+            raise L.LoraError(L.LORA_E_ARG, "dA or dB is given and not wanted")
+        if (dA is None) != (dB is None):
+            raise L.LoraError(L.LORA_E_ARG, "dA and dB go together: one of them is None")
+        with torch.cuda.device(self.A.device):
+            if need_grads and dA is None:
+                dA = torch.zeros(want["dA"][1], device=self.A.device)
+                dB = torch.zeros(want["dB"][1], device=self.A.device)
+            if need_dx and dx is None:
+                dx = torch.empty_like(x)
+            ws = self._backward_workspace(T)
+            if T:
+                L.lora_delta_backward(self.desc, self.A, self.B, x, dy, dx_in, dx, dA, dB, T,
+                                      plan.struct, plan.image, accumulate, ws, ws.numel())
+        return dx, dA, dB
+
+    def _backward_workspace(self, T: int):
+        need = L.lora_delta_backward_workspace_bytes(self.desc, T)
+        have = 0 if self._bws is None else self._bws.numel()
+        if have < max(need, 1):
+            if have:   # graphs that were captured before hold its address
+                self._outgrown.append(self._bws)
+            self._bws = self.torch.empty(max(need, 2 * have, 256), dtype=self.torch.uint8,
+                                         device=self.A.device)
+        return self._bws
+
+    def slot_grads(self, dA, dB, slots, outs=None) -> L.GradList:
+        """The gradients of some slots as lora_clip_grads takes them, a group for each slot in
+        turn; outs: (dA, dB) that the clipped gradients go to (None: in place)."""
+        pick = lambda a, b: [t[int(k)] for k in slots for t in (a, b)]  # noqa: E731
+        return L.GradList(pick(dA, dB), [g for g in range(len(slots)) for _ in range(2)],
+                          None if outs is None else pick(*outs), num_groups=len(slots))
 
     def slot_ranks(self) -> np.ndarray:
         """int32[max_loras]: the largest rank loaded into each slot; a slot with

@@ -1,0 +1,57 @@
+"""LoraPool.backward's and LoraMlp.backward's checks on the CPU (nothing is launched)."""
+import numpy as np
+import pytest
+import torch
+
+import lora_adapter_pool_amd as L
+from lora_adapter_pool_amd import _lib
+
+
+def refused(status, f, *a, **k):
+    with pytest.raises(L.LoraError) as e:
+        f(*a, **k)
+    assert e.value.status == status
+
+
+def test_pool_refusals():
+    pool = L.LoraPool("bf16", 2, 8, 64, [72], device="cpu")
+    plan = pool.backward_plan([0, 1, -1])
+    assert plan.T == 3 and plan.image.dtype == torch.int32
+    x, dy = torch.zeros(3, 64).bfloat16(), torch.zeros(3, 72).bfloat16()
+    refused(_lib.LORA_E_ARG, pool.backward, x, dy, plan)            # not on a GPU
+    refused(_lib.LORA_E_ID, pool.backward_plan, [0, 2])
+    refused(_lib.LORA_E_SHAPE, pool.backward_plan, np.zeros((2, 2), np.int32))
+
+
+def test_another_pools_plan():
+    a = L.make_desc("bf16", 8, 16, 256, [256])
+    b = L.make_desc("bf16", 4, 16, 256, [256])
+    plan, _ = L.lora_delta_backward_plan(a, [7, 0, 1])
+    refused(_lib.LORA_E_ARG, L.lora_delta_backward, b, *[1 << 20] * 8, 3, plan, 1 << 20, False,
+            1 << 20, 1 << 40, stream=0)
+
+
+def test_mlp_refusals():
+    w = [torch.ones(64).bfloat16(), torch.zeros(144, 64).bfloat16(), torch.zeros(64, 72).bfloat16()]
+    refused(_lib.LORA_E_DTYPE, L.LoraMlp, *w, gate=torch.ones(64))
+    refused(_lib.LORA_E_SHAPE, L.LoraMlp, *w, post_norm_weight=torch.ones(72).bfloat16())
+    m = L.LoraMlp(*w)
+    dy, wt = torch.zeros(4, 64).bfloat16(), torch.zeros(72, 64).bfloat16()
+    refused(_lib.LORA_E_ARG, m.backward, dy, wt)                    # nothing kept
+    m._saved, m._saved_rest = (dy, torch.zeros(4, 144).bfloat16()), (dy, dy, None, None)
+    refused(_lib.LORA_E_SHAPE, m.backward, dy[:3], wt)
+    refused(_lib.LORA_E_DTYPE, m.backward, dy.float(), wt)
+    refused(_lib.LORA_E_SHAPE, m.backward, dy, wt.t())
+    refused(_lib.LORA_E_DTYPE, m.backward, dy, wt.float())
+    refused(_lib.LORA_E_ARG, m.backward, dy, wt, grads={"x": dy})
+    refused(_lib.LORA_E_SHAPE, m.backward, dy, wt, grads={"gate": torch.zeros(64).bfloat16()})
+    assert m._saved is not None
+
+
+def test_forms_of_the_block():
+    w = [torch.ones(64), torch.zeros(144, 64), torch.zeros(64, 72)]
+    assert L.LoraMlp(*w).join_desc is None
+    d = L.LoraMlp(*w, residual_scale=0.5).join_desc
+    assert (d.gate, d.residual_scale, d.block_scale) == (0, 0.5, 1.0)
+    d = L.LoraMlp(*w, gate=torch.ones(64), block_scale=2.0).join_desc
+    assert (d.gate, d.residual_scale, d.block_scale) == (1, 1.0, 2.0)

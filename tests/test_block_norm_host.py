@@ -89,12 +89,13 @@ def test_backward_refusals():
     variants(L.lora_block_norm_backward, ok, [(0, b, w) for b, w in BAD[:-1]] + [
         (0, mk("bf16", 1024, 1e-5), _lib.LORA_E_ARG), (1, None, _lib.LORA_E_ARG),
         (3, None, _lib.LORA_E_ARG), (4, None, _lib.LORA_E_ARG), (5, None, _lib.LORA_E_ARG),
-        (6, None, _lib.LORA_E_ARG), (7, None, _lib.LORA_E_ARG), (8, None, _lib.LORA_E_ARG),
-        (9, None, _lib.LORA_E_ARG), (12, FAKE + 4, _lib.LORA_E_ALIGN),
+        (6, None, _lib.LORA_E_ARG), (7, None, _lib.LORA_E_ARG), (12, FAKE + 4, _lib.LORA_E_ALIGN),
         (15, FAKE + 4, _lib.LORA_E_ALIGN), (13, 2, _lib.LORA_E_ARG), (14, -1, _lib.LORA_E_ARG),
         (14, (1 << 21) + 1, _lib.LORA_E_SHAPE), (15, None, _lib.LORA_E_ARG),
         (16, need - 1, _lib.LORA_E_WORKSPACE)])
     none = [d, None, None] + [FAKE] * 3 + [FAKE, None] + [FAKE] * 4 + [None, 0, 4, FAKE, need]
     assert status(L.lora_block_norm_backward, *none) == _lib.LORA_E_ARG   # no gradient comes in
+    nothing = [d] + [FAKE] * 7 + [None] * 5 + [0, 4, FAKE, need]
+    assert status(L.lora_block_norm_backward, *nothing) == _lib.LORA_E_ARG   # and none goes out
     # nothing to add to over no rows
     assert status(L.lora_block_norm_backward, d, *[None] * 12, 1, 0, None, 0) == 0

@@ -125,6 +125,26 @@ def test_in_place(dtype, H):
             assert torch.equal(want[k], got[k]), (gate, k)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H", [520, 8192, 16384])
+def test_outputs_that_are_not_wanted(dtype, H):
+    for gate, post in (("channel", True), ("element", False), ("none", False)):
+        s = inputs(H + 1, 9, H, dtype, gate)
+        want = run_join_backward(s, dtype, gate, post=post)
+        d = L.make_block_norm_desc(dtype, H, 1e-5, gate)
+        n = L.lora_block_norm_backward_workspace_bytes(d, 9)
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        y = s["y"] if post or gate != "none" else None
+        for name in ("dy", "dresidual", "dpre"):
+            out = torch.full_like(want[name], float("nan"))
+            o = {name: out}
+            L.lora_block_norm_backward(
+                d, s["dout"], s["dsum"], y, s["sum"], s["gate"], s["post"] if post else None,
+                s["pre"], o.get("dy"), o.get("dresidual"), None, None, o.get("dpre"), False, 9, ws,
+                n)
+            assert torch.equal(out, want[name]), (gate, post, name)
+
+
 def test_plain_norm_is_the_same():
     """No gate, scales of one and no norm after the block: lora_add_rms_norm, bit for bit."""
     for dtype in ("bf16", "f32"):
