@@ -63,6 +63,7 @@ struct DeltaArgs {
   int32_t accumulate;
   int32_t jobs;       // workgroups of the ranks for one tile
   int32_t dx_groups;  // of dx for one tile
+  int32_t dx_blocks;  // of dx in the gradients' launch
   int32_t out[LORA_MAX_SLICES], off[LORA_MAX_SLICES];
 };
 
@@ -518,18 +519,18 @@ __global__ __launch_bounds__(256) void join_kernel(DeltaArgs a) {
 // A for these columns in LDS, 128 ranks at a time, a wave's 16 rows of u and of dx_in
 // straight to registers.  The columns are dealt to the output's index so that a
 // lane's are neighbours in memory.
+constexpr int kDxLds = 128 * 256;
 template <int DT>
-__global__ __launch_bounds__(256, 4) void dx_kernel(DeltaArgs a) {
-  constexpr int ES = es(DT), RB = 256, CB = RB / ES, RANKS = 128;
+__device__ __forceinline__ void dx_tile(const DeltaArgs& a, char* lds, int block) {
+  constexpr int ES = es(DT), RB = 256, CB = RB / ES, RANKS = kDxLds / RB;
   constexpr int P = DT == LORA_BF16 ? 2 : 1, XV = sizeof(Frag<DT>) / 16;
   constexpr int CT = CB / 16, V = 16 / ES;  // column tiles; columns of a 16-byte piece
   constexpr int TV = V / 4, NV = CT / TV;   // tiles a piece spans; a lane's pieces
-  __shared__ __attribute__((aligned(16))) char lds[RANKS * RB];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   // (where the groups are a multiple of 8, one XCD takes a column group of all tiles)
-  const int tile = blockIdx.x / a.dx_groups, c0 = (blockIdx.x - tile * a.dx_groups) * CB;
+  const int tile = block / a.dx_groups, c0 = (block - tile * a.dx_groups) * CB;
   int slot, rows, first;
   const bool none = tile >= a.num_tiles;
   if (none) {
@@ -765,13 +766,25 @@ __device__ __forceinline__ void grads_tile(const DeltaArgs& a, char* lds, int sl
   }
 }
 
+template <int DT>
+__global__ __launch_bounds__(256, 4) void dx_kernel(DeltaArgs a) {
+  __shared__ __attribute__((aligned(16))) char lds[kDxLds];
+  dx_tile<DT>(a, lds, blockIdx.x);
+}
+
 // NST: stages of the ring.  Three, 48 KB, let three workgroups share a compute unit;
 // pieces of at most two steps take no third.
 template <int DT, int NT, int NST>
 __global__ __launch_bounds__(256, 2) void grads_kernel(DeltaArgs a) {
-  __shared__ __attribute__((aligned(16))) char lds[NST * 32 * kDeltaColumnBytes];
+  constexpr int LDS = NST * 32 * kDeltaColumnBytes;
+  __shared__ __attribute__((aligned(16))) char lds[LDS > kDxLds ? LDS : kDxLds];
   constexpr int CB = kDeltaColumnBytes / es(DT);
-  const int jobs = gridDim.x / a.num_parts, part = blockIdx.x / jobs;
+  const int nb = gridDim.x - a.dx_blocks;
+  if ((int)blockIdx.x >= nb) {
+    dx_tile<DT>(a, lds, blockIdx.x - nb);
+    return;
+  }
+  const int jobs = nb / a.num_parts, part = blockIdx.x / jobs;
   int job = blockIdx.x - part * jobs, slot, n, first;
   const int32_t* rec = a.parts + 4 * part;  // (the longest first)
   const int rows = rec[1], tile = rec[2], partial = rec[3];
@@ -828,18 +841,20 @@ int32_t run(DeltaArgs& a, hipStream_t st) {
       hipLaunchKernelGGL(join_kernel<DT>, dim3(a.num_tiles, 2 * a.S, a.padded / 16), dim3(256), 0,
                          st, a);
   }
-  if (a.dx) {
-    const int64_t blocks = (int64_t)(a.num_tiles + a.none_tiles) * a.dx_groups;
-    if (blocks > INT32_MAX) return fail(LORA_E_SHAPE, "too many workgroups");
-    hipLaunchKernelGGL(dx_kernel<DT>, dim3((uint32_t)blocks), dim3(256), 0, st, a);
-  }
-  if (a.dA && a.rows) {
-    const int64_t blocks = a.num_parts * count(kDeltaColumnBytes / es(DT));
-    if (blocks > INT32_MAX) return fail(LORA_E_SHAPE, "too many workgroups");
+  const int64_t grads =
+      a.dA && a.rows ? a.num_parts * count(kDeltaColumnBytes / es(DT)) : 0;
+  const int64_t dx = a.dx ? (int64_t)(a.num_tiles + a.none_tiles) * a.dx_groups : 0;
+  if (grads + dx > INT32_MAX) return fail(LORA_E_SHAPE, "too many workgroups");
+  const bool one = grads && dx;
+  a.dx_blocks = one ? (int32_t)dx : 0;
+  if (dx && !one)
+    hipLaunchKernelGGL(dx_kernel<DT>, dim3((uint32_t)dx), dim3(256), 0, st, a);
+  if (grads) {
+    const dim3 grid((uint32_t)(grads + a.dx_blocks));
     if (a.longest <= 64)
-      hipLaunchKernelGGL((grads_kernel<DT, NT, 2>), dim3((uint32_t)blocks), dim3(256), 0, st, a);
+      hipLaunchKernelGGL((grads_kernel<DT, NT, 2>), grid, dim3(256), 0, st, a);
     else
-      hipLaunchKernelGGL((grads_kernel<DT, NT, 3>), dim3((uint32_t)blocks), dim3(256), 0, st, a);
+      hipLaunchKernelGGL((grads_kernel<DT, NT, 3>), grid, dim3(256), 0, st, a);
   }
   if (a.dA && a.num_multi) {
     const int64_t values = (int64_t)a.R * ((int64_t)a.S * a.K + a.O);
