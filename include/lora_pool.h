@@ -517,14 +517,16 @@ int32_t lora_apply_ranked(const lora_pool_desc* desc, const void* A_pool, const 
  * added to where accumulate is 1; other slots' are never touched.  dx may be
  * dx_in itself (rows without an adapter are then left alone); without dx_in
  * (NULL) dx is the delta's part alone, zero in rows without an adapter.  dx may be
- * NULL (dx_in then too), and dA and dB may be NULL together.
+ * NULL (dx_in then too), and dA and dB may be NULL together.  Other overlaps of dx,
+ * dA, dB or the workspace with any buffer are refused (LORA_E_ARG).
  *
  * lora_delta_backward_plan (host only, deterministic) sorts the rows by adapter
  * and cuts the work; the plan serves every call with this pool's geometry and
  * these ids (the layers of a step).  image: host memory of
  * lora_delta_backward_image_bytes(desc, T) bytes; the caller copies its first
  * plan->image_bytes to the GPU (16-byte aligned).  Errors: LORA_E_ID for an id
- * outside [-1, max_loras), LORA_E_WORKSPACE, LORA_E_ARG, LORA_E_SHAPE for T > 2^21.
+ * outside [-1, max_loras), LORA_E_WORKSPACE, LORA_E_ARG, LORA_E_SHAPE for T > 2^21
+ * (the call's also for in_features > 2^22 or max_lora_rank > 2^16).
  * The kernels skip rows, slots and pieces of the device image that are out of
  * range.  The workspace's size depends on the pool and T alone and does not
  * shrink as T grows. */

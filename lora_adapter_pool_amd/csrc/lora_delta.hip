@@ -32,6 +32,8 @@ using gemm::read_columns;
 using gemm::wait_all_lds;
 
 constexpr int kMaxFeatures = 1 << 22;
+constexpr int kMaxRank = 1 << 16;             // (rank tiles are a grid's z)
+constexpr int64_t kMaxGroups = (1 << 24) - 1;  // of 256 threads: a grid holds under 2^32
 constexpr int kPlanes = 3;       // bf16 pieces of an fp32 value
 
 struct DeltaArgs {
@@ -829,10 +831,15 @@ int32_t run(DeltaArgs& a, hipStream_t st) {
     for (int s = 0; s < a.S; ++s) n += (a.out[s] + width - 1) / width;
     return n * a.blocks;
   };
+  const int64_t jobs = count(a.chunk);
+  const int64_t blocks = (a.num_tiles >= 64 ? (a.num_tiles + 7) & ~7 : a.num_tiles) * jobs;
+  const int64_t grads =
+      a.dA && a.rows ? a.num_parts * count(kDeltaColumnBytes / es(DT)) : 0;
+  const int64_t dx = a.dx ? (int64_t)(a.num_tiles + a.none_tiles) * a.dx_groups : 0;
+  const int64_t values = (int64_t)a.R * ((int64_t)a.S * a.K + a.O);
+  if (blocks > kMaxGroups || grads + dx > kMaxGroups || values / 1024 >= kMaxGroups)
+    return fail(LORA_E_SHAPE, "too many workgroups");
   if (a.rows) {
-    const int64_t jobs = count(a.chunk);
-    const int64_t blocks = (a.num_tiles >= 64 ? (a.num_tiles + 7) & ~7 : a.num_tiles) * jobs;
-    if (blocks > INT32_MAX) return fail(LORA_E_SHAPE, "too many workgroups");
     a.jobs = (int32_t)jobs;
     hipLaunchKernelGGL((ranks_kernel<DT, NT>), dim3((uint32_t)blocks), dim3(256), 0, st, a);
     bool cut = a.K > a.chunk;
@@ -841,10 +848,6 @@ int32_t run(DeltaArgs& a, hipStream_t st) {
       hipLaunchKernelGGL(join_kernel<DT>, dim3(a.num_tiles, 2 * a.S, a.padded / 16), dim3(256), 0,
                          st, a);
   }
-  const int64_t grads =
-      a.dA && a.rows ? a.num_parts * count(kDeltaColumnBytes / es(DT)) : 0;
-  const int64_t dx = a.dx ? (int64_t)(a.num_tiles + a.none_tiles) * a.dx_groups : 0;
-  if (grads + dx > INT32_MAX) return fail(LORA_E_SHAPE, "too many workgroups");
   const bool one = grads && dx;
   a.dx_blocks = one ? (int32_t)dx : 0;
   if (dx && !one)
@@ -857,7 +860,6 @@ int32_t run(DeltaArgs& a, hipStream_t st) {
       hipLaunchKernelGGL((grads_kernel<DT, NT, 3>), grid, dim3(256), 0, st, a);
   }
   if (a.dA && a.num_multi) {
-    const int64_t values = (int64_t)a.R * ((int64_t)a.S * a.K + a.O);
     hipLaunchKernelGGL(sums_kernel, dim3((uint32_t)((values + 1023) / 1024), a.num_multi),
                        dim3(256), 0, st, a);
   }
@@ -884,8 +886,9 @@ extern "C" int32_t lora_delta_backward(const lora_pool_desc* desc, const void* A
     return fail(LORA_E_ARG, "accumulate must be 0 or 1, got %d", accumulate);
   if (T == 0) return LORA_OK;
   // (offsets inside 64 ranks' rows of A have 32 bits)
-  if (g.K > kMaxFeatures || g.R > kMaxFeatures)
-    return fail(LORA_E_SHAPE, "in_features and max_lora_rank must be at most %d", kMaxFeatures);
+  if (g.K > kMaxFeatures || g.R > kMaxRank)
+    return fail(LORA_E_SHAPE, "in_features and max_lora_rank must be at most %d and %d",
+                kMaxFeatures, kMaxRank);
   if (int32_t e = delta_check_plan(g, T, plan)) return e;
   if (!A_pool || !B_pool || !x || !dy || !image)
     return fail(LORA_E_ARG, "A_pool, B_pool, x, dy and image must not be NULL");
@@ -901,6 +904,20 @@ extern "C" int32_t lora_delta_backward(const lora_pool_desc* desc, const void* A
   const void* ptrs[] = {A_pool, B_pool, x, dy, dx_in, dx, dA, dB, image, ws};
   for (const void* p : ptrs)
     if (!aligned16(p)) return fail(LORA_E_ALIGN, "every buffer must be 16-byte aligned");
+  // Later launches read x, dy and the pools again, so that nothing may be written over them.
+  const int64_t e = elem_bytes(g.dtype), of_a = (int64_t)g.max_loras * g.S * g.R * g.K,
+                of_b = (int64_t)g.max_loras * g.O * g.R;
+  const int64_t sizes[] = {of_a * e,      of_b * e,      T * (int64_t)g.K * e, T * (int64_t)g.O * e,
+                           T * (int64_t)g.K * e, T * (int64_t)g.K * e, of_a * 4, of_b * 4,
+                           plan->image_bytes,    l.total};
+  constexpr int kDxIn = 4, kDx = 5, kDA = 6, kDB = 7, kWs = 9;
+  for (int i : {kDx, kDA, kDB, kWs})
+    for (int j = 0; j <= kWs; ++j) {
+      if (i == j || !ptrs[i] || !ptrs[j] || (i == kDx && j == kDxIn && dx == dx_in)) continue;
+      const uintptr_t p = (uintptr_t)ptrs[i], q = (uintptr_t)ptrs[j];
+      if (p < q + (uint64_t)sizes[j] && q < p + (uint64_t)sizes[i])
+        return fail(LORA_E_ARG, "an output or the workspace overlaps another buffer");
+    }
 
   const DeltaRanks r = delta_ranks(g.R);
   const int32_t* im = (const int32_t*)image;

@@ -129,3 +129,24 @@ def test_call_refusals():
     assert status(L.lora_delta_backward, *none) == _lib.LORA_E_ARG    # nothing to compute
     empty, _ = L.lora_delta_backward_plan(desc, [])
     assert status(L.lora_delta_backward, desc, *[None] * 8, 0, empty, None, 0, None, 0) == 0
+
+
+def test_overlaps_and_limits():
+    """dx is dx_in or apart; nothing else that is written overlaps a buffer."""
+    desc = L.make_desc("bf16", 4, 16, 256, [256])
+    plan, _ = L.lora_delta_backward_plan(desc, [0, 1, -1, 3, 0])
+    need = L.lora_delta_backward_workspace_bytes(desc, 5)
+    apart = [(i + 1) << 30 for i in range(10)]   # A, B, x, dy, dx_in, dx, dA, dB, image, ws
+
+    def call(at, d=desc, p=plan):
+        return status(L.lora_delta_backward, d, *at[:8], 5, p, at[8], 0, at[9], need)
+
+    x_bytes = 5 * 256 * 2
+    for i, j, shift in ((5, 2, 0), (5, 3, 16), (5, 4, 512), (5, 4, -x_bytes + 16), (6, 7, 0),
+                        (6, 0, 0), (7, 1, 0), (9, 8, 0), (9, 2, x_bytes - 16), (8, 9, need - 16)):
+        at = list(apart)
+        at[i] = apart[j] + shift
+        assert call(at) == _lib.LORA_E_ARG, (i, j)
+    tall = L.make_desc("bf16", 1, (1 << 16) + 8, 64, [64])
+    p, _ = L.lora_delta_backward_plan(tall, [0] * 5)
+    assert call(apart, tall, p) == _lib.LORA_E_SHAPE
