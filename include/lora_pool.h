@@ -742,7 +742,8 @@ int32_t lora_block_norm_backward(const lora_block_norm_desc* desc, const void* d
  * bytes, to the GPU (16-byte aligned) and keeps the tensors.  Tensors are contiguous
  * device memory of any size, aligned to their elements; out NULL is in place.
  * Errors: LORA_E_ARG where two of the list's arrays overlap (out == grad apart),
- * LORA_E_ID for a group outside [0, groups), LORA_E_DTYPE, LORA_E_SHAPE,
+ * LORA_E_ID for a group outside [0, groups), LORA_E_DTYPE, LORA_E_SHAPE (more than
+ * 2^20 groups, or 2^24 - 1 chunks of at most 32768 elements of one tensor),
  * LORA_E_ALIGN, LORA_E_WORKSPACE. */
 typedef struct {
   void* grad;

@@ -29,7 +29,7 @@ constexpr int kStep = kThreads * 8;      // elements a pass of a workgroup
 constexpr int64_t kMinChunk = kStep, kMaxChunk = 16 * kStep;
 constexpr int64_t kAimChunks = 2048;     // eight a compute unit
 constexpr int32_t kMaxGroups = 1 << 20;
-constexpr int64_t kMaxChunks = 1 << 26;
+constexpr int64_t kMaxChunks = (1 << 24) - 1;  // a grid holds under 2^32 threads
 // most chunks of a group whose partials every workgroup adds by itself
 constexpr int kOwnSums = 512;
 
@@ -154,6 +154,9 @@ int32_t check_grads(const lora_grad* g, int32_t n, int32_t groups, int64_t* chun
     if (((uintptr_t)g[i].grad | (uintptr_t)g[i].out) & mask)
       return fail(LORA_E_ALIGN, "tensor %d is not aligned to its elements", i);
     total += g[i].count;
+    if (total > kMaxChunks * kMaxChunk)
+      return fail(LORA_E_SHAPE, "the tensors hold more than %lld elements",
+                  (long long)(kMaxChunks * kMaxChunk));
   }
   *size = chunk_size(total);
   *chunks = 0;

@@ -119,3 +119,17 @@ def test_tensors_that_a_list_refuses():
         with pytest.raises(L.LoraError) as e:
             L.GradList(a, **k)
         assert e.value.status == want
+
+
+def test_lists_past_a_grids_limit():
+    """A workgroup of 256 threads a chunk, and a grid holds less than 2^32 threads."""
+    lib = L.lib()
+
+    def size(counts):
+        a = entries([(FAKE + (i << 48), 0, n, 1, 0) for i, n in enumerate(counts)])
+        return lib.lora_grad_list_bytes(a.ctypes.data, len(a), 1)
+
+    most = ((1 << 24) - 1) * 32768
+    assert size([most]) == 32 * ((1 << 24) - 1) + 32
+    assert size([most, 1]) == size([most + 1]) == size([1 << 40] * 9) == _lib.LORA_E_SHAPE
+    assert size([most - 1, 1]) == _lib.LORA_E_SHAPE      # two chunks that are not full
