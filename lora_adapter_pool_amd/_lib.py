@@ -741,7 +741,7 @@ class GradList:
     """The tensors of lora_clip_grads, cut into chunks once: contiguous fp32 or bf16
     tensors of one GPU, the group of each (default: one group of all), and where the
     clipped gradients go (outs, or an entry of it, None: in place).  It keeps the
-    tensors and the list's image on their GPU."""
+    tensors and the list's image on their GPU; their memory is read where it was then."""
 
     def __init__(self, tensors, groups=None, outs=None, num_groups: Optional[int] = None):
         import torch
@@ -772,7 +772,8 @@ class GradList:
         self.tensors, self.outs = tensors, outs
         self.num_groups = max(groups) + 1 if num_groups is None else int(num_groups)
         self.struct, image = lora_grad_list_build(grads, self.num_groups)
-        self.image = torch.from_numpy(image).to(tensors[0].device)
+        self.device = tensors[0].device
+        self.image = torch.from_numpy(image).to(self.device)
 
 
 def lora_clip_grads_workspace_bytes(grads) -> int:
@@ -780,6 +781,21 @@ def lora_clip_grads_workspace_bytes(grads) -> int:
 
 
 def lora_clip_grads(grads, max_norm: float, norms, ws, ws_bytes, stream=None) -> None:
-    """norms[g]: fp32 norm of group g's tensors; each tensor times min(1, max_norm / norm)."""
+    """norms[g]: fp32 norm of group g's tensors; each tensor times min(1, max_norm / norm).
+    stream None: the current stream of the tensors' GPU, whichever GPU is the current one."""
+    device = getattr(grads, "device", None)
+    if device is not None:
+        import torch
+
+        for t in (norms, ws):
+            if isinstance(t, torch.Tensor) and t.device != device:
+                raise LoraError(LORA_E_ARG, "norms and the workspace must be on the tensors' GPU")
+        if device.index != torch.cuda.current_device():
+            with torch.cuda.device(device):
+                return _clip_grads(grads, max_norm, norms, ws, ws_bytes, stream)
+    _clip_grads(grads, max_norm, norms, ws, ws_bytes, stream)
+
+
+def _clip_grads(grads, max_norm, norms, ws, ws_bytes, stream) -> None:
     _check(pycall().clip_grads(entry_address("lora_clip_grads"), ctypes.addressof(grads.struct),
                                grads.image, max_norm, norms, ws, ws_bytes, _stream(stream)))

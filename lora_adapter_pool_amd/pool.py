@@ -99,34 +99,28 @@ class LoraPool:
         dx [T, K] = dx_in (the base projection's part; None: zeros) + the delta's; it may be
         dx_in itself.  dA, dB: fp32 gradients of A_view() and B_view(), overwritten or added to
         (accumulate) for the batch's slots, others left; new ones are zeros.  peft's lora_B has
-        the adapter's scale times dB's gradient."""
+        the adapter's scale times dB's gradient.  A pool's calls share a workspace: two that run
+        at once, or graphs of them, need pools of their own."""
         torch = self.torch
         if not self.A.is_cuda:
             raise L.LoraError(L.LORA_E_ARG, "the pool is not on a GPU")
         if not need_dx and not need_grads:
             raise L.LoraError(L.LORA_E_ARG, "neither dx nor the adapters' gradients are wanted")
+        if plan.image.device != self.A.device:
+            raise L.LoraError(L.LORA_E_ARG, "the plan is not on the pool's GPU")
         T, S = plan.T, len(self.out_features)
         want = {"x": (x, (T, self.K), self.tdtype), "dy": (dy, (T, self.O), self.tdtype),
-                "dx_in": (dx_in, (T, self.K), self.tdtype), "dx": (dx, (T, self.K), self.tdtype),
-                "dA": (dA, (self.max_loras, S, self.R, self.K), torch.float32),
-                "dB": (dB, (self.max_loras, self.O, self.R), torch.float32)}
-        for name, (t, shape, dtype) in want.items():
-            if t is None:
-                continue
-            if t.dtype != dtype or t.device != self.A.device:
-                raise L.LoraError(L.LORA_E_DTYPE, f"{name} must be {dtype} on the pool's GPU")
-            if tuple(t.shape) != shape or not t.is_contiguous():
-                raise L.LoraError(L.LORA_E_SHAPE, f"{name} must be a contiguous {list(shape)}")
+                "dx_in": (dx_in, (T, self.K), self.tdtype), "dx": (dx, (T, self.K), self.tdtype)}
+        self._check_tensors(want)
         if not need_dx and (dx is not None or dx_in is not None):
             raise L.LoraError(L.LORA_E_ARG, "dx is given and not wanted")
         if not need_grads and (dA is not None or dB is not None):
             raise L.LoraError(L.LORA_E_ARG, "dA or dB is given and not wanted")
-        if (dA is None) != (dB is None):
-            raise L.LoraError(L.LORA_E_ARG, "dA and dB go together: one of them is None")
+        self.check_grads(dA, dB)
         with torch.cuda.device(self.A.device):
             if need_grads and dA is None:
-                dA = torch.zeros(want["dA"][1], device=self.A.device)
-                dB = torch.zeros(want["dB"][1], device=self.A.device)
+                dA = torch.zeros((self.max_loras, S, self.R, self.K), device=self.A.device)
+                dB = torch.zeros((self.max_loras, self.O, self.R), device=self.A.device)
             if need_dx and dx is None:
                 dx = torch.empty_like(x)
             ws = self._backward_workspace(T)
@@ -134,6 +128,25 @@ class LoraPool:
                 L.lora_delta_backward(self.desc, self.A, self.B, x, dy, dx_in, dx, dA, dB, T,
                                       plan.struct, plan.image, accumulate, ws, ws.numel())
         return dx, dA, dB
+
+    def check_grads(self, dA, dB) -> None:
+        """Refuses what backward cannot take as dA and dB (both None: new ones)."""
+        if (dA is None) != (dB is None):
+            raise L.LoraError(L.LORA_E_ARG, "dA and dB go together: one of them is None")
+        f32 = self.torch.float32
+        self._check_tensors({
+            "dA": (dA, (self.max_loras, len(self.out_features), self.R, self.K), f32),
+            "dB": (dB, (self.max_loras, self.O, self.R), f32)})
+
+    def _check_tensors(self, want) -> None:
+        """{name: (tensor or None, shape, dtype)}: contiguous and on the pool's GPU."""
+        for name, (t, shape, dtype) in want.items():
+            if t is None:
+                continue
+            if t.dtype != dtype or t.device != self.A.device:
+                raise L.LoraError(L.LORA_E_DTYPE, f"{name} must be {dtype} on the pool's GPU")
+            if tuple(t.shape) != shape or not t.is_contiguous():
+                raise L.LoraError(L.LORA_E_SHAPE, f"{name} must be a contiguous {list(shape)}")
 
     def _backward_workspace(self, T: int):
         need = L.lora_delta_backward_workspace_bytes(self.desc, T)
@@ -148,7 +161,13 @@ class LoraPool:
     def slot_grads(self, dA, dB, slots, outs=None) -> L.GradList:
         """The gradients of some slots as lora_clip_grads takes them, a group for each slot in
         turn; outs: (dA, dB) that the clipped gradients go to (None: in place)."""
-        pick = lambda a, b: [t[int(k)] for k in slots for t in (a, b)]  # noqa: E731
+        for pair in (dA, dB), outs or (None, None):
+            self.check_grads(*pair)
+        slots = [int(k) for k in slots]
+        for k in slots:
+            if not 0 <= k < self.max_loras:
+                raise L.LoraError(L.LORA_E_ID, f"slot {k} of {self.max_loras}")
+        pick = lambda a, b: [t[k] for k in slots for t in (a, b)]  # noqa: E731
         return L.GradList(pick(dA, dB), [g for g in range(len(slots)) for _ in range(2)],
                           None if outs is None else pick(*outs), num_groups=len(slots))
 

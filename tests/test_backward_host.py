@@ -55,3 +55,15 @@ def test_forms_of_the_block():
     assert (d.gate, d.residual_scale, d.block_scale) == (0, 0.5, 1.0)
     d = L.LoraMlp(*w, gate=torch.ones(64), block_scale=2.0).join_desc
     assert (d.gate, d.residual_scale, d.block_scale) == (1, 1.0, 2.0)
+
+
+def test_slots_of_a_list():
+    pool = L.LoraPool("bf16", 2, 8, 64, [72], device="cpu")
+    dA, dB = torch.zeros(pool.A_view().shape), torch.zeros(pool.B_view().shape)
+    for slots in ([-1], [2], [0, 5]):
+        refused(_lib.LORA_E_ID, pool.slot_grads, dA, dB, slots)
+    refused(_lib.LORA_E_SHAPE, pool.slot_grads, dA[:1], dB, [0])
+    refused(_lib.LORA_E_SHAPE, pool.slot_grads, dA, dB, [0], (dA, dB[:, :8]))
+    refused(_lib.LORA_E_DTYPE, pool.slot_grads, dA.bfloat16(), dB, [0])
+    refused(_lib.LORA_E_ARG, pool.slot_grads, dA, None, [0])
+    refused(_lib.LORA_E_ARG, pool.slot_grads, dA, dB, [])

@@ -133,3 +133,32 @@ def test_lists_past_a_grids_limit():
     assert size([most]) == 32 * ((1 << 24) - 1) + 32
     assert size([most, 1]) == size([most + 1]) == size([1 << 40] * 9) == _lib.LORA_E_SHAPE
     assert size([most - 1, 1]) == _lib.LORA_E_SHAPE      # two chunks that are not full
+
+
+def test_a_lists_gpu(monkeypatch):
+    """A list is clipped on its tensors' GPU, whichever is the current one."""
+    lst, _ = L.lora_grad_list_build(entries([(FAKE, 0, 100, 0, 0)]), 1)
+    now, calls = [0], []
+
+    class On:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.device.index
+
+        def __exit__(self, *_):
+            now[0] = self.before
+
+    class Grads:
+        struct, image, device = lst, FAKE, torch.device("cuda", 1)
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", On)
+    monkeypatch.setattr(_lib, "_clip_grads", lambda *a: calls.append(now[0]))
+    L.lora_clip_grads(Grads, 1.0, FAKE, FAKE, 1 << 20)
+    now[0] = 1
+    L.lora_clip_grads(Grads, 1.0, FAKE, FAKE, 1 << 20)
+    assert calls == [1, 1] and now == [1]
+    with pytest.raises(L.LoraError):                  # the norms lie elsewhere
+        L.lora_clip_grads(Grads, 1.0, torch.zeros(4), FAKE, 1 << 20)
