@@ -165,8 +165,10 @@ class LoraMlp:
             L.lora_block_norm(self.join_desc, block, s, self.gate, self.post_norm_weight, None, y,
                               None, None, None, T)
         self._saved = (n, pre) if keep else None
-        kept = None if ids is None else np.array(ids, dtype=np.int32)
-        self._saved_rest = (s, h, block, kept) if keep else None
+        self._saved_rest = None
+        if keep:
+            kept = None if ids is None else np.array(ids, dtype=np.int32)
+            self._saved_rest = (s, h, block, kept)
         return y
 
     def _delta(self, pool, x, ids, prefill, width):
@@ -202,14 +204,17 @@ class LoraMlp:
                                   dpre, dn, dw, T, ws, ws.numel())
         return dpre, dn, dw
 
-    def backward(self, dy, w_down_t, need_dw: bool = False, grads=None, accumulate: bool = False):
+    def backward(self, dy, w_down_t, need_dw: bool = False, grads=None, accumulate: bool = False,
+                 plans=None):
         """Gradients of the kept forward pass from dy [T][H], the gradient of y, as a dict:
         "x" (also residual's), "norm_weight" (fp32, as the next two), "post_norm_weight", "gate",
         "gate_up" and "down" ((dA, dB) of the pools, as LoraPool.backward gives them) and
         "w_gate_up" (need_dw).  w_down_t: w_down transposed, [I][H]; the base is frozen in this
         pass, so that a program makes it once.  grads: buffers for the fp32 sums by these names,
-        which accumulate adds to; new ones are made for the others.  Weights must not be in
-        e4m3.  Takes the kept pass with it."""
+        which accumulate adds to; new ones are made for the others.  plans: the pools'
+        backward_plan of the kept ids by "gate_up" and "down", where a program makes them once for
+        a step's layers or captures the pass; made here otherwise, which waits for the GPU.
+        Weights must not be in e4m3.  Takes the kept pass with it."""
         if self._saved is None:
             raise L.LoraError(L.LORA_E_ARG, "no forward pass was kept (keep=True)")
         if self.eight:
@@ -221,20 +226,39 @@ class LoraMlp:
             raise L.LoraError(L.LORA_E_SHAPE, "w_down_t must be a contiguous [I, H]")
         if w_down_t.dtype != self.w_down.dtype or w_down_t.device != self.w_down.device:
             raise L.LoraError(L.LORA_E_DTYPE, "w_down_t must have w_down's dtype and device")
-        grads = dict(grads or {})
-        names = {"norm_weight", "post_norm_weight", "gate", "gate_up", "down"}
-        if set(grads) - names:
-            raise L.LoraError(L.LORA_E_ARG, f"unknown gradients {sorted(set(grads) - names)}")
+        grads = {k: v for k, v in (grads or {}).items() if v is not None}
+        plans = dict(plans or {})
+        pools = {k: p for k, p in (("gate_up", self.gate_up), ("down", self.down)) if p is not None}
+        rows = {"norm_weight": self.norm_weight, "post_norm_weight": self.post_norm_weight,
+                "gate": self.gate}
+        rows = {k for k, v in rows.items() if v is not None}
         for k in ("norm_weight", "post_norm_weight", "gate"):
             t = grads.get(k)
             if t is not None and (t.dtype != self.torch.float32 or tuple(t.shape) != (self.H,) or
                                   not t.is_contiguous() or t.device != self.w_down.device):
                 raise L.LoraError(L.LORA_E_SHAPE, f"the gradient of {k} must be fp32 [H]")
-        return self._on_device(self._backward, dy, w_down_t, need_dw, grads, accumulate)
+        for what, given, names in (("gradients", grads, rows | set(pools)),
+                                   ("plans", plans, set(pools))):
+            if set(given) - names:
+                raise L.LoraError(L.LORA_E_ARG, f"{what} of {sorted(set(given) - names)}, which "
+                                                "the block does not have")
+        for k in set(grads) & set(pools):
+            pools[k].check_grads(*grads[k])
+        ids = self._saved_rest[3]
+        for k, pool in pools.items():
+            if ids is None:
+                plans.pop(k, None)
+                continue
+            if k not in plans:
+                if dy.is_cuda and self.torch.cuda.is_current_stream_capturing():
+                    raise L.LoraError(L.LORA_E_ARG, "a captured pass takes its plans from outside")
+                plans[k] = pool.backward_plan(ids)
+            pool.check_plan(plans[k], dy.shape[0])
+        return self._on_device(self._backward, dy, w_down_t, need_dw, grads, accumulate, plans)
 
-    def _backward(self, dy, w_down_t, need_dw, grads, accumulate):
+    def _backward(self, dy, w_down_t, need_dw, grads, accumulate, plans):
         torch = self.torch
-        (n, pre), (s, h, block, ids) = self._saved, self._saved_rest
+        (n, pre), (s, h, block, _) = self._saved, self._saved_rest
         T, out = int(dy.shape[0]), {}
         row = lambda k: (grads[k] if k in grads else  # noqa: E731
                          torch.zeros(self.H, device=dy.device))
@@ -245,11 +269,11 @@ class LoraMlp:
 
         def adapters(name, pool, x, d, dx):
             """dx += the adapters' part; their gradients."""
-            if pool is None or ids is None:
+            if name not in plans:
                 return
             dA, dB = grads.get(name, (None, None))
-            plan = pool.backward_plan(ids)
-            out[name] = pool.backward(x, d, plan, dx, dx, dA, dB, accumulate=accumulate)[1:]
+            out[name] = pool.backward(x, d, plans[name], dx, dx, dA, dB,
+                                      accumulate=accumulate)[1:]
 
         ds, db = dy, dy     # gradients of s and of the block's output
         if self.join_desc is not None:

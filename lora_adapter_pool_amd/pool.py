@@ -27,6 +27,7 @@ class DeltaPlan:
 
         self.struct, image = L.lora_delta_backward_plan(desc, ids)
         self.T = self.struct.rows + self.struct.none
+        self.geometry = bytes(desc)
         self.image = torch.from_numpy(image).to(device)
 
 
@@ -106,9 +107,8 @@ class LoraPool:
             raise L.LoraError(L.LORA_E_ARG, "the pool is not on a GPU")
         if not need_dx and not need_grads:
             raise L.LoraError(L.LORA_E_ARG, "neither dx nor the adapters' gradients are wanted")
-        if plan.image.device != self.A.device:
-            raise L.LoraError(L.LORA_E_ARG, "the plan is not on the pool's GPU")
         T, S = plan.T, len(self.out_features)
+        self.check_plan(plan, T)
         want = {"x": (x, (T, self.K), self.tdtype), "dy": (dy, (T, self.O), self.tdtype),
                 "dx_in": (dx_in, (T, self.K), self.tdtype), "dx": (dx, (T, self.K), self.tdtype)}
         self._check_tensors(want)
@@ -128,6 +128,13 @@ class LoraPool:
                 L.lora_delta_backward(self.desc, self.A, self.B, x, dy, dx_in, dx, dA, dB, T,
                                       plan.struct, plan.image, accumulate, ws, ws.numel())
         return dx, dA, dB
+
+    def check_plan(self, plan: DeltaPlan, T: int) -> None:
+        """Refuses a plan of other rows, another geometry or another GPU."""
+        if plan.T != T or plan.geometry != bytes(self.desc):
+            raise L.LoraError(L.LORA_E_ARG, "the plan is not of these rows and this pool's geometry")
+        if plan.image.device != self.A.device:
+            raise L.LoraError(L.LORA_E_ARG, "the plan is not on the pool's GPU")
 
     def check_grads(self, dA, dB) -> None:
         """Refuses what backward cannot take as dA and dB (both None: new ones)."""

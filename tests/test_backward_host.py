@@ -67,3 +67,41 @@ def test_slots_of_a_list():
     refused(_lib.LORA_E_DTYPE, pool.slot_grads, dA.bfloat16(), dB, [0])
     refused(_lib.LORA_E_ARG, pool.slot_grads, dA, None, [0])
     refused(_lib.LORA_E_ARG, pool.slot_grads, dA, dB, [])
+
+
+def test_a_block_refuses_before_it_adds():
+    """Gradients and plans that do not fit are refused while nothing has been added to."""
+    w = [torch.ones(64), torch.zeros(144, 64), torch.zeros(64, 72)]
+    pools = [L.LoraPool("f32", 2, 8, 64, [72, 72], device="cpu"),
+             L.LoraPool("f32", 2, 8, 72, [64], device="cpu")]
+    m = L.LoraMlp(*w, gate_up=pools[0], down=pools[1], gate=torch.ones(64))
+    dy, wt, ids = torch.zeros(4, 64), torch.zeros(72, 64), np.array([0, 1, -1, 0], np.int32)
+    m._saved, m._saved_rest = (dy, torch.zeros(4, 144)), (dy, dy, dy, ids)
+    pair = [torch.zeros(p.A_view().shape) for p in pools]
+    for grads in ({"post_norm_weight": torch.zeros(64)},                  # the block has none
+                  {"gate_up": (pair[0], None)}, {"down": (pair[0], pair[1])},
+                  {"norm_weight": torch.zeros(72)}):
+        with pytest.raises(L.LoraError):
+            m.backward(dy, wt, grads=grads)
+    for plans in ({"norm_weight": None}, {"down": pools[0].backward_plan(ids)},
+                  {"down": pools[1].backward_plan(ids[:3])}):
+        refused(_lib.LORA_E_ARG, m.backward, dy, wt, plans=plans)
+    assert m._saved is not None and m._saved_rest is not None
+
+
+def test_only_a_kept_pass_copies_its_ids():
+    class Ids:
+        def __array__(self, *a, **k):
+            raise AssertionError("copied")
+
+    m = L.LoraMlp(torch.ones(64), torch.zeros(144, 64), torch.zeros(64, 72))
+    m._workspace = lambda need: torch.zeros(1)
+    x = torch.zeros(3, 64)
+    names = ("lora_add_rms_norm", "lora_gated_ffn", "lora_linear")
+    with pytest.MonkeyPatch.context() as patch:
+        for name in names:
+            patch.setattr(_lib, name, lambda *a, **k: None)
+        m._forward(x, x, Ids(), None, False)
+        assert m._saved_rest is None
+        m._forward(x, x, [0, 1, 0], None, True)
+        assert m._saved_rest[3].tolist() == [0, 1, 0]

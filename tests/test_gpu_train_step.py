@@ -206,3 +206,34 @@ def test_captured_step():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((dx, dA, dB, norms), want)), k
+
+
+def test_plans_from_outside_and_a_captured_pass():
+    """The block's backward pass with plans made once: eager, and replayed from a graph."""
+    mlp, w, pools, ids, x, residual, dy = make("bf16", 12, 150, True)
+    wt = w["down"].t().contiguous()
+    plans = {k: p.backward_plan(ids) for k, p in zip(("gate_up", "down"), pools)}
+    mlp.forward(x, residual, ids, np.ones(150, np.uint8), keep=True)
+    kept = mlp._saved, mlp._saved_rest
+    want = flat(mlp.backward(dy, wt))
+
+    def step():
+        mlp._saved, mlp._saved_rest = kept
+        return flat(mlp.backward(dy, wt, plans=plans))
+
+    got = step()
+    assert set(got) == set(want) and all(torch.equal(got[k], want[k]) for k in want)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mlp._saved, mlp._saved_rest = kept
+        with pytest.raises(L.LoraError):
+            mlp.backward(dy, wt)
+        out = step()
+    for k in range(3):
+        dy.normal_()
+        want = {name: t.clone() for name, t in step().items()}
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(out[name], want[name]) for name in want), k
