@@ -1,7 +1,8 @@
 """The feed-forward half of a decoder layer with adapters, on one GPU: a mixed
 batch of prefill and decode rows through norm, gate/up, activation and down, each
 row with its own adapter or none; then the gate/up gradients of the same pass;
-then the same layer with its gate/up weights in 8 bits.
+then one training step's gradients of the adapters, clipped slot by slot; then the
+same layer with its gate/up weights in 8 bits.
 
     python examples/mlp_block.py [--hidden 1024 --inter 2816 --rows 300]
 """
@@ -47,6 +48,17 @@ def main():
     y = mlp.forward(x, residual, ids, prefill, keep=True)
     dpre, dn, dw = mlp.gate_up_backward((normal(T, I) * 0.1).bfloat16())
     print("y", tuple(y.shape), "dn", tuple(dn.shape), "dW", tuple(dw.shape))
+
+    dy, w_down_t = (normal(T, H) * 0.1).bfloat16(), w_down.t().contiguous()
+    out = mlp.backward(dy, w_down_t)
+    for name, pool in (("gate_up", gate_up), ("down", down)):
+        grads = pool.slot_grads(*out[name], range(pool.max_loras))
+        need = L.lora_clip_grads_workspace_bytes(grads)
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        norms = torch.empty(pool.max_loras, device="cuda")
+        L.lora_clip_grads(grads, 1.0, norms, ws, need)
+        print(f"{name}: gradient norms of the slots before clipping to 1", norms.tolist())
+    print("dx", tuple(out["x"].shape), "dnorm", tuple(out["norm_weight"].shape))
 
     scale = (w_gate_up.float().abs().amax(1) / 448).clamp_min(2.0 ** -126)
     w8 = (w_gate_up.float() / scale[:, None]).to(torch.float8_e4m3fn)

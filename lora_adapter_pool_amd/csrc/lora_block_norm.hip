@@ -22,6 +22,11 @@
 // anyhow, so that the forward pass keeps nothing else.  A workgroup takes every
 // n-th row and keeps the columns' sums in registers; their partials are added in
 // a second launch, in an order that depends on the sizes alone.
+//
+// Measured (us, bf16): 8960 x 4096 with an element gate and 8-bit output 71, 5.6 TB/s;
+// its gradients with a channel gate 101 to 115 by the card (4.1 TB/s; vector units are
+// busy half of the cycles, and a row waits for two reductions), 5 of it the sums'
+// launch.  64 rows 4.2, a launch's time.
 #include <hip/hip_runtime.h>
 
 #include "lora_norm.h"
@@ -32,7 +37,8 @@ namespace {
 
 constexpr int kMaxHidden = 16384;
 constexpr int kForwardThreads = 1024, kBackwardThreads = 512;
-// workgroups that keep sums over rows, two a compute unit
+// workgroups that keep sums over rows, two a compute unit (8960 x 4096 before the next row
+// was fetched ahead: 132 us; with 256 workgroups 186, with 1024 133 to 138)
 constexpr int kSumGroups = 512;
 
 struct JoinArgs {
@@ -301,8 +307,9 @@ struct BackRow {
 template <int DT, int NP, bool kPre, bool kPost, bool kGate>
 __global__ __launch_bounds__(kBackwardThreads, DT == LORA_BF16 && NP == 1 ? 4 : 2)
 void join_backward_kernel(BackArgs a) {
-  // One piece a thread: the next row's is fetched while this one is worked on.  Four pieces leave no registers to hold a row over the reductions: it
-  // is read again, from the caches.
+  // One piece a thread: the next row's is fetched while this one is worked on.  Four
+  // pieces leave no registers to hold a row over the reductions: it is read again, from
+  // the caches.
   constexpr bool kAhead = NP == 1;
   constexpr uint32_t ES = DT == LORA_F32 ? 4 : 2;
   constexpr int kHeld = NP < 4 ? NP : 1;
@@ -495,7 +502,7 @@ void join_backward_kernel(BackArgs a) {
 }
 
 // The partials' sums.  A workgroup takes 64 columns of one kind; its 16 waves
-// take every 16th partial.
+// take every 16th partial.  25 MB of partials for 4096 columns of three kinds: 5.2 us.
 struct SumArgs {
   const float* part;
   float* to[3];

@@ -30,7 +30,9 @@ constexpr int64_t kMinChunk = kStep, kMaxChunk = 16 * kStep;
 constexpr int64_t kAimChunks = 2048;     // eight a compute unit
 constexpr int32_t kMaxGroups = 1 << 20;
 constexpr int64_t kMaxChunks = (1 << 24) - 1;  // a grid holds under 2^32 threads
-// most chunks of a group whose partials every workgroup adds by itself
+// most chunks of a group whose partials every workgroup adds by itself: 0.5 to 1.3 us in
+// the second pass where a launch between the two takes 2 to 4.6 (128 tensors in 64
+// groups); for 7869 chunks 210 us where the launch (5) leaves it at 179
 constexpr int kOwnSums = 512;
 
 struct Chunk {

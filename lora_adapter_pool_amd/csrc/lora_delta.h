@@ -9,7 +9,10 @@ namespace lora {
 constexpr int kDeltaTileRows = 64;      // rows of a shrink's or a dx's workgroup
 constexpr int kDeltaColumnBytes = 512;  // columns of a gradient's workgroup, in stored bytes
 constexpr int64_t kDeltaAim = 512;      // workgroups of the gradients, two a compute unit
-constexpr int64_t kDeltaShrinks = 1024;  // workgroups of the ranks, four a compute unit
+// Workgroups of the ranks, four a compute unit: 53 us and a join of 9.5 for 8704 x 4096 x
+// 4096 of 64 ranks; two a unit 56 and 7, reductions never cut 66 (gate/up: 235, and 190 with
+// 7 for the join).
+constexpr int64_t kDeltaShrinks = 1024;
 constexpr int kDeltaMaxSplits = 8;
 
 // Rank tiles of 16 in a rank block, rank blocks, and the ranks they pad to.

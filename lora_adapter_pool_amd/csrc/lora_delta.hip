@@ -5,15 +5,23 @@
 //   1 ranks  u and v of 64-row tiles (reductions over out and in features, cut
 //            into parts where tiles are few)
 //   2 join   adds the parts, where there are any
-//   3 dx     of 64-row tiles by 256 bytes of columns
-//   4 grads  dA and dB of a piece of an adapter's rows by 512 bytes of columns
+//   3 dx     of 64-row tiles by 256 bytes of columns, and
+//   4 grads  dA and dB of a piece of an adapter's rows by 512 bytes of columns, in
+//            one launch where both are wanted: they read the same rank space, and
+//            the end of one fills with the other (8704 x 4096 x 4096 168 -> 152 us,
+//            32 rows 13.3 -> 9.9)
 //   5 sums   adds the partials of adapters whose rows were cut
 //
 // Every product is MFMA (16x16x32 bf16, 16x16x4 fp32).  The ranks are at most a
 // few hundred, so that every product is bound by memory: x and dy are read twice
 // (once for the ranks, once for the gradients), dx once in and out.  A bf16
 // pool's u and v are held as sums of three bf16 values (24 bits): one product with
-// fp32 operands is three with bf16 ones, which the loads hide.
+// fp32 operands is three with bf16 ones, which the loads hide (matrix units are busy
+// 18 to 24% of the cycles).
+//
+// Measured (us, bf16, 64 ranks): 8704 x 4096 x 4096 of 16 adapters 140 (floor of
+// its 335 MB at a copy's rate 65), 8960 x 4096 x 2 x 14336 of 28 adapters 453 (230);
+// 256 x 4096 x 6144 of 43 adapters of 16 ranks 46 (17); 32 rows fp32 9.5.
 #include <hip/hip_runtime.h>
 
 #include "lora_delta.h"
@@ -63,7 +71,6 @@ struct DeltaArgs {
   int32_t padded, blocks;
   int32_t chunk;
   int32_t accumulate;
-  int32_t jobs;       // workgroups of the ranks for one tile
   int32_t dx_groups;  // of dx for one tile
   int32_t dx_blocks;  // of dx in the gradients' launch
   int32_t out[LORA_MAX_SLICES], off[LORA_MAX_SLICES];
@@ -249,7 +256,10 @@ __device__ __forceinline__ void finish_ranks(const DeltaArgs& a, const float* su
 // multiplies all rows with all ranks of the block, and the waves' sums meet in LDS at
 // the end.  So nothing waits for another wave on the way: x or dy comes straight to
 // registers, two steps ahead, and A or B through the wave's own part of LDS (B is
-// read as columns there).
+// read as columns there).  8704 x 4096 x 4096: 53 us, 3.4 TB/s; 2 x 14336 out features:
+// 196 us, 3.9 TB/s.  Bound by what a compute unit pulls: the weights' block of each
+// 64 rows is as many bytes as the rows.  (Rings that the waves share, three and eight
+// steps deep, with their barriers: the same; larger tiles leave units idle.)
 template <int DT, int NT>
 constexpr int ranks_lds() {
   const int ring = 4 * 2 * 16 * NT * 128, sums = 4 * 64 * (16 * NT + 4) * 4;
@@ -455,20 +465,11 @@ __device__ __forceinline__ bool take_tile(const DeltaArgs& a, int tile, int& slo
 template <int DT, int NT>
 __global__ __launch_bounds__(256, 2) void ranks_kernel(DeltaArgs a) {
   __shared__ __attribute__((aligned(16))) char lds[ranks_lds<DT, NT>()];
-  // Many tiles: an XCD takes neighbouring ones, which share x, dy and the weights in
-  // its L2, and all its tiles' first job before the second, so that a compute unit
-  // gets jobs of every length.
-  int tile, job, slot, rows, first;
-  if (a.num_tiles >= 64) {
-    const int x = blockIdx.x & 7, at = blockIdx.x >> 3;
-    const int q = a.num_tiles >> 3, r = a.num_tiles & 7, n = q + (x < r);
-    job = at / n;
-    tile = x * q + (x < r ? x : r) + at - job * n;
-    if (job >= a.jobs) return;
-  } else {
-    job = blockIdx.x / a.num_tiles;
-    tile = blockIdx.x - job * a.num_tiles;
-  }
+  // All tiles' first job before the second, so that a compute unit gets jobs of every
+  // length.  (Neighbouring tiles on one XCD, whose L2 they would share: the same at 8960
+  // rows, 188 us, and 19.8 against 14.4 at 256 rows of 43 adapters.)
+  int job = blockIdx.x / a.num_tiles, slot, rows, first;
+  const int tile = blockIdx.x - job * a.num_tiles;
   if (!take_tile(a, tile, slot, rows, first)) return;
   const int rank0 = job % a.blocks * 16 * NT;
   job /= a.blocks;
@@ -484,6 +485,7 @@ __global__ __launch_bounds__(256, 2) void ranks_kernel(DeltaArgs a) {
     s = job / n;
     job %= n;
   }
+  // (few rows: a quarter of the products; 256 rows of 43 adapters 14.4 us against 15.9)
   if (rows <= 16) {
     if (out)
       ranks_tile<DT, NT, true, 1>(a, lds, tile, slot, rows, first, s, rank0, job);
@@ -498,6 +500,9 @@ __global__ __launch_bounds__(256, 2) void ranks_kernel(DeltaArgs a) {
 }
 
 // ------------------------------------------------------- 2: parts of the sums
+//
+// 64 rows by 16 ranks a workgroup.  9.5 us for 2 parts of 8704 rows (u and v of 64
+// ranks: 18 MB in, 13 out): most of it a launch's latency.
 template <int DT>
 __global__ __launch_bounds__(256) void join_kernel(DeltaArgs a) {
   constexpr int LD = 16 + 4;
@@ -520,7 +525,8 @@ __global__ __launch_bounds__(256) void join_kernel(DeltaArgs a) {
 // 64 rows of one adapter (or none: a copy) by 256 bytes of columns: the ranks' rows of
 // A for these columns in LDS, 128 ranks at a time, a wave's 16 rows of u and of dx_in
 // straight to registers.  The columns are dealt to the output's index so that a
-// lane's are neighbours in memory.
+// lane's are neighbours in memory.  Alone 42 us for 8704 x 4096 of 64 ranks (143 MB in
+// and out: 3.4 TB/s).
 constexpr int kDxLds = 128 * 256;
 template <int DT>
 __device__ __forceinline__ void dx_tile(const DeltaArgs& a, char* lds, int block) {
@@ -629,7 +635,10 @@ __device__ __forceinline__ void dx_tile(const DeltaArgs& a, char* lds, int block
 // One workgroup: a piece of an adapter's rows, 512 bytes of columns of x or dy,
 // one rank block.  x or dy goes through a ring of stages of 32 rows in LDS, from which
 // both reads are of columns (a row of memory is a reduction index); a wave's 16
-// ranks of u or v come straight to registers, with the stages.
+// ranks of u or v come straight to registers, with the stages.  Half of the columns a
+// workgroup take twice as long (8704 x 4096 x 4096: 97 us alone against 50): u and v are
+// read once for each.  dx and gradients there together: 79 us, 5.1 TB/s; 2 x 14336 out
+// features 248 us, 4.5 TB/s.
 template <int DT, int NT, int NST, bool kOut>  // kOut: dB, from dy and v; else dA, from x and u
 __device__ __forceinline__ void grads_tile(const DeltaArgs& a, char* lds, int slot, int rows,
                                            int first, int tile, int partial, int s, int rank0,
@@ -774,8 +783,9 @@ __global__ __launch_bounds__(256, 4) void dx_kernel(DeltaArgs a) {
   dx_tile<DT>(a, lds, blockIdx.x);
 }
 
-// NST: stages of the ring.  Three, 48 KB, let three workgroups share a compute unit;
-// pieces of at most two steps take no third.
+// NST: stages of the ring.  Three, 48 KB, let three workgroups share a compute unit
+// (four and five stages: slower); pieces of at most two steps take no third (256 rows of
+// 64 adapters 50 us, with the third 56).
 template <int DT, int NT, int NST>
 __global__ __launch_bounds__(256, 2) void grads_kernel(DeltaArgs a) {
   constexpr int LDS = NST * 32 * kDeltaColumnBytes;
@@ -809,6 +819,7 @@ __global__ __launch_bounds__(256, 2) void grads_kernel(DeltaArgs a) {
 }
 
 // ----------------------------------------------------- 5: cut adapters' sums
+// 1024 values a workgroup.  5 us where two adapters of 8704 x 4096 x 4096 are cut (12 MB).
 __global__ __launch_bounds__(256) void sums_kernel(DeltaArgs a) {
   const int32_t* rec = a.multi + 4 * blockIdx.y;
   const int slot = rec[0], from = rec[1], n = rec[2];
@@ -832,7 +843,7 @@ int32_t run(DeltaArgs& a, hipStream_t st) {
     return n * a.blocks;
   };
   const int64_t jobs = count(a.chunk);
-  const int64_t blocks = (a.num_tiles >= 64 ? (a.num_tiles + 7) & ~7 : a.num_tiles) * jobs;
+  const int64_t blocks = a.num_tiles * jobs;
   const int64_t grads =
       a.dA && a.rows ? a.num_parts * count(kDeltaColumnBytes / es(DT)) : 0;
   const int64_t dx = a.dx ? (int64_t)(a.num_tiles + a.none_tiles) * a.dx_groups : 0;
@@ -840,7 +851,6 @@ int32_t run(DeltaArgs& a, hipStream_t st) {
   if (blocks > kMaxGroups || grads + dx > kMaxGroups || values / 1024 >= kMaxGroups)
     return fail(LORA_E_SHAPE, "too many workgroups");
   if (a.rows) {
-    a.jobs = (int32_t)jobs;
     hipLaunchKernelGGL((ranks_kernel<DT, NT>), dim3((uint32_t)blocks), dim3(256), 0, st, a);
     bool cut = a.K > a.chunk;
     for (int s = 0; s < a.S; ++s) cut |= a.out[s] > a.chunk;
