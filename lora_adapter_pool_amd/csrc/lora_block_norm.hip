@@ -24,10 +24,12 @@
 // a second launch, in an order that depends on the sizes alone.
 //
 // Measured (us, bf16): 8960 x 4096 with an element gate and 8-bit output 71, 5.6 TB/s;
-// its gradients with a channel gate 101 to 115 by the card (4.1 TB/s; vector units are
-// busy half of the cycles, and a row waits for two reductions), 5 of it the sums'
-// launch.  64 rows 4.2, a launch's time.
+// its gradients with a channel gate 108, 4.1 TB/s (a row waits for two reductions, and
+// vector units are busy half of the cycles), 5 of it the sums' launch.  64 rows 4.2, a
+// launch's time.
 #include <hip/hip_runtime.h>
+
+#include <algorithm>
 
 #include "lora_norm.h"
 
@@ -37,9 +39,16 @@ namespace {
 
 constexpr int kMaxHidden = 16384;
 constexpr int kForwardThreads = 1024, kBackwardThreads = 512;
-// workgroups that keep sums over rows, two a compute unit (8960 x 4096 before the next row
-// was fetched ahead: 132 us; with 256 workgroups 186, with 1024 133 to 138)
-constexpr int kSumGroups = 512;
+// Workgroups that keep sums over rows: as many as a compute unit holds at once, two of 256
+// or 512 threads, one of 512 with more than one piece a thread (8960 x 8192 bf16 225 us,
+// with two in turn 234), more where they are smaller (8960 x 1024 39 us, with two 60), but
+// four rows each (700 x 1024 12 us, with a row each 14: every one writes its sums).
+inline int sum_groups(int H, int T) {
+  int n = H > 4096 ? 256 : 512;
+  for (int h = 2048; h >= H && n < 4096; h /= 2) n *= 2;
+  if (n > 512) n = std::min(n, std::max(T / 4, 512));
+  return std::min(n, T);
+}
 
 struct JoinArgs {
   const void* y;
@@ -307,10 +316,10 @@ struct BackRow {
 template <int DT, int NP, bool kPre, bool kPost, bool kGate>
 __global__ __launch_bounds__(kBackwardThreads, DT == LORA_BF16 && NP == 1 ? 4 : 2)
 void join_backward_kernel(BackArgs a) {
-  // One piece a thread: the next row's is fetched while this one is worked on.  Four
-  // pieces leave no registers to hold a row over the reductions: it is read again, from
-  // the caches.
-  constexpr bool kAhead = NP == 1;
+  // One piece a thread, or two of bf16: the next row's are fetched while this one is worked
+  // on.  Four pieces leave no registers to hold a row over the reductions: it is read
+  // again, from the caches.
+  constexpr bool kAhead = NP == 1 || (NP == 2 && DT == LORA_BF16);
   constexpr uint32_t ES = DT == LORA_F32 ? 4 : 2;
   constexpr int kHeld = NP < 4 ? NP : 1;
   // by the row's parity: a row's reductions may meet the next row's writes
@@ -342,7 +351,10 @@ void join_backward_kernel(BackArgs a) {
     if (kPre) pre[j % kHeld].load_at(a.pre, c * ES);
     if (kPost) post[j % kHeld].load_at(a.post, c * ES);
   };
-  if (kAhead && tid * 8 < a.H) load_row(blockIdx.x, 0, tid * 8, next);
+  if (kAhead)
+#pragma unroll
+    for (int j = 0; j < NP; ++j)
+      if ((tid + j * nt) * 8 < a.H) load_row(blockIdx.x, j, (tid + j * nt) * 8, next);
   int parity = 0;
   for (int row = blockIdx.x; row < a.T; row += gridDim.x, parity ^= 1) {
     const int64_t base = (int64_t)row * a.H;
@@ -352,9 +364,13 @@ void join_backward_kernel(BackArgs a) {
       asm volatile("" : "+v"(mine));
       now = next;
       const int after = row + (int)gridDim.x;
-      if (mine < (uint32_t)a.H) {
-        load_rest(row, 0, mine, now);
-        if (after < a.T) load_row(after, 0, mine, next);
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const uint32_t c = mine + (uint32_t)(j * nt) * 8;
+        if (c < (uint32_t)a.H) {
+          load_rest(row, j, c, now);
+          if (after < a.T) load_row(after, j, c, next);
+        }
       }
     }
     double s[3] = {0.0, 0.0, 0.0};  // of t^2, dout w_pre t and y^2
@@ -501,25 +517,30 @@ void join_backward_kernel(BackArgs a) {
   }
 }
 
-// The partials' sums.  A workgroup takes 64 columns of one kind; its 16 waves
-// take every 16th partial.  25 MB of partials for 4096 columns of three kinds: 5.2 us.
+// The partials' sums.  A workgroup takes kCols columns of one kind, its threads every
+// (1024 / kCols)-th partial.  25 MB of partials for 4096 columns of three kinds: 5.2 us;
+// with few columns there are few workgroups, so that they take half as many (8960 x 1024
+// in all 38.6 us against 41.0; a quarter 41.7).
 struct SumArgs {
   const float* part;
   float* to[3];
   int32_t groups, H, accumulate;
 };
+template <int kCols>
 __global__ __launch_bounds__(1024) void column_sums(SumArgs a) {
-  __shared__ float room[16][64];
+  __shared__ float room[16][kCols];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + lane;
+  const int col = threadIdx.x % kCols, c = blockIdx.x * kCols + col;
   const float* from = a.part + (int64_t)blockIdx.y * a.groups * a.H + c;
   float s = 0.f;
   if (c < a.H)
 #pragma unroll 8
-    for (int r = wave; r < a.groups; r += 16) s += from[(int64_t)r * a.H];
-  room[wave][lane] = s;
+    for (int r = threadIdx.x / kCols; r < a.groups; r += 1024 / kCols) s += from[(int64_t)r * a.H];
+#pragma unroll
+  for (int d = kCols; d < 64; d *= 2) s += __shfl_xor(s, d);
+  if (lane < kCols) room[wave][lane] = s;
   __syncthreads();
-  if (wave || c >= a.H) return;
+  if ((int)threadIdx.x >= kCols || c >= a.H) return;
   s = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) s += room[i][lane];
@@ -547,7 +568,13 @@ void launch_pieces(const BackArgs& a, int groups, int nt, hipStream_t st) {
 }
 template <int DT>
 void launch_backward(const BackArgs& a, int groups, hipStream_t st) {
-  const int nt = threads_of(a.H, kBackwardThreads), np = (a.H / 8 + nt - 1) / nt;
+  // Two pieces a thread, where they are filled and there are rows enough: a wave's share of
+  // the reductions is half (8960 x 4096 bf16 125 -> 116 us, fp32 201 -> 186; 700 rows
+  // 22.6 -> 24.0, 2560 columns 83 -> 86).  By the sizes alone, so that a row's gradients do
+  // not depend on which sums are wanted.
+  int nt = threads_of(a.H, kBackwardThreads);
+  if (nt == kBackwardThreads && a.H / 8 <= nt && a.H >= 7 * nt && a.T >= 2048) nt /= 2;
+  const int np = (a.H / 8 + nt - 1) / nt;
   if (np == 1)
     launch_pieces<DT, 1>(a, groups, nt, st);
   else if (np == 2)
@@ -633,7 +660,7 @@ extern "C" int64_t lora_block_norm_backward_workspace_bytes(const lora_block_nor
   clear_error();
   if (int32_t e = check_join(desc)) return e;
   if (int32_t e = check_rows(T)) return e;
-  return (int64_t)3 * (T < kSumGroups ? T : kSumGroups) * desc->hidden * 4;
+  return (int64_t)3 * sum_groups(desc->hidden, T) * desc->hidden * 4;
 }
 
 extern "C" int32_t lora_block_norm_backward(
@@ -675,7 +702,7 @@ extern "C" int32_t lora_block_norm_backward(
   if (dpost_weight) s.to[kinds] = dpost_weight, a.k_post = kinds++;
   if (dgate && !element) s.to[kinds] = (float*)dgate, a.k_gate = kinds++;
   // without sums over the rows nothing is kept from row to row
-  const int groups = kinds ? (T < kSumGroups ? T : kSumGroups) : T;
+  const int groups = kinds ? sum_groups(desc->hidden, T) : T;
   if (kinds && T) {
     const int64_t need = lora_block_norm_backward_workspace_bytes(desc, T);
     if (!ws) return fail(LORA_E_ARG, "workspace is NULL");
@@ -714,6 +741,11 @@ extern "C" int32_t lora_block_norm_backward(
   s.groups = T ? groups : 0;
   s.H = desc->hidden;
   s.accumulate = accumulate;
-  hipLaunchKernelGGL(column_sums, dim3((desc->hidden + 63) / 64, kinds), dim3(1024), 0, st, s);
+  if (desc->hidden > 1024)
+    hipLaunchKernelGGL(column_sums<64>, dim3((desc->hidden + 63) / 64, kinds), dim3(1024), 0, st,
+                       s);
+  else
+    hipLaunchKernelGGL(column_sums<32>, dim3((desc->hidden + 31) / 32, kinds), dim3(1024), 0, st,
+                       s);
   return check_launch("sums over the rows");
 }

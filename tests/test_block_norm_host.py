@@ -84,7 +84,7 @@ def test_backward_refusals():
     need = L.lora_block_norm_backward_workspace_bytes(d, 4)
     assert need == 3 * 4 * 1024 * 4
     assert L.lora_block_norm_backward_workspace_bytes(d, 0) == 0
-    assert L.lora_block_norm_backward_workspace_bytes(d, 1 << 21) == 3 * 512 * 1024 * 4
+    assert L.lora_block_norm_backward_workspace_bytes(d, 1 << 21) == 3 * 2048 * 1024 * 4
     ok = [d] + [FAKE] * 12 + [0, 4, FAKE, need]
     variants(L.lora_block_norm_backward, ok, [(0, b, w) for b, w in BAD[:-1]] + [
         (0, mk("bf16", 1024, 1e-5), _lib.LORA_E_ARG), (1, None, _lib.LORA_E_ARG),

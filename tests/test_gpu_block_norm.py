@@ -244,3 +244,16 @@ def test_another_stream_and_replays():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs + sums, want)), k
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H", [(2048, 3600), (4100, 1024), (2500, 2048), (9000, 72), (530, 8192)])
+def test_backward_by_rows_and_width(dtype, T, H):
+    """Two pieces a thread, more workgroups for narrow rows, fewer for wide ones; a row's
+    gradients are the same whether the sums are wanted or not."""
+    s = inputs(T + H, T, H, dtype, "channel")
+    got = run_join_backward(s, dtype, "channel", start=0.5)
+    check_backward(s, got, dtype, 1.0, 1.0, 1e-5, True, True, True, f"T={T} H={H}", 0.5)
+    bare = run_join_backward(s, dtype, "channel", sums=False)
+    for k in ("dy", "dresidual"):
+        assert torch.equal(bare[k], got[k]), k
