@@ -19,8 +19,9 @@
 // fp32 operands is three with bf16 ones, which the loads hide (matrix units are busy
 // 18 to 24% of the cycles).
 //
-// Measured (us, bf16, 64 ranks): 8704 x 4096 x 4096 of 16 adapters 140 (floor of
-// its 335 MB at a copy's rate 65), 8960 x 4096 x 2 x 14336 of 28 adapters 453 (230);
+// Measured (us, bf16, 64 ranks): 8704 x 4096 x 4096 of 16 adapters 141 (floor of
+// its 335 MB at a copy's rate 65), 8960 x 4096 x 2 x 14336 of 28 adapters 453 to 469 by
+// the card (230);
 // 256 x 4096 x 6144 of 43 adapters of 16 ranks 46 (17); 32 rows fp32 9.5.
 #include <hip/hip_runtime.h>
 
@@ -259,7 +260,7 @@ __device__ __forceinline__ void finish_ranks(const DeltaArgs& a, const float* su
 // read as columns there).  8704 x 4096 x 4096: 53 us, 3.4 TB/s; 2 x 14336 out features:
 // 196 us, 3.9 TB/s.  Bound by what a compute unit pulls: the weights' block of each
 // 64 rows is as many bytes as the rows.  (Rings that the waves share, three and eight
-// steps deep, with their barriers: the same; larger tiles leave units idle.)
+// steps deep, with their barriers: the same.)
 template <int DT, int NT>
 constexpr int ranks_lds() {
   const int ring = 4 * 2 * 16 * NT * 128, sums = 4 * 64 * (16 * NT + 4) * 4;
@@ -466,8 +467,9 @@ template <int DT, int NT>
 __global__ __launch_bounds__(256, 2) void ranks_kernel(DeltaArgs a) {
   __shared__ __attribute__((aligned(16))) char lds[ranks_lds<DT, NT>()];
   // All tiles' first job before the second, so that a compute unit gets jobs of every
-  // length.  (Neighbouring tiles on one XCD, whose L2 they would share: the same at 8960
-  // rows, 188 us, and 19.8 against 14.4 at 256 rows of 43 adapters.)
+  // length.  (Neighbouring tiles on one XCD, whose L2 they would share: 55 us against
+  // 56 for 8704 x 4096 x 4096, 200 against 194 for gate/up of 8960 rows, 19.8 against 14.4
+  // for 256 rows of 43 adapters.)
   int job = blockIdx.x / a.num_tiles, slot, rows, first;
   const int tile = blockIdx.x - job * a.num_tiles;
   if (!take_tile(a, tile, slot, rows, first)) return;
@@ -502,7 +504,7 @@ __global__ __launch_bounds__(256, 2) void ranks_kernel(DeltaArgs a) {
 // ------------------------------------------------------- 2: parts of the sums
 //
 // 64 rows by 16 ranks a workgroup.  9.5 us for 2 parts of 8704 rows (u and v of 64
-// ranks: 18 MB in, 13 out): most of it a launch's latency.
+// ranks: 18 MB in, 9 out), half of it a launch and its latency.
 template <int DT>
 __global__ __launch_bounds__(256) void join_kernel(DeltaArgs a) {
   constexpr int LD = 16 + 4;
