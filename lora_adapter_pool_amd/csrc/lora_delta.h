@@ -29,7 +29,7 @@ inline int32_t delta_column_tile(const Geo& g) {
 }
 
 // A workspace's parts (byte offsets): the rows' rank-space values (u of every slice,
-// then v of every slice) ranks outside, u rows outside, partials of their reductions,
+// then v of every slice) ranks outside, u rows outside in fp32, partials of their reductions,
 // partials of the gradients.
 struct DeltaLayout {
   int64_t turned, straight, partial, grads, total;

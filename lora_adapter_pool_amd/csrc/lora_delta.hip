@@ -15,9 +15,10 @@
 // Every product is MFMA (16x16x32 bf16, 16x16x4 fp32).  The ranks are at most a
 // few hundred, so that every product is bound by memory: x and dy are read twice
 // (once for the ranks, once for the gradients), dx once in and out.  A bf16
-// pool's u and v are held as sums of three bf16 values (24 bits): one product with
-// fp32 operands is three with bf16 ones, which the loads hide (matrix units are busy
-// 18 to 24% of the cycles).
+// pool's u and v enter every product as sums of three bf16 values (24 bits): one
+// product with fp32 operands is three with bf16 ones, which the loads hide (matrix units
+// are busy 18 to 24% of the cycles; a third piece for dx, which had two, left 8704 x 4096
+// x 4096 at 142 us and took gate/up of 8960 rows from 459 to 461).
 //
 // Measured (us, bf16, 64 ranks): 8704 x 4096 x 4096 of 16 adapters 141 (floor of
 // its 335 MB at a copy's rate 65), 8960 x 4096 x 2 x 14336 of 28 adapters 453 to 469 by
@@ -59,7 +60,7 @@ struct DeltaArgs {
   const int32_t* parts;
   const int32_t* multi;
   char* turned;     // rank space, ranks outside
-  char* straight;   // u, rows outside
+  float* straight;  // u, rows outside
   float* partial;   // [splits][2 S][slots][padded]
   float* grads;     // [partials][values of a slot]
   int32_t num_tiles, none_tiles, num_parts, num_multi;
@@ -195,22 +196,40 @@ __device__ __forceinline__ void pieces_of(const float (&v)[4], bk_u32x2 (&p)[kPl
   }
 }
 
+// a fragment's values, as the matrix instruction takes them
+__device__ __forceinline__ void pieces_of(const Frag<LORA_F32>& v, Frag<LORA_BF16> (&f)[kPlanes]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float x[4] = {__uint_as_float(v.v[h][0]), __uint_as_float(v.v[h][1]),
+                        __uint_as_float(v.v[h][2]), __uint_as_float(v.v[h][3])};
+    bk_u32x2 p[kPlanes];
+    pieces_of(x, p);
+#pragma unroll
+    for (int k = 0; k < kPlanes; ++k) {
+      f[k].v[0][2 * h] = p[k][0];
+      f[k].v[0][2 * h + 1] = p[k][1];
+    }
+  }
+}
+__device__ __forceinline__ void pieces_of(const Frag<LORA_F32>& v, Frag<LORA_F32> (&f)[1]) {
+  f[0] = v;
+}
+
 typedef const __attribute__((address_space(4))) int32_t* scalar_words;
 
 // Where a value of rank space is kept: `turned` [planes][2 S][padded][slots], ranks
 // outside (a gradient's operand, whose reduction is over the rows), and for u also
-// `straight` [planes][S][slots][padded] (dx's operand).  slots: 64 for every tile;
-// those past a tile's rows are zero.
+// `straight` [S][slots][padded] in fp32 (dx's operand, read for every 256 bytes of
+// columns and cut into its pieces there: 8704 x 4096 x 4096 142 us in all, and 150 with
+// three planes of pieces in memory, which are half as many bytes again).  slots: 64 for
+// every tile; those past a tile's rows are zero.
 __device__ __forceinline__ int64_t turned_values(const DeltaArgs& a) {
   return (int64_t)2 * a.S * a.padded * a.slots;
-}
-__device__ __forceinline__ int64_t straight_values(const DeltaArgs& a) {
-  return (int64_t)a.S * a.padded * a.slots;
 }
 
 // Stores four values as they are kept, pieces `apart` values from each other.
 template <int DT>
-__device__ __forceinline__ void keep(char* base, int64_t at, int64_t apart, int planes,
+__device__ __forceinline__ void keep(char* base, int64_t at, int64_t apart,
                                      const float (&v)[4]) {
   if constexpr (DT == LORA_F32) {
     *reinterpret_cast<bk_f32x4*>(base + at * 4) = bk_f32x4{v[0], v[1], v[2], v[3]};
@@ -219,7 +238,7 @@ __device__ __forceinline__ void keep(char* base, int64_t at, int64_t apart, int 
     pieces_of(v, p);
 #pragma unroll
     for (int k = 0; k < kPlanes; ++k)
-      if (k < planes) *reinterpret_cast<bk_u32x2*>(base + (k * apart + at) * 2) = p[k];
+      *reinterpret_cast<bk_u32x2*>(base + (k * apart + at) * 2) = p[k];
   }
 }
 
@@ -237,16 +256,15 @@ __device__ __forceinline__ void finish_ranks(const DeltaArgs& a, const float* su
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = sums[(row + j) * LD + r];
     keep<DT>(a.turned, ((int64_t)q * a.padded + rank0 + r) * a.slots + tile * 64 + row,
-                turned_values(a), kPlanes, v);
+             turned_values(a), v);
   }
   if (q >= a.S || !a.dx) return;
 #pragma unroll
   for (int i = 0; i < RB / 16; ++i) {
     const int o = (i * 256 + tid) * 4;
-    const bk_f32x4 w = *reinterpret_cast<const bk_f32x4*>(sums + o / RB * LD + o % RB);
-    const float v[4] = {w[0], w[1], w[2], w[3]};
-    keep<DT>(a.straight, ((int64_t)q * a.slots + tile * 64 + o / RB) * a.padded + rank0 + o % RB,
-                straight_values(a), 2, v);
+    *reinterpret_cast<bk_f32x4*>(
+        a.straight + ((int64_t)q * a.slots + tile * 64 + o / RB) * a.padded + rank0 + o % RB) =
+        *reinterpret_cast<const bk_f32x4*>(sums + o / RB * LD + o % RB);
   }
 }
 
@@ -526,16 +544,16 @@ __global__ __launch_bounds__(256) void join_kernel(DeltaArgs a) {
 //
 // 64 rows of one adapter (or none: a copy) by 256 bytes of columns: the ranks' rows of
 // A for these columns in LDS, 128 ranks at a time, a wave's 16 rows of u and of dx_in
-// straight to registers.  The columns are dealt to the output's index so that a
-// lane's are neighbours in memory.  Alone 42 us for 8704 x 4096 of 64 ranks (143 MB in
+// straight to registers, u 64 ranks at a time.  The columns are dealt to the output's
+// index so that a lane's are neighbours in memory.  Alone 42 us for 8704 x 4096 of 64 ranks (143 MB in
 // and out: 3.4 TB/s).
 constexpr int kDxLds = 128 * 256;
 template <int DT>
 __device__ __forceinline__ void dx_tile(const DeltaArgs& a, char* lds, int block) {
   constexpr int ES = es(DT), RB = 256, CB = RB / ES, RANKS = kDxLds / RB;
-  constexpr int P = DT == LORA_BF16 ? 2 : 1, XV = sizeof(Frag<DT>) / 16;
   constexpr int CT = CB / 16, V = 16 / ES;  // column tiles; columns of a 16-byte piece
   constexpr int TV = V / 4, NV = CT / TV;   // tiles a piece spans; a lane's pieces
+  constexpr int P = DT == LORA_BF16 ? kPlanes : 1;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
@@ -554,6 +572,7 @@ __device__ __forceinline__ void dx_tile(const DeltaArgs& a, char* lds, int block
     return;
   }
   const int row = 16 * wave + l16;
+  const bool busy = 16 * wave < rows;  // (the wave has a row)
   int t = row < rows ? a.perm[first + row] : -1;
   // a lane's pieces of dx_in: columns c0 + i 4 V + g V ..
   bk_u32x4 base[NV];
@@ -580,33 +599,34 @@ __device__ __forceinline__ void dx_tile(const DeltaArgs& a, char* lds, int block
       to_lds(in ? a.A + ((((int64_t)slot * a.S + s) * a.R + r) * a.K + c) * ES : zeros(),
              lds + j * 1024);
     }
-    Frag<DT> u[P][RANKS / 32];
-#pragma unroll
-    for (int q = 0; q < RANKS / 32; ++q) {
+    Frag<LORA_F32> u[2];  // of 32 ranks, and of the next 32
+    auto load_u = [&](int q) {
       const int i = r0 + 32 * q + 8 * g, s = i / a.padded, r = i - s * a.padded;
-      const int64_t at = ((int64_t)s * a.slots + tile * 64 + row) * a.padded + r;
+      const bk_u32x4* from = reinterpret_cast<const bk_u32x4*>(
+          a.straight + ((int64_t)s * a.slots + tile * 64 + row) * a.padded + r);
 #pragma unroll
-      for (int p = 0; p < P; ++p)
-#pragma unroll
-        for (int h = 0; h < XV; ++h)
-          u[p][q].v[h] =
-              i < r0 + n ? reinterpret_cast<const bk_u32x4*>(
-                               a.straight + (p * straight_values(a) + at) * ES)[h]
-                         : bk_u32x4{0, 0, 0, 0};
+      for (int h = 0; h < 2; ++h) u[q & 1].v[h] = i < r0 + n ? from[h] : bk_u32x4{0, 0, 0, 0};
+    };
+    if (busy) {
+      load_u(0);
+      load_u(1);
     }
     if (r0 == 0) fetch();
     wait_loads<0>();
     barrier();
 #pragma unroll
     for (int q = 0; q < RANKS / 32; ++q) {
-      if (32 * q >= n) break;
+      if (32 * q >= n || !busy) break;
+      Frag<DT> f[P];
+      pieces_of(u[q & 1], f);
 #pragma unroll
       for (int i = 0; i < CT; ++i) {
         const Frag<DT> w =
             read_cols<DT, RB>(lds, 32 * q, i / TV * 4 * V + i % TV * 4, V, l16, g);
 #pragma unroll
-        for (int p = P - 1; p >= 0; --p) acc[i] = product<DT>(w, u[p][q], acc[i]);
+        for (int p = P - 1; p >= 0; --p) acc[i] = product<DT>(w, f[p], acc[i]);
       }
+      if (q + 2 < RANKS / 32 && 32 * (q + 2) < n) load_u(q + 2);
     }
     wait_loads<0>();
     barrier();
@@ -947,7 +967,7 @@ extern "C" int32_t lora_delta_backward(const lora_pool_desc* desc, const void* A
   a.parts = im + plan->off_parts;
   a.multi = im + plan->off_multi;
   a.turned = (char*)ws + l.turned;
-  a.straight = (char*)ws + l.straight;
+  a.straight = (float*)((char*)ws + l.straight);
   a.partial = (float*)((char*)ws + l.partial);
   a.grads = (float*)((char*)ws + l.grads);
   a.num_tiles = plan->tiles;

@@ -80,11 +80,11 @@ DeltaLayout delta_layout(const Geo& g, int32_t T) {
   const int64_t tiles = T < T / tile + runs ? T : T / tile + runs;
   // Reductions are cut only while the unsplit workgroups are fewer than wanted.
   const int64_t few = kDeltaShrinks / (sides * r.blocks) + 1;
-  const int64_t planes = g.dtype == LORA_BF16 ? 3 : 1, two = g.dtype == LORA_BF16 ? 2 : 1;
+  const int64_t planes = g.dtype == LORA_BF16 ? 3 : 1;
   DeltaLayout l;
   l.turned = 0;
   l.straight = l.turned + align_up(planes * sides * tiles * tile * r.padded * e, 256);
-  l.partial = l.straight + align_up(two * g.S * tiles * tile * r.padded * e, 256);
+  l.partial = l.straight + align_up(g.S * tiles * tile * r.padded * 4, 256);
   l.grads = l.partial + align_up((int64_t)kDeltaMaxSplits * sides * (tiles < few ? tiles : few) *
                                      tile * r.padded * 4,
                                  256);
