@@ -374,22 +374,27 @@ void join_backward_kernel(BackArgs a) {
       }
     }
     double s[3] = {0.0, 0.0, 0.0};  // of t^2, dout w_pre t and y^2
+    // (One piece a thread, four waves a SIMD: elements are unpacked again behind the
+    // reduction, and y's behind t's; kept over them they are more than the registers.)
     auto stat = [&](int j) {
       const int k = j % kHeld;
-      float x[8], v[8];
+      float x[8];
       if (kPre) {
+        // (products of dout and the stream may be past fp32's range where no square is)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           x[i] = now.t[k].at(i);
-          v[i] = now.dout[k].at(i) * pre[k].at(i);
+          s[1] = __builtin_fma((double)(now.dout[k].at(i) * pre[k].at(i)), (double)x[i], s[1]);
         }
         s[0] += (double)dot8(x, x);
-        s[1] += (double)dot8(v, x);
+        if (NP == 1) now.t[k].opaque(), now.dout[k].opaque(), pre[k].opaque();
       }
       if (kPost) {
+        if (NP == 1 && kPre) now.y[k].opaque();
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = now.y[k].at(i);
         s[2] += (double)dot8(x, x);
+        if (NP == 1) now.y[k].opaque();
       }
     };
 #pragma unroll

@@ -38,6 +38,11 @@ struct Raw {
     v[0] = p[0];
     if constexpr (DT == LORA_F32) v[1] = p[1];
   }
+  // What was unpacked or computed from the piece before is not kept for what follows.
+  __device__ __forceinline__ void opaque() {
+#pragma unroll
+    for (bk_u32x4& p : v) asm volatile("" : "+v"(p));
+  }
   __device__ __forceinline__ float at(int i) const {
     if constexpr (DT == LORA_F32) return __uint_as_float(v[i >> 2][i & 3]);
     const uint32_t w = v[0][i >> 1];
