@@ -19,12 +19,15 @@
 //   dw_pre = sum_rows dout t_hat,  dw_post = sum_rows dp y_hat, and dgate's sum
 //   over the rows where the gate is one a channel
 // The statistics are made again from y and the stream, which have to be read
-// anyhow, so that the forward pass keeps nothing else.  A workgroup takes every
+// anyhow, so that the forward pass keeps nothing else, and in 64 bits as there: a
+// row's factors are the same numbers in both passes, and rows of any size take the same
+// path (squares summed in fp32 where they fit, and such rows of zeros again: 108 us for
+// the case below, not 112, and 163 where half of the rows are zeros, not 112).  A workgroup takes every
 // n-th row and keeps the columns' sums in registers; their partials are added in
 // a second launch, in an order that depends on the sizes alone.
 //
 // Measured (us, bf16): 8960 x 4096 with an element gate and 8-bit output 71, 5.6 TB/s;
-// its gradients with a channel gate 108, 4.1 TB/s (a row waits for two reductions, and
+// its gradients with a channel gate 112, 3.9 TB/s (a row waits for two reductions, and
 // vector units are busy half of the cycles), 5 of it the sums' launch.  64 rows 4.2, a
 // launch's time.
 #include <hip/hip_runtime.h>
@@ -274,15 +277,14 @@ struct BackArgs {
 };
 
 // Sum of eight products in fp32, in three levels: off by at most four half steps of the
-// sum of their magnitudes.
+// sum of their magnitudes.  For the products with the normalised y, which are of dp's
+// size; sums of squares, and of products with the stream itself, are of any size.
 __device__ __forceinline__ float dot8(const float (&a)[8], const float (&b)[8]) {
   float p[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) p[i] = __builtin_fmaf(a[2 * i], b[2 * i], a[2 * i + 1] * b[2 * i + 1]);
   return (p[0] + p[1]) + (p[2] + p[3]);
 }
-// Whether fp32 holds a sum of squares with all its bits, terms of 2^-24 of it too.
-__device__ __forceinline__ bool in_range(double s) { return s > 0x1p-80 && s < 0x1p120; }
 
 // Eight elements to a uniform address and an offset in bytes.
 template <int DT>
@@ -297,11 +299,6 @@ __device__ __forceinline__ void put8(void* base, uint32_t at, const float (&v)[8
       p[h] = bk_u32x4{__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]),
                       __float_as_uint(v[4 * h + 2]), __float_as_uint(v[4 * h + 3])};
   }
-}
-template <int DT>
-__device__ __forceinline__ float element(const void* p, int64_t i) {
-  if constexpr (DT == LORA_F32) return ((const float*)p)[i];
-  return __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16);
 }
 
 // A thread's pieces of a row, as they are stored.
@@ -378,22 +375,19 @@ void join_backward_kernel(BackArgs a) {
     // reduction, and y's behind t's; kept over them they are more than the registers.)
     auto stat = [&](int j) {
       const int k = j % kHeld;
-      float x[8];
       if (kPre) {
-        // (products of dout and the stream may be past fp32's range where no square is)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          x[i] = now.t[k].at(i);
-          s[1] = __builtin_fma((double)(now.dout[k].at(i) * pre[k].at(i)), (double)x[i], s[1]);
+          const double x = now.t[k].at(i);
+          s[0] = __builtin_fma(x, x, s[0]);
+          s[1] = __builtin_fma((double)(now.dout[k].at(i) * pre[k].at(i)), x, s[1]);
         }
-        s[0] += (double)dot8(x, x);
         if (NP == 1) now.t[k].opaque(), now.dout[k].opaque(), pre[k].opaque();
       }
       if (kPost) {
         if (NP == 1 && kPre) now.y[k].opaque();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = now.y[k].at(i);
-        s[2] += (double)dot8(x, x);
+        for (int i = 0; i < 8; ++i) s[2] = square_plus(now.y[k].at(i), s[2]);
         if (NP == 1) now.y[k].opaque();
       }
     };
@@ -411,22 +405,6 @@ void join_backward_kernel(BackArgs a) {
       for (int j = 0; j < NP; ++j)
         if (mine + (uint32_t)(j * nt) * 8 < (uint32_t)a.H) stat(j);
     if (kPre || kPost) sum_over(s, first[parity]);
-    if ((kPre && !in_range(s[0])) || (kPost && !in_range(s[2]))) {
-      // Squares past fp32's range: the row again, in 64 bits, an element at a time.
-      __syncthreads();
-      s[0] = s[1] = s[2] = 0.0;
-#pragma unroll 1
-      for (int i = tid; i < a.H; i += nt) {
-        if (kPre) {
-          const double x = element<DT>(a.sum, base + i);
-          s[0] = __builtin_fma(x, x, s[0]);
-          s[1] = __builtin_fma(
-              (double)(element<DT>(a.dout, base + i) * element<DT>(a.pre, i)), x, s[1]);
-        }
-        if (kPost) s[2] = square_plus(element<DT>(a.y, base + i), s[2]);
-      }
-      sum_over(s, first[parity]);
-    }
     const double rt = reciprocal_root(__builtin_fma(s[0], a.over_h, a.eps));
     const double ry = reciprocal_root(__builtin_fma(s[2], a.over_h, a.eps));
     const Factor ft = factor_of(rt), fy = factor_of(ry);
