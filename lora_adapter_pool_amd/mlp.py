@@ -211,7 +211,8 @@ class LoraMlp:
         "gate_up" and "down" ((dA, dB) of the pools, as LoraPool.backward gives them) and
         "w_gate_up" (need_dw).  w_down_t: w_down transposed, [I][H]; the base is frozen in this
         pass, so that a program makes it once.  grads: buffers for the fp32 sums by these names,
-        which accumulate adds to; new ones are made for the others.  plans: the pools'
+        which accumulate adds to (16-byte aligned, apart from each other); new ones are made for
+        the others.  plans: the pools'
         backward_plan of the kept ids by "gate_up" and "down", where a program makes them once for
         a step's layers or captures the pass; made here otherwise, which waits for the GPU.
         Weights must not be in e4m3.  Takes the kept pass with it."""
@@ -244,6 +245,10 @@ class LoraMlp:
                                                 "the block does not have")
         for k in set(grads) & set(pools):
             pools[k].check_grads(*grads[k])
+        self._check_buffers(
+            [(k, t) for k, v in grads.items() for t in (v if k in pools else (v,)) if t is not None],
+            [("dy", dy), ("w_down_t", w_down_t)] +
+            [(f"{k}'s pool", t) for k, p in pools.items() for t in (p.A, p.B)])
         ids = self._saved_rest[3]
         for k, pool in pools.items():
             if ids is None:
@@ -255,6 +260,20 @@ class LoraMlp:
                 plans[k] = pool.backward_plan(ids)
             pool.check_plan(plans[k], dy.shape[0])
         return self._on_device(self._backward, dy, w_down_t, need_dw, grads, accumulate, plans)
+
+    def _check_buffers(self, written, read) -> None:
+        """Refuses what an operator of the pass would refuse after others have added to their
+        sums: tensors off 16 bytes, and gradients that overlap each other or what is read."""
+        for name, t in written + read:
+            if t.data_ptr() % 16:
+                raise L.LoraError(L.LORA_E_ALIGN, f"{name} must be 16-byte aligned")
+        span = lambda t: (t.data_ptr(), t.data_ptr() + t.nbytes)  # noqa: E731
+        for i, (name, t) in enumerate(written):
+            a, b = span(t)
+            for other, u in written[i + 1:] + read:
+                c, d = span(u)
+                if max(a, c) < min(b, d):
+                    raise L.LoraError(L.LORA_E_ARG, f"the gradient of {name} overlaps {other}")
 
     def _backward(self, dy, w_down_t, need_dw, grads, accumulate, plans):
         torch = self.torch
