@@ -125,10 +125,14 @@ class LoraMlp:
         if t.dim() != 2 or t.shape[1] != width or not t.is_contiguous():
             raise L.LoraError(L.LORA_E_SHAPE, f"{name} must be a contiguous [T, {width}]")
 
-    def forward(self, x, residual, ids=None, prefill=None, keep: bool = False):
+    def forward(self, x, residual, ids=None, prefill=None, keep=False):
         """y [T][H] on the current stream of the weights' GPU.  ids, prefill: as
-        LoraPool.apply takes them (None: no adapters).  keep: hold what
-        gate_up_backward and backward need."""
+        LoraPool.apply takes them (None: no adapters).  keep: True holds what
+        gate_up_backward and backward need, "gate_up" what gate_up_backward alone needs
+        (T H values fewer, and T I fewer where down has adapters, T H fewer behind a norm
+        after the block or a gate)."""
+        if isinstance(keep, str) and keep != "gate_up":
+            raise L.LoraError(L.LORA_E_ARG, f'keep must be True, False or "gate_up", got {keep!r}')
         self._check_rows(x, self.H, "x")
         self._check_rows(residual, self.H, "residual")
         if residual.shape != x.shape:
@@ -166,8 +170,12 @@ class LoraMlp:
                               None, None, None, T)
         self._saved = (n, pre) if keep else None
         self._saved_rest = None
-        if keep:
+        if keep and keep != "gate_up" and not self.eight:
             kept = None if ids is None else np.array(ids, dtype=np.int32)
+            if self.down is None or ids is None:
+                h = None       # (its adapters alone take it)
+            if self.post_norm_weight is None and self.gate is None:
+                block = None   # (scales alone need no value of it)
             self._saved_rest = (s, h, block, kept)
         return y
 
@@ -220,6 +228,8 @@ class LoraMlp:
             raise L.LoraError(L.LORA_E_ARG, "no forward pass was kept (keep=True)")
         if self.eight:
             raise L.LoraError(L.LORA_E_DTYPE, "the gradients take weights in fp32 or bf16")
+        if self._saved_rest is None:
+            raise L.LoraError(L.LORA_E_ARG, "the pass was kept for gate_up_backward alone")
         self._check_rows(dy, self.H, "dy")
         if dy.shape[0] != self._saved[0].shape[0]:
             raise L.LoraError(L.LORA_E_SHAPE, "dy must have the kept pass's rows")
@@ -305,7 +315,7 @@ class LoraMlp:
                 self.join_desc, None, dy, block, None, self.gate, self.post_norm_weight, None, db,
                 ds, out.get("gate"), out.get("post_norm_weight"), None, accumulate, T, ws,
                 ws.numel())
-        dh = torch.empty_like(h)
+        dh = torch.empty((T, self.I), dtype=dy.dtype, device=dy.device)
         L.lora_linear(self.dh_desc, db, w_down_t, None, None, None, None, None, dh, T, ws,
                       ws.numel())
         adapters("down", self.down, h, db, dh)
