@@ -249,15 +249,16 @@ __device__ __forceinline__ void finish_ranks(const DeltaArgs& a, const float* su
                                              int rank0) {
   constexpr int LD = RB + 4;
   const int tid = threadIdx.x, row = tid % 16 * 4;
+  if (a.dA)
 #pragma unroll
-  for (int i = 0; i < RB / 16; ++i) {
-    const int r = 16 * i + tid / 16;
-    float v[4];
+    for (int i = 0; i < RB / 16; ++i) {
+      const int r = 16 * i + tid / 16;
+      float v[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = sums[(row + j) * LD + r];
-    keep<DT>(a.turned, ((int64_t)q * a.padded + rank0 + r) * a.slots + tile * 64 + row,
-             turned_values(a), v);
-  }
+      for (int j = 0; j < 4; ++j) v[j] = sums[(row + j) * LD + r];
+      keep<DT>(a.turned, ((int64_t)q * a.padded + rank0 + r) * a.slots + tile * 64 + row,
+               turned_values(a), v);
+    }
   if (q >= a.S || !a.dx) return;
 #pragma unroll
   for (int i = 0; i < RB / 16; ++i) {
@@ -859,8 +860,11 @@ __global__ __launch_bounds__(256) void sums_kernel(DeltaArgs a) {
 
 template <int DT, int NT>
 int32_t run(DeltaArgs& a, hipStream_t st) {
+  // Jobs of the out slices, and behind them those of x, whose v (as u ranks outside) is for
+  // dA and dB: a call for dx alone leaves them out (8704 x 4096 x 4096 105 -> 81 us, gate/up
+  // of 8960 rows 260 -> 224, 256 rows of 43 adapters 27 -> 23).
   auto count = [&](int32_t width) {
-    int64_t n = (int64_t)a.S * ((a.K + width - 1) / width);
+    int64_t n = a.dA ? (int64_t)a.S * ((a.K + width - 1) / width) : 0;
     for (int s = 0; s < a.S; ++s) n += (a.out[s] + width - 1) / width;
     return n * a.blocks;
   };
@@ -874,11 +878,11 @@ int32_t run(DeltaArgs& a, hipStream_t st) {
     return fail(LORA_E_SHAPE, "too many workgroups");
   if (a.rows) {
     hipLaunchKernelGGL((ranks_kernel<DT, NT>), dim3((uint32_t)blocks), dim3(256), 0, st, a);
-    bool cut = a.K > a.chunk;
+    bool cut = a.dA && a.K > a.chunk;
     for (int s = 0; s < a.S; ++s) cut |= a.out[s] > a.chunk;
     if (cut)
-      hipLaunchKernelGGL(join_kernel<DT>, dim3(a.num_tiles, 2 * a.S, a.padded / 16), dim3(256), 0,
-                         st, a);
+      hipLaunchKernelGGL(join_kernel<DT>, dim3(a.num_tiles, a.dA ? 2 * a.S : a.S, a.padded / 16),
+                         dim3(256), 0, st, a);
   }
   const bool one = grads && dx;
   a.dx_blocks = one ? (int32_t)dx : 0;
