@@ -512,7 +512,8 @@ int32_t lora_apply_ranked(const lora_pool_desc* desc, const void* A_pool, const 
  *   x, dx_in, dx [T][K], dy [T][O] of the pool's dtype; dA [max_loras][S][R][K] and
  *   dB [max_loras][O][R] fp32
  * Products keep fp32: u and v enter the matrix instructions of a bf16 pool in
- * three pieces of 8 bits each (24 bits).  dA and dB of the batch's adapters are overwritten, or
+ * three pieces of 8 bits each (24 bits), of either sign, so that an infinite dy or x
+ * may come out as NaN in dB or dA (and an infinite A in dx).  dA and dB of the batch's adapters are overwritten, or
  * added to where accumulate is 1; other slots' are never touched.  dx may be
  * dx_in itself (rows without an adapter are then left alone); without dx_in
  * (NULL) dx is the delta's part alone, zero in rows without an adapter.  dx may be

@@ -262,10 +262,12 @@ __device__ __forceinline__ void finish_ranks(const DeltaArgs& a, const float* su
   if (q >= a.S || !a.dx) return;
 #pragma unroll
   for (int i = 0; i < RB / 16; ++i) {
-    const int o = (i * 256 + tid) * 4;
-    *reinterpret_cast<bk_f32x4*>(
-        a.straight + ((int64_t)q * a.slots + tile * 64 + o / RB) * a.padded + rank0 + o % RB) =
-        *reinterpret_cast<const bk_f32x4*>(sums + o / RB * LD + o % RB);
+    const int o = (i * 256 + tid) * 4, r = rank0 + o % RB;
+    // (an infinite dy times the zeros past the last rank is NaN, and so would dx be)
+    *reinterpret_cast<bk_f32x4*>(a.straight +
+                                 ((int64_t)q * a.slots + tile * 64 + o / RB) * a.padded + r) =
+        r < a.R ? *reinterpret_cast<const bk_f32x4*>(sums + o / RB * LD + o % RB)
+                : bk_f32x4{0.f, 0.f, 0.f, 0.f};
   }
 }
 

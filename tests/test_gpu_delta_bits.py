@@ -1,7 +1,7 @@
 """The input's gradient of a bf16 pool keeps fp32 products: whole numbers in rank space that
 need all three bf16 pieces (17 to 20 bits), whose large parts cancel in the sum over the
 ranks.  Every product and partial sum is a whole number below 2^24, so that the sum is exact
-in fp32 and what is left, at most 128, is exact in bf16."""
+in fp32 and what is left, at most 128, is exact in bf16.  And an infinite dy."""
 import numpy as np
 import pytest
 import torch
@@ -50,3 +50,30 @@ def test_ranks_that_cancel(dtype, T, K, slots, kind):
     assert want.abs().max() <= 128
     for dx_in in (False, True):
         assert torch.equal(run_delta(s, dx_in=dx_in)["dx"].double(), want), dx_in
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R", [8, 24, 40, 64, 72])
+def test_an_infinity_stays_one(dtype, R):
+    """A row whose dy has one infinity, through positive A and B: its dx is infinite (and not
+    NaN, whatever the ranks are padded to), its dA infinite or NaN by x's sign alone."""
+    T, K, O = 5, 136, 72
+    g = torch.Generator(device="cuda").manual_seed(R)
+    pos = lambda *s: (torch.rand(s, generator=g, device="cuda") + 0.5).to(TORCH[dtype])  # noqa: E731
+    s = {"ids": np.array([0, 1, -1, 1, 0], np.int32), "x": pos(T, K), "dy": pos(T, O),
+         "A": pos(2, 1, R, K), "B": pos(2, O, R), "dx_in": pos(T, K), "outs": [O], "dtype": dtype}
+    clean = run_delta(s)
+    for sign in (1, -1):
+        t = dict(s, dy=s["dy"].clone())
+        t["dy"][3, 7] = sign * float("inf")
+        got = run_delta(t)
+        assert (got["dx"][3] == sign * float("inf")).all(), sign
+        rows = [0, 1, 2, 4]
+        assert torch.equal(got["dx"][rows], clean["dx"][rows])
+        assert (got["dA"][1] == sign * float("inf")).all()
+        assert torch.equal(got["dA"][0], clean["dA"][0])
+        # v of a bf16 pool is a sum of pieces p + q + r, and q is of either sign: an infinite dy
+        # times p and times q are infinities whose sum is NaN where the signs differ
+        assert (got["dB"][1, 7] == sign * float("inf")).all() if dtype == "f32" else \
+            not got["dB"][1, 7].isfinite().any()
+        assert torch.equal(got["dB"][1, 8:], clean["dB"][1, 8:])
