@@ -551,12 +551,14 @@ void launch_pieces(const BackArgs& a, int groups, int nt, hipStream_t st) {
 }
 template <int DT>
 void launch_backward(const BackArgs& a, int groups, hipStream_t st) {
-  // Two pieces a thread, where they are filled and there are rows enough: a wave's share of
-  // the reductions is half (8960 x 4096 bf16 125 -> 116 us, fp32 201 -> 186; 700 rows
-  // 22.6 -> 24.0, 2560 columns 83 -> 86).  By the sizes alone, so that a row's gradients do
-  // not depend on which sums are wanted.
+  // Two pieces a thread for rows of more than 2048 columns, where a workgroup has more than
+  // a row to go through: a wave's share of the reductions is half (8960 x 4096 bf16 119 ->
+  // 112 us, fp32 205 -> 188; 2560 columns 88 -> 86 and 156 -> 127; 700 x 4096 19.9 -> 19.7
+  // and 28.2 -> 25.6), and with fewer rows, where more threads wait for a row's loads at
+  // once, one (256 x 4096 12.7 against 13.1, fp32 14.3 against 15.1).  By the sizes alone, so
+  // that a row's gradients do not depend on which sums are wanted.
   int nt = threads_of(a.H, kBackwardThreads);
-  if (nt == kBackwardThreads && a.H / 8 <= nt && a.H >= 7 * nt && a.T >= 2048) nt /= 2;
+  if (nt == kBackwardThreads && a.H / 8 <= nt && a.T > 512) nt /= 2;
   const int np = (a.H / 8 + nt - 1) / nt;
   if (np == 1)
     launch_pieces<DT, 1>(a, groups, nt, st);

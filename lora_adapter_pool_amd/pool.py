@@ -99,8 +99,9 @@ class LoraPool:
         stream of the pool's GPU.
         dx [T, K] = dx_in (the base projection's part; None: zeros) + the delta's; it may be
         dx_in itself.  dA, dB: fp32 gradients of A_view() and B_view(), overwritten or added to
-        (accumulate) for the batch's slots, others left; new ones are zeros.  peft's lora_B has
-        the adapter's scale times dB's gradient.  A pool's calls share a workspace: two that run
+        (accumulate) for the batch's slots, others left; new ones are zeros, of the whole pool's
+        size, so that a program makes its own once.  peft's lora_B has the adapter's scale times
+        dB's gradient.  A pool's calls share a workspace: two that run
         at once, or graphs of them, need pools of their own."""
         torch = self.torch
         if not self.A.is_cuda:
