@@ -26,10 +26,10 @@
 // n-th row and keeps the columns' sums in registers; their partials are added in
 // a second launch, in an order that depends on the sizes alone.
 //
-// Measured (us, bf16): 8960 x 4096 with an element gate and 8-bit output 71, 5.6 TB/s;
+// Measured (us, bf16): 8960 x 4096 with an element gate and 8-bit output 72, 5.6 TB/s;
 // its gradients with a channel gate 112, 3.9 TB/s (a row waits for two reductions, and
-// vector units are busy half of the cycles), 5 of it the sums' launch.  64 rows 4.2, a
-// launch's time.
+// vector units issue in 47% of the cycles), 5 of it the sums' launch.  64 rows 4.2 to
+// 4.7, a launch's time.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -43,7 +43,7 @@ namespace {
 constexpr int kMaxHidden = 16384;
 constexpr int kForwardThreads = 1024, kBackwardThreads = 512;
 // Workgroups that keep sums over rows: as many as a compute unit holds at once, two of 256
-// or 512 threads, one of 512 with more than one piece a thread (8960 x 8192 bf16 225 us,
+// or 512 threads, one of 512 with more than one piece a thread (8960 x 8192 bf16 222 us,
 // with two in turn 234), more where they are smaller (8960 x 1024 39 us, with two 60), but
 // four rows each (700 x 1024 12 us, with a row each 14: every one writes its sums).
 inline int sum_groups(int H, int T) {

@@ -17,13 +17,12 @@
 // (once for the ranks, once for the gradients), dx once in and out.  A bf16
 // pool's u and v enter every product as sums of three bf16 values (24 bits): one
 // product with fp32 operands is three with bf16 ones, which the loads hide (matrix units
-// are busy 18 to 24% of the cycles; a third piece for dx, which had two, left 8704 x 4096
+// are busy 20 to 26% of the gradients' cycles; a third piece for dx, which had two, left 8704 x 4096
 // x 4096 at 142 us and took gate/up of 8960 rows from 459 to 461).
 //
-// Measured (us, bf16, 64 ranks): 8704 x 4096 x 4096 of 16 adapters 141 (floor of
-// its 335 MB at a copy's rate 65), 8960 x 4096 x 2 x 14336 of 28 adapters 453 to 469 by
-// the card (230);
-// 256 x 4096 x 6144 of 43 adapters of 16 ranks 46 (17); 32 rows fp32 9.5.
+// Measured (us, bf16, 64 ranks): 8704 x 4096 x 4096 of 16 adapters 142 (floor of
+// its 335 MB at a copy's rate 65), 8960 x 4096 x 2 x 14336 of 28 adapters 442 to 465 by
+// the card (230); 256 x 4096 x 6144 of 43 adapters of 16 ranks 47 (17); 32 rows fp32 8.8.
 #include <hip/hip_runtime.h>
 
 #include "lora_delta.h"
@@ -279,7 +278,7 @@ __device__ __forceinline__ void finish_ranks(const DeltaArgs& a, const float* su
 // the end.  So nothing waits for another wave on the way: x or dy comes straight to
 // registers, two steps ahead, and A or B through the wave's own part of LDS (B is
 // read as columns there).  8704 x 4096 x 4096: 53 us, 3.4 TB/s; 2 x 14336 out features:
-// 196 us, 3.9 TB/s.  Bound by what a compute unit pulls: the weights' block of each
+// 193 us, 3.9 TB/s.  Bound by what a compute unit pulls: the weights' block of each
 // 64 rows is as many bytes as the rows.  (Rings that the waves share, three and eight
 // steps deep, with their barriers: the same.)
 template <int DT, int NT>
@@ -524,7 +523,7 @@ __global__ __launch_bounds__(256, 2) void ranks_kernel(DeltaArgs a) {
 
 // ------------------------------------------------------- 2: parts of the sums
 //
-// 64 rows by 16 ranks a workgroup.  9.5 us for 2 parts of 8704 rows (u and v of 64
+// 64 rows by 16 ranks a workgroup.  8 to 9.5 us for 2 parts of 8704 rows (u and v of 64
 // ranks: 18 MB in, 9 out), half of it a launch and its latency.
 template <int DT>
 __global__ __launch_bounds__(256) void join_kernel(DeltaArgs a) {
@@ -548,8 +547,8 @@ __global__ __launch_bounds__(256) void join_kernel(DeltaArgs a) {
 // 64 rows of one adapter (or none: a copy) by 256 bytes of columns: the ranks' rows of
 // A for these columns in LDS, 128 ranks at a time, a wave's 16 rows of u and of dx_in
 // straight to registers, u 64 ranks at a time.  The columns are dealt to the output's
-// index so that a lane's are neighbours in memory.  Alone 42 us for 8704 x 4096 of 64 ranks (143 MB in
-// and out: 3.4 TB/s).
+// index so that a lane's are neighbours in memory.  Alone 44 us for 8704 x 4096 of 64 ranks (143 MB in
+// and out: 3.2 TB/s).
 constexpr int kDxLds = 128 * 256;
 template <int DT>
 __device__ __forceinline__ void dx_tile(const DeltaArgs& a, char* lds, int block) {
@@ -663,7 +662,7 @@ __device__ __forceinline__ void dx_tile(const DeltaArgs& a, char* lds, int block
 // ranks of u or v come straight to registers, with the stages.  Half of the columns a
 // workgroup take twice as long (8704 x 4096 x 4096: 97 us alone against 50): u and v are
 // read once for each.  dx and gradients there together: 79 us, 5.1 TB/s; 2 x 14336 out
-// features 248 us, 4.5 TB/s.
+// features 250 to 262 us, 4.3 to 4.5 TB/s.
 template <int DT, int NT, int NST, bool kOut>  // kOut: dB, from dy and v; else dA, from x and u
 __device__ __forceinline__ void grads_tile(const DeltaArgs& a, char* lds, int slot, int rows,
                                            int first, int tile, int partial, int s, int rank0,
