@@ -20,8 +20,8 @@
 // are busy 20 to 26% of the gradients' cycles; a third piece for dx, which had two, left 8704 x 4096
 // x 4096 at 142 us and took gate/up of 8960 rows from 459 to 461).
 //
-// Measured (us, bf16, 64 ranks): 8704 x 4096 x 4096 of 16 adapters 142 (floor of
-// its 335 MB at a copy's rate 65), 8960 x 4096 x 2 x 14336 of 28 adapters 442 to 465 by
+// Measured (us, bf16, 64 ranks): 8704 x 4096 x 4096 of 16 adapters 142 to 146 (floor of
+// its 335 MB at a copy's rate 65), 8960 x 4096 x 2 x 14336 of 28 adapters 442 to 478 by
 // the card (230); 256 x 4096 x 6144 of 43 adapters of 16 ranks 47 (17); 32 rows fp32 8.8.
 #include <hip/hip_runtime.h>
 
